@@ -342,6 +342,170 @@ int moe_permute_noalloc(const int32_t* topk_ids, int32_t num_tokens, int32_t top
  */
 int moe_plan_set_wait_timeout(moe_plan_t plan, uint64_t timeout_ns);
 
+/* ================================================================ around the experts
+ *
+ * Operators that sit right before and beside the expert layer in a model's block: the
+ * residual add with RMSNorm and quantised outputs, the router with its balance loss and
+ * per-expert counts (forward and backward), and a dense linear product in the experts'
+ * microscaled formats. The same conventions as above (status codes, caller-owned device
+ * memory, no allocation, asynchronous on the given stream, every call capturable in a
+ * CUDA graph), except for alignment: row-strided tensors (x, residual, sum, out, logits,
+ * gradients) only need their element's alignment, with rows a stride (in elements) apart;
+ * codes, scales and workspaces are 256-byte aligned unless noted.
+ */
+
+/* Where quantised rows go: codes, block scales and (NVFP4) one fp32 scale per row.
+ *   format     MOE_FMT_MXFP8 / MOE_FMT_NVFP4 / MOE_FMT_MXFP4
+ *   sf_layout  MOE_SF_ROWS:  sf u8 [rows, K/g] row-major (g = 32; NVFP4: 16)
+ *              MOE_SF_ATOMS: the layout moe_linear_forward_quantized reads: scale block kb of
+ *                            row r at byte moe_sf_atoms_size's layout [row tile of 128][K stage]
+ *                            [S][512], (r % 32) * 16 + (r % 128 / 32) * 4 + kb % 4 inside an
+ *                            atom; scale bytes past K are written as zero, rows past the last
+ *                            one are left alone
+ *   codes      u8 [rows, K/vpe], contiguous, 16-byte aligned
+ *   row_scale  fp32 [rows] for NVFP4, else NULL
+ * Recipe: the dispatch quantiser's. MX: e = the smallest exponent with amax <= top * 2^e
+ * (top 448 or 6), codes round(v / 2^e); NVFP4: row scale amax / 2688, block scale
+ * E4M3(amax_b / (row_scale * 6)), codes E2M1(v / (scale * row_scale)). Round to nearest even,
+ * saturating. Values that are not finite are not hidden: a block holding a NaN or an
+ * infinity gets the scale NaN (MX: byte 255), an NVFP4 row holding one gets a NaN row scale.
+ */
+#define MOE_SF_ROWS  0
+#define MOE_SF_ATOMS 1
+typedef struct moe_quant {
+    int32_t format;
+    int32_t sf_layout;
+    void*   codes;
+    void*   sf;
+    float*  row_scale;
+} moe_quant_t;
+
+/* Bytes of the scales of [rows, K] in the given layout. Host-only. */
+int moe_quant_sf_size(int32_t format, int32_t sf_layout, int64_t rows, int64_t K, size_t* bytes);
+
+/*
+ * Quantise the rows of x (bf16 [rows, K], row stride x_stride elements) into q.
+ * K a multiple of 32, at most 16384. rows == 0 launches nothing.
+ */
+int moe_quantize(int32_t rows, int32_t K, const void* x, int64_t x_stride, const moe_quant_t* q, void* stream);
+
+/*
+ * z = x + residual (fp32; z = x when residual is NULL), sum_out = bf16(z),
+ * y = gamma * z / sqrt(mean(z^2) + eps), out = bf16(y), q = quantised y (from the fp32 y).
+ *   x, residual, sum_out, out   bf16 [rows, H] with their own row strides; residual, sum_out,
+ *                               out and q may be NULL, but one of out and q is given; sum_out may
+ *                               be residual or x, and out may be x, at the same stride (each row
+ *                               is read before it is written); no other overlap
+ *   gamma                       fp32 [H], applied verbatim
+ *   H                           1 .. 16384; a multiple of 32 with q
+ */
+int moe_add_rmsnorm(int32_t rows, int32_t hidden, const void* x, int64_t x_stride, const void* residual,
+                    int64_t residual_stride, const float* gamma, float eps, void* sum_out, int64_t sum_stride,
+                    void* out, int64_t out_stride, const moe_quant_t* q, void* stream);
+
+/*
+ * Router: probabilities p = softmax(logits), the top_k experts of each token by descending
+ * logit (ties to the lowest expert id), their weights p (renormalize: divided by their sum),
+ * tokens per expert, and the balance loss
+ *   loss = coef * E * sum_e f_e P_e,  f_e = counts_e / (top_k * n),  P_e = sum_t p[t,e] / n
+ * over the n valid tokens (0 when n = 0). A token is not valid when its mask byte is 0 or all
+ * its logits are -inf: its ids are -1 (which moe_forward masks), its weights 0, and it adds to
+ * no count, whatever its logits hold. An expert whose logit is -inf is never taken: slots
+ * left over get id -1, weight 0. A NaN (which sorts above every number) or +inf logit of a valid
+ * token makes its weights, and the loss, NaN; its ids stay in range.
+ */
+#define MOE_LOGITS_F32  0
+#define MOE_LOGITS_BF16 1
+typedef struct moe_router_config {
+    int32_t num_experts;     /* 1 .. 512 */
+    int32_t top_k;           /* 1 .. min(num_experts, 32) */
+    int32_t renormalize;     /* 0 or 1 */
+    int32_t logits_type;     /* MOE_LOGITS_* of logits and of their gradient */
+    float   balance_coef;    /* finite */
+} moe_router_config_t;
+
+/* Bytes of the workspace of moe_router_forward for num_tokens tokens. Host-only. */
+int moe_router_workspace_size(const moe_router_config_t* cfg, int32_t num_tokens, size_t* bytes);
+
+/*
+ *   logits        [T, E], row stride logits_stride elements
+ *   token_mask    u8 [T] (0: not valid) or NULL
+ *   topk_ids      int32 [T, k], topk_weights fp32 [T, k], contiguous
+ *   counts        int32 [E], num_valid int32 [1], prob_mean fp32 [E] (P_e), loss fp32 [1]: each
+ *                 may be NULL. Without prob_mean and loss no probabilities are summed.
+ * Deterministic: every sum has a fixed order. The workspace's contents do not matter.
+ */
+int moe_router_forward(const moe_router_config_t* cfg, int32_t num_tokens, const void* logits, int64_t logits_stride,
+                       const uint8_t* token_mask, int32_t* topk_ids, float* topk_weights, int32_t* counts,
+                       int32_t* num_valid, float* prob_mean, float* loss, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
+ * d_logits [T, E] (stride d_logits_stride) of  sum(d_weights * topk_weights) + d_loss * loss.
+ *   topk_ids, counts, num_valid   as moe_router_forward wrote them (counts are constants of the loss)
+ *   d_weights   fp32 [T, k] or NULL (no gradient through the weights)
+ *   d_loss      fp32 [1] on the device or NULL (no gradient through the loss; counts and num_valid
+ *               may then be NULL)
+ * Rows of tokens that are not valid get zeros. Slots with id -1 take no gradient.
+ */
+int moe_router_backward(const moe_router_config_t* cfg, int32_t num_tokens, const void* logits, int64_t logits_stride,
+                        const uint8_t* token_mask, const int32_t* topk_ids, const int32_t* counts,
+                        const int32_t* num_valid, const float* d_weights, const float* d_loss, void* d_logits,
+                        int64_t d_logits_stride, void* stream);
+
+/*
+ * Linear product in a microscaled format: out[t, n] = bf16(sum_k x[t, k] W[n, k]), with x
+ * quantised in the weight's format (MXFP8, NVFP4 or MXFP4) and fp32 accumulation on the tensor
+ * cores. out_features 1 .. 2^20, in_features a multiple of 32 up to 16384, max_tokens >= 1.
+ */
+typedef struct moe_linear_config {
+    int32_t out_features;    /* N */
+    int32_t in_features;     /* K */
+    int32_t max_tokens;
+    int32_t format;          /* MOE_FMT_MXFP8, MOE_FMT_NVFP4 or MOE_FMT_MXFP4 */
+} moe_linear_config_t;
+
+typedef struct moe_linear_plan_s* moe_linear_plan_t;
+
+int moe_linear_config_validate(const moe_linear_config_t* cfg);
+int moe_linear_plan(const moe_linear_config_t* cfg, moe_linear_plan_t* out);
+int moe_linear_plan_destroy(moe_linear_plan_t plan);
+/* Limit of each bounded wait inside the product's kernels (0: the default, 2 s). */
+int moe_linear_set_wait_timeout(moe_linear_plan_t plan, uint64_t timeout_ns);
+
+/*
+ * A weight. Checkpoint layout (src): codes [N, K/vpe], sf u8 [N, K/g] row-major, global_scale fp32 [1]
+ * (NVFP4, else NULL). Kernel layout (dst): codes unchanged (dst may share them with src: then
+ * nothing is copied), sf in atoms [K stage][round_up(N, 256) / 128][S][512] with zeros past N and K
+ * (moe_linear_weight_sf_size bytes), global_scale copied.
+ */
+typedef struct moe_linear_weight {
+    void*  codes;
+    void*  sf;
+    float* global_scale;
+} moe_linear_weight_t;
+int moe_linear_weight_sf_size(moe_linear_plan_t plan, size_t* bytes);
+int moe_linear_transform_weight(moe_linear_plan_t plan, const moe_linear_weight_t* src, moe_linear_weight_t* dst,
+                                void* stream);
+
+/* Bytes of the workspace of the two forwards below for num_tokens tokens. */
+int moe_linear_workspace_size(moe_linear_plan_t plan, int32_t num_tokens, size_t* bytes);
+
+/*
+ * moe_linear_forward:            x bf16 [T, K], row stride x_stride: quantised by the call.
+ * moe_linear_forward_quantized:  x already quantised (moe_quantize or moe_add_rmsnorm with
+ *                                MOE_SF_ATOMS) in the plan's format.
+ * out bf16 [T, N], row stride out_stride. Deterministic. T == 0 launches nothing.
+ */
+int moe_linear_forward(moe_linear_plan_t plan, int32_t num_tokens, const void* x, int64_t x_stride,
+                       const moe_linear_weight_t* weight, void* out, int64_t out_stride, void* workspace,
+                       size_t workspace_bytes, void* stream);
+int moe_linear_forward_quantized(moe_linear_plan_t plan, int32_t num_tokens, const moe_quant_t* x,
+                                 const moe_linear_weight_t* weight, void* out, int64_t out_stride, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+/* As moe_last_status, for a workspace of the two forwards above. */
+int moe_linear_last_status(moe_linear_plan_t plan, void* workspace, void* stream, int32_t* status);
+
 /* Static string for a status code. */
 const char* moe_error_string(int32_t status);
 

@@ -1,0 +1,432 @@
+"""Binding of the operators around the experts (include/moe.h, "around the experts"): residual
+add with RMSNorm and quantised outputs, the router with its balance loss, and the linear
+product in the microscaled formats. Argument checks and marshalling only: every step runs in
+the library's CUDA kernels, on the current stream unless one is given.
+"""
+from __future__ import annotations
+
+import ctypes
+from ctypes import byref
+from dataclasses import dataclass
+
+import torch
+
+from .moe import FORMATS, MOE_OK, MoeError, lib
+
+SF_LAYOUTS = {"rows": 0, "atoms": 1}
+SF_BLOCK = {"mxfp8": 32, "nvfp4": 16, "mxfp4": 32}
+VALUES_PER_BYTE = {"mxfp8": 1, "nvfp4": 2, "mxfp4": 2}
+LOGITS = {torch.float32: 0, torch.bfloat16: 1}
+
+P, I32, I64, SZ, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+
+
+class QuantC(ctypes.Structure):
+    _fields_ = [("format", I32), ("sf_layout", I32), ("codes", P), ("sf", P), ("row_scale", P)]
+
+
+class RouterConfigC(ctypes.Structure):
+    _fields_ = [("num_experts", I32), ("top_k", I32), ("renormalize", I32), ("logits_type", I32),
+                ("balance_coef", F32)]
+
+
+class LinearConfigC(ctypes.Structure):
+    _fields_ = [("out_features", I32), ("in_features", I32), ("max_tokens", I32), ("format", I32)]
+
+
+class LinearWeightC(ctypes.Structure):
+    _fields_ = [("codes", P), ("sf", P), ("global_scale", P)]
+
+
+_SIGNATURES = {
+    "moe_quant_sf_size": [I32, I32, I64, I64, P],
+    "moe_quantize": [I32, I32, P, I64, P, P],
+    "moe_add_rmsnorm": [I32, I32, P, I64, P, I64, P, F32, P, I64, P, I64, P, P],
+    "moe_router_workspace_size": [P, I32, P],
+    "moe_router_forward": [P, I32, P, I64, P, P, P, P, P, P, P, P, SZ, P],
+    "moe_router_backward": [P, I32, P, I64, P, P, P, P, P, P, P, I64, P],
+    "moe_linear_config_validate": [P],
+    "moe_linear_plan": [P, P],
+    "moe_linear_plan_destroy": [P],
+    "moe_linear_set_wait_timeout": [P, ctypes.c_uint64],
+    "moe_linear_weight_sf_size": [P, P],
+    "moe_linear_transform_weight": [P, P, P, P],
+    "moe_linear_workspace_size": [P, I32, P],
+    "moe_linear_forward": [P, I32, P, I64, P, P, I64, P, SZ, P],
+    "moe_linear_forward_quantized": [P, I32, P, P, P, I64, P, SZ, P],
+    "moe_linear_last_status": [P, P, P, P],
+}
+_fns = None
+
+
+def _lib():
+    global _fns
+    if _fns is None:
+        L = lib()
+        for name, args in _SIGNATURES.items():
+            fn = getattr(L, name)
+            fn.argtypes = args
+            fn.restype = ctypes.c_int
+        _fns = L
+    return _fns
+
+
+def _fail(fn: str, status: int):
+    raise MoeError(fn, status)
+
+
+def _stream(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _rows(name: str, t: torch.Tensor, dtype, shape=None):
+    """A 2-D CUDA tensor whose rows are contiguous (any row stride)."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(1) != 1 and t.shape[1] > 1 and t.shape[0] > 0:
+        raise ValueError(f"{name} must have contiguous rows")
+
+
+def _flat(name: str, t: torch.Tensor, dtype, numel: int):
+    """A contiguous CUDA tensor of numel elements."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous() or t.numel() != numel:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {numel} elements")
+
+
+# ----------------------------------------------------------------------------- quantised rows
+
+def sf_size(fmt: str, sf_layout: str, rows: int, K: int) -> int:
+    """Bytes of the block scales of [rows, K] (moe_quant_sf_size)."""
+    n = SZ()
+    st = _lib().moe_quant_sf_size(FORMATS[fmt], SF_LAYOUTS[sf_layout], rows, K, byref(n))
+    if st != MOE_OK:
+        _fail("moe_quant_sf_size", st)
+    return n.value
+
+
+class Quantized:
+    """Quantised rows: codes [rows, K / values per byte], block scales and, for NVFP4, one fp32
+    scale per row (moe_quant_t). Codes and scales are byte tensors (uint8 or a float8 type)."""
+
+    def __init__(self, fmt: str, shape, codes: torch.Tensor, sf: torch.Tensor, row_scale: torch.Tensor | None,
+                 sf_layout: str = "rows"):
+        rows, K = shape
+        vpb = VALUES_PER_BYTE[fmt]
+        if codes.element_size() != 1 or sf.element_size() != 1:
+            raise ValueError("codes and scales must be byte tensors")
+        if not codes.is_cuda or not codes.is_contiguous() or codes.numel() != rows * K // vpb:
+            raise ValueError(f"codes must be a contiguous CUDA tensor of {rows * K // vpb} bytes")
+        if not sf.is_cuda or not sf.is_contiguous() or sf.numel() < sf_size(fmt, sf_layout, rows, K):
+            raise ValueError("scales must be a contiguous CUDA tensor of sf_size(...) bytes")
+        if (row_scale is not None) != (fmt == "nvfp4"):
+            raise ValueError("NVFP4, and only NVFP4, has a scale per row")
+        if row_scale is not None:
+            _flat("row_scale", row_scale, torch.float32, rows)
+        self.fmt, self.shape, self.sf_layout = fmt, (rows, K), sf_layout
+        self.codes, self.sf, self.row_scale = codes, sf, row_scale
+        self._c = QuantC(FORMATS[fmt], SF_LAYOUTS[sf_layout], codes.data_ptr(), sf.data_ptr(),
+                         None if row_scale is None else row_scale.data_ptr())
+
+    @classmethod
+    def alloc(cls, fmt: str, rows: int, K: int, sf_layout: str = "atoms", device=None) -> "Quantized":
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        return cls(fmt, (rows, K),
+                   torch.empty((rows, K // VALUES_PER_BYTE[fmt]), dtype=torch.uint8, device=device),
+                   torch.empty(sf_size(fmt, sf_layout, rows, K), dtype=torch.uint8, device=device),
+                   torch.empty(rows, dtype=torch.float32, device=device) if fmt == "nvfp4" else None, sf_layout)
+
+
+def quantize(x: torch.Tensor, fmt: str, sf_layout: str = "atoms", out: Quantized | None = None,
+             stream=None) -> Quantized:
+    """moe_quantize: the rows of x (bf16 [rows, K]) in a microscaled format."""
+    _rows("x", x, torch.bfloat16)
+    if out is None:
+        out = Quantized.alloc(fmt, x.shape[0], x.shape[1], sf_layout, x.device)
+    elif out.shape != tuple(x.shape) or out.fmt != fmt:
+        raise ValueError(f"out holds {out.fmt} {out.shape}, x is {tuple(x.shape)} for {fmt}")
+    st = _lib().moe_quantize(x.shape[0], x.shape[1], x.data_ptr(), x.stride(0), byref(out._c), _stream(stream))
+    if st != MOE_OK:
+        _fail("moe_quantize", st)
+    return out
+
+
+def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                sum_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                quantized: Quantized | None = None, stream=None):
+    """moe_add_rmsnorm: z = x + residual, y = gamma * z / sqrt(mean(z^2) + eps).
+
+    x, residual, sum_out (receives z), out (receives y): bf16 [rows, H]; gamma: fp32 [H];
+    quantized: receives y in its format. Without out and quantized, out is allocated.
+    Returns out if there is one, else quantized."""
+    _rows("x", x, torch.bfloat16)
+    shape = x.shape
+    rows, H = shape
+    _flat("gamma", gamma, torch.float32, H)
+    if out is None:
+        if quantized is None:
+            out = torch.empty((rows, H), dtype=torch.bfloat16, device=x.device)
+    else:
+        _rows("out", out, torch.bfloat16, shape)
+    if residual is not None:
+        _rows("residual", residual, torch.bfloat16, shape)
+    if sum_out is not None:
+        _rows("sum_out", sum_out, torch.bfloat16, shape)
+    if quantized is not None and quantized.shape != (rows, H):
+        raise ValueError(f"quantized holds {quantized.shape}, x is {tuple(shape)}")
+    st = _lib().moe_add_rmsnorm(
+        rows, H, x.data_ptr(), x.stride(0), None if residual is None else residual.data_ptr(),
+        0 if residual is None else residual.stride(0), gamma.data_ptr(), eps,
+        None if sum_out is None else sum_out.data_ptr(), 0 if sum_out is None else sum_out.stride(0),
+        None if out is None else out.data_ptr(), 0 if out is None else out.stride(0),
+        None if quantized is None else byref(quantized._c), _stream(stream))
+    if st != MOE_OK:
+        _fail("moe_add_rmsnorm", st)
+    return out if out is not None else quantized
+
+
+# ----------------------------------------------------------------------------- router
+
+@dataclass
+class RouterConfig:
+    num_experts: int
+    top_k: int
+    renormalize: bool = True
+    balance_coef: float = 0.0
+
+
+@dataclass
+class RouterOutput:
+    """Buffers of one Router.forward: topk_ids int32 [T, k] (-1: no expert), topk_weights fp32
+    [T, k], counts int32 [E], num_valid int32 [1] and, when training, prob_mean fp32 [E] and
+    loss fp32 [1]."""
+    topk_ids: torch.Tensor
+    topk_weights: torch.Tensor
+    counts: torch.Tensor | None
+    num_valid: torch.Tensor | None
+    prob_mean: torch.Tensor | None
+    loss: torch.Tensor | None
+    workspace: torch.Tensor
+
+
+class Router:
+    """Softmax router: top-k experts, their weights, per-expert counts and the balance loss
+    (moe_router_forward, moe_router_backward)."""
+
+    def __init__(self, cfg: RouterConfig):
+        self.cfg = cfg
+        self._c = {d: RouterConfigC(cfg.num_experts, cfg.top_k, 1 if cfg.renormalize else 0, code, cfg.balance_coef)
+                   for d, code in LOGITS.items()}
+        n = SZ()
+        st = _lib().moe_router_workspace_size(byref(self._c[torch.float32]), 0, byref(n))
+        if st != MOE_OK:
+            _fail("moe_router_workspace_size", st)
+
+    def workspace_size(self, num_tokens: int) -> int:
+        n = SZ()
+        st = _lib().moe_router_workspace_size(byref(self._c[torch.float32]), num_tokens, byref(n))
+        if st != MOE_OK:
+            _fail("moe_router_workspace_size", st)
+        return n.value
+
+    def alloc(self, num_tokens: int, training: bool = False, device=None) -> RouterOutput:
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        E, k, T = self.cfg.num_experts, self.cfg.top_k, num_tokens
+        empty = torch.empty
+        return RouterOutput(
+            empty((T, k), dtype=torch.int32, device=device), empty((T, k), dtype=torch.float32, device=device),
+            empty(E, dtype=torch.int32, device=device), empty(1, dtype=torch.int32, device=device),
+            empty(E, dtype=torch.float32, device=device) if training else None,
+            empty(1, dtype=torch.float32, device=device) if training else None,
+            empty(max(self.workspace_size(T), 1), dtype=torch.uint8, device=device))
+
+    def _inputs(self, logits: torch.Tensor, token_mask: torch.Tensor | None):
+        if logits.dtype not in LOGITS:
+            raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+        _rows("logits", logits, logits.dtype)
+        if logits.shape[1] != self.cfg.num_experts:
+            raise ValueError(f"logits must be [T, {self.cfg.num_experts}], got {tuple(logits.shape)}")
+        if token_mask is not None:
+            if token_mask.dtype not in (torch.bool, torch.uint8):
+                raise ValueError("token_mask must be bool or uint8")
+            _flat("token_mask", token_mask, token_mask.dtype, logits.shape[0])
+
+    def forward(self, logits: torch.Tensor, token_mask: torch.Tensor | None = None, out: RouterOutput | None = None,
+                training: bool = False, stream=None) -> RouterOutput:
+        """logits fp32 or bf16 [T, E]; token_mask bool [T] (False: padding). With out, its buffers
+        are written (prob_mean and loss when it has them); else they are allocated."""
+        self._inputs(logits, token_mask)
+        T, E, k = logits.shape[0], self.cfg.num_experts, self.cfg.top_k
+        o = self.alloc(T, training, logits.device) if out is None else out
+        if out is not None:
+            _flat("topk_ids", o.topk_ids, torch.int32, T * k)
+            _flat("topk_weights", o.topk_weights, torch.float32, T * k)
+            for name, dtype, n in (("counts", torch.int32, E), ("num_valid", torch.int32, 1),
+                                   ("prob_mean", torch.float32, E), ("loss", torch.float32, 1)):
+                t = getattr(o, name)
+                if t is not None:
+                    _flat(name, t, dtype, n)
+        st = _lib().moe_router_forward(
+            byref(self._c[logits.dtype]), T, logits.data_ptr(), logits.stride(0),
+            None if token_mask is None else token_mask.data_ptr(), o.topk_ids.data_ptr(), o.topk_weights.data_ptr(),
+            None if o.counts is None else o.counts.data_ptr(), None if o.num_valid is None else o.num_valid.data_ptr(),
+            None if o.prob_mean is None else o.prob_mean.data_ptr(), None if o.loss is None else o.loss.data_ptr(),
+            o.workspace.data_ptr(), o.workspace.numel(), _stream(stream))
+        if st != MOE_OK:
+            _fail("moe_router_forward", st)
+        return o
+
+    def backward(self, logits: torch.Tensor, topk_ids: torch.Tensor, counts: torch.Tensor | None = None,
+                 num_valid: torch.Tensor | None = None, d_weights: torch.Tensor | None = None,
+                 d_loss: torch.Tensor | None = None, token_mask: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The gradient of sum(d_weights * topk_weights) + d_loss * loss with respect to logits
+        (counts held constant), in the logits' type."""
+        self._inputs(logits, token_mask)
+        T, E, k = logits.shape[0], self.cfg.num_experts, self.cfg.top_k
+        if out is None:
+            out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        else:
+            _rows("out", out, logits.dtype, logits.shape)
+        _flat("topk_ids", topk_ids, torch.int32, T * k)
+        if d_weights is not None:
+            _flat("d_weights", d_weights, torch.float32, T * k)
+        if d_loss is not None:
+            _flat("d_loss", d_loss, torch.float32, 1)
+            if counts is None or num_valid is None:
+                raise ValueError("the loss's gradient needs counts and num_valid")
+            _flat("counts", counts, torch.int32, E)
+            _flat("num_valid", num_valid, torch.int32, 1)
+        st = _lib().moe_router_backward(
+            byref(self._c[logits.dtype]), T, logits.data_ptr(), logits.stride(0),
+            None if token_mask is None else token_mask.data_ptr(), topk_ids.data_ptr(),
+            None if counts is None else counts.data_ptr(), None if num_valid is None else num_valid.data_ptr(),
+            None if d_weights is None else d_weights.data_ptr(), None if d_loss is None else d_loss.data_ptr(),
+            out.data_ptr(), out.stride(0), _stream(stream))
+        if st != MOE_OK:
+            _fail("moe_router_backward", st)
+        return out
+
+
+# ----------------------------------------------------------------------------- linear product
+
+@dataclass
+class LinearConfig:
+    out_features: int
+    in_features: int
+    max_tokens: int
+    fmt: str = "nvfp4"
+
+    def to_c(self) -> LinearConfigC:
+        return LinearConfigC(self.out_features, self.in_features, self.max_tokens, FORMATS[self.fmt])
+
+
+def linear_validate(cfg: LinearConfig) -> int:
+    return _lib().moe_linear_config_validate(byref(cfg.to_c()))
+
+
+class LinearWeight:
+    """A weight in the kernel layout (LinearPlan.transform_weight)."""
+
+    def __init__(self, codes: torch.Tensor, sf: torch.Tensor, global_scale: torch.Tensor | None):
+        self.codes, self.sf, self.global_scale = codes, sf, global_scale
+        self._c = LinearWeightC(codes.data_ptr(), sf.data_ptr(),
+                                None if global_scale is None else global_scale.data_ptr())
+
+
+class LinearPlan:
+    """out[t, n] = sum_k x[t, k] W[n, k] with x and W in a microscaled format (moe_linear_*)."""
+
+    def __init__(self, cfg: LinearConfig):
+        self.cfg = cfg
+        h = ctypes.c_void_p()
+        st = _lib().moe_linear_plan(byref(cfg.to_c()), byref(h))
+        if st != MOE_OK:
+            _fail("moe_linear_plan", st)
+        self._h = h
+
+    def __del__(self):
+        if getattr(self, "_h", None) and _fns is not None:
+            _fns.moe_linear_plan_destroy(self._h)
+            self._h = None
+
+    def workspace_size(self, num_tokens: int) -> int:
+        n = SZ()
+        st = _lib().moe_linear_workspace_size(self._h, num_tokens, byref(n))
+        if st != MOE_OK:
+            _fail("moe_linear_workspace_size", st)
+        return n.value
+
+    def alloc_workspace(self, num_tokens: int, device=None) -> torch.Tensor:
+        return torch.zeros(max(self.workspace_size(num_tokens), 1), dtype=torch.uint8,
+                           device=device or torch.device("cuda", torch.cuda.current_device()))
+
+    def transform_weight(self, codes: torch.Tensor, sf: torch.Tensor, global_scale: torch.Tensor | None = None,
+                         stream=None) -> LinearWeight:
+        """Checkpoint codes [N, K / values per byte] and row-major block scales [N, K / g] (bytes), with
+        the NVFP4 global scale (fp32 [1]), in the kernel layout. The codes are shared, not copied."""
+        c = self.cfg
+        N, K = c.out_features, c.in_features
+        for name, t, n in (("codes", codes, N * K // VALUES_PER_BYTE[c.fmt]), ("sf", sf, N * K // SF_BLOCK[c.fmt])):
+            if t.element_size() != 1 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+                raise ValueError(f"{name} must be a contiguous CUDA byte tensor of {n} bytes")
+        if global_scale is not None:
+            _flat("global_scale", global_scale, torch.float32, 1)
+        n = SZ()
+        st = _lib().moe_linear_weight_sf_size(self._h, byref(n))
+        if st != MOE_OK:
+            _fail("moe_linear_weight_sf_size", st)
+        dst = LinearWeight(codes, torch.empty(n.value, dtype=torch.uint8, device=codes.device), global_scale)
+        src = LinearWeightC(codes.data_ptr(), sf.data_ptr(), None if global_scale is None else global_scale.data_ptr())
+        st = _lib().moe_linear_transform_weight(self._h, byref(src), byref(dst._c), _stream(stream))
+        if st != MOE_OK:
+            _fail("moe_linear_transform_weight", st)
+        return dst
+
+    def forward(self, x, weight: LinearWeight, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """x: bf16 [T, K] (quantised by the call) or a Quantized with scales in atoms; out bf16 [T, N]."""
+        c = self.cfg
+        quantized = isinstance(x, Quantized)
+        T, K = x.shape
+        if K != c.in_features:
+            raise ValueError(f"x must be [T, {c.in_features}], got {tuple(x.shape)}")
+        if not quantized:
+            _rows("x", x, torch.bfloat16)
+        if out is None:
+            out = torch.empty((T, c.out_features), dtype=torch.bfloat16, device=weight.codes.device)
+        else:
+            _rows("out", out, torch.bfloat16, (T, c.out_features))
+        if workspace is None:
+            workspace = self.alloc_workspace(T, out.device)
+        elif not workspace.is_cuda or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
+        L = _lib()
+        if quantized:
+            st = L.moe_linear_forward_quantized(self._h, T, byref(x._c), byref(weight._c), out.data_ptr(),
+                                                out.stride(0), workspace.data_ptr(), workspace.numel(),
+                                                _stream(stream))
+        else:
+            st = L.moe_linear_forward(self._h, T, x.data_ptr(), x.stride(0), byref(weight._c), out.data_ptr(),
+                                      out.stride(0), workspace.data_ptr(), workspace.numel(), _stream(stream))
+        if st != MOE_OK:
+            _fail("moe_linear_forward", st)
+        return out
+
+    def set_wait_timeout(self, ns: int):
+        """Limit of each bounded wait in the product's kernels (0: the default, 2 s)."""
+        st = _lib().moe_linear_set_wait_timeout(self._h, ns)
+        if st != MOE_OK:
+            _fail("moe_linear_set_wait_timeout", st)
+
+    def last_status(self, workspace: torch.Tensor, stream=None) -> int:
+        v = I32()
+        st = _lib().moe_linear_last_status(self._h, workspace.data_ptr(), _stream(stream), byref(v))
+        if st != MOE_OK:
+            _fail("moe_linear_last_status", st)
+        return v.value
