@@ -75,8 +75,10 @@ def _fail(fn: str, status: int):
     raise MoeError(fn, status)
 
 
-def _stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _stream(stream, t: torch.Tensor) -> int:
+    """The given stream, or the current one of t's device (its raw handle: a torch.cuda.Stream
+    object costs microseconds to make)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _rows(name: str, t: torch.Tensor, dtype, shape=None):
@@ -150,7 +152,7 @@ def quantize(x: torch.Tensor, fmt: str, sf_layout: str = "atoms", out: Quantized
         out = Quantized.alloc(fmt, x.shape[0], x.shape[1], sf_layout, x.device)
     elif out.shape != tuple(x.shape) or out.fmt != fmt:
         raise ValueError(f"out holds {out.fmt} {out.shape}, x is {tuple(x.shape)} for {fmt}")
-    st = _lib().moe_quantize(x.shape[0], x.shape[1], x.data_ptr(), x.stride(0), byref(out._c), _stream(stream))
+    st = _lib().moe_quantize(x.shape[0], x.shape[1], x.data_ptr(), x.stride(0), byref(out._c), _stream(stream, x))
     if st != MOE_OK:
         _fail("moe_quantize", st)
     return out
@@ -184,7 +186,7 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residua
         0 if residual is None else residual.stride(0), gamma.data_ptr(), eps,
         None if sum_out is None else sum_out.data_ptr(), 0 if sum_out is None else sum_out.stride(0),
         None if out is None else out.data_ptr(), 0 if out is None else out.stride(0),
-        None if quantized is None else byref(quantized._c), _stream(stream))
+        None if quantized is None else byref(quantized._c), _stream(stream, x))
     if st != MOE_OK:
         _fail("moe_add_rmsnorm", st)
     return out if out is not None else quantized
@@ -276,7 +278,7 @@ class Router:
             None if token_mask is None else token_mask.data_ptr(), o.topk_ids.data_ptr(), o.topk_weights.data_ptr(),
             None if o.counts is None else o.counts.data_ptr(), None if o.num_valid is None else o.num_valid.data_ptr(),
             None if o.prob_mean is None else o.prob_mean.data_ptr(), None if o.loss is None else o.loss.data_ptr(),
-            o.workspace.data_ptr(), o.workspace.numel(), _stream(stream))
+            o.workspace.data_ptr(), o.workspace.numel(), _stream(stream, logits))
         if st != MOE_OK:
             _fail("moe_router_forward", st)
         return o
@@ -307,7 +309,7 @@ class Router:
             None if token_mask is None else token_mask.data_ptr(), topk_ids.data_ptr(),
             None if counts is None else counts.data_ptr(), None if num_valid is None else num_valid.data_ptr(),
             None if d_weights is None else d_weights.data_ptr(), None if d_loss is None else d_loss.data_ptr(),
-            out.data_ptr(), out.stride(0), _stream(stream))
+            out.data_ptr(), out.stride(0), _stream(stream, logits))
         if st != MOE_OK:
             _fail("moe_router_backward", st)
         return out
@@ -383,7 +385,7 @@ class LinearPlan:
             _fail("moe_linear_weight_sf_size", st)
         dst = LinearWeight(codes, torch.empty(n.value, dtype=torch.uint8, device=codes.device), global_scale)
         src = LinearWeightC(codes.data_ptr(), sf.data_ptr(), None if global_scale is None else global_scale.data_ptr())
-        st = _lib().moe_linear_transform_weight(self._h, byref(src), byref(dst._c), _stream(stream))
+        st = _lib().moe_linear_transform_weight(self._h, byref(src), byref(dst._c), _stream(stream, codes))
         if st != MOE_OK:
             _fail("moe_linear_transform_weight", st)
         return dst
@@ -410,10 +412,10 @@ class LinearPlan:
         if quantized:
             st = L.moe_linear_forward_quantized(self._h, T, byref(x._c), byref(weight._c), out.data_ptr(),
                                                 out.stride(0), workspace.data_ptr(), workspace.numel(),
-                                                _stream(stream))
+                                                _stream(stream, out))
         else:
             st = L.moe_linear_forward(self._h, T, x.data_ptr(), x.stride(0), byref(weight._c), out.data_ptr(),
-                                      out.stride(0), workspace.data_ptr(), workspace.numel(), _stream(stream))
+                                      out.stride(0), workspace.data_ptr(), workspace.numel(), _stream(stream, out))
         if st != MOE_OK:
             _fail("moe_linear_forward", st)
         return out
@@ -426,7 +428,7 @@ class LinearPlan:
 
     def last_status(self, workspace: torch.Tensor, stream=None) -> int:
         v = I32()
-        st = _lib().moe_linear_last_status(self._h, workspace.data_ptr(), _stream(stream), byref(v))
+        st = _lib().moe_linear_last_status(self._h, workspace.data_ptr(), _stream(stream, workspace), byref(v))
         if st != MOE_OK:
             _fail("moe_linear_last_status", st)
         return v.value

@@ -30,7 +30,7 @@ struct NormArgs {
     int* zero;                   // words zeroed by the first CTA (the product's error word and counters)
     int n_zero;
 };
-cudaError_t launch_norm(const NormArgs& a, cudaStream_t st, bool pdl = false);
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
 
 // ------------------------------------------------------------------ router
 struct RouterArgs {
@@ -66,7 +66,7 @@ struct RouterGradArgs {
     void* dlogits;
     int64_t ldd;
 };
-int router_grid(int T, int E);
+int router_grid(int T);  // CTAs that leave partial sums in the workspace
 cudaError_t launch_router(const RouterArgs& a, cudaStream_t st);
 cudaError_t launch_router_grad(const RouterGradArgs& a, cudaStream_t st);
 

@@ -64,12 +64,14 @@ __device__ __forceinline__ uint32_t e2m1_codes(const float (&f)[8]) {
 constexpr uint32_t UE8M0_NAN = 0xFF;
 constexpr uint32_t E4M3_NAN = 0x7F;
 
-// exponent of the smallest power of two with amax <= TOP * 2^e, TOP = 448 (FP8) or 6, from
-// the bits of a positive finite amax: amax = m 2^(p) with m in [0.5, 1); 0 for zero and
-// subnormal magnitudes go through frexp's path in common.cuh
+// The smallest e with amax <= TOP * 2^e, clamped to -127, and 0 for amax = 0; TOP = 448 = 1.75 * 2^8
+// (FP8) or 6 = 1.5 * 2^2. For amax = (1 + f) 2^p: e = p - 8 while 1 + f <= 1.75, else p - 7 (FP4:
+// p - 2, 1.5, p - 1). A subnormal amax (biased exponent 0) lies below every clamped e.
 template <bool FP8>
 __device__ __forceinline__ int mx_exponent(float amax) {
-    return FP8 ? ue8m0_exponent(amax) : ue8m0_exponent_fp4(amax);
+    const uint32_t b = __float_as_uint(amax);
+    const int e = (int)(b >> 23) - 127 - (FP8 ? 8 : 2) + ((b & 0x7FFFFFu) > (FP8 ? 0x600000u : 0x400000u));
+    return b == 0 ? 0 : max(e, -127);
 }
 
 template <bool FP8>
