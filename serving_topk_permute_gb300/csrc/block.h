@@ -85,7 +85,17 @@ struct LinearArgs {
 // weight scale atoms [nks][sf_blocks][S][512] from row-major [N, K/g] bytes, zeros past N and K
 cudaError_t launch_pack_linear_sf(const uint8_t* src, uint8_t* dst, int fmt, int N, int K, cudaStream_t st);
 cudaError_t linear_prepare(int fmt);
-cudaError_t launch_linear(int fmt, const CUtensorMap& a, const CUtensorMap& b, const LinearArgs& p, int num_sms,
-                          cudaStream_t st, bool pdl = false);
+// The kernel for a product of these sizes: bt 0 means CTA pairs, else bt tokens a tile with K split
+// over `splits` CTAs.
+struct LinearShape {
+    int bt, splits;
+};
+LinearShape linear_shape(int M, int N, int nks);
+struct LinearMaps {
+    CUtensorMap w, x;      // code rows, boxes of 128 weight rows, and of bt (pairs: 128) tokens
+    CUtensorMap sfw, sfx;  // scale atoms as uint32 [atoms][128], boxes of S atoms (pairs only)
+};
+cudaError_t launch_linear(int fmt, const LinearMaps& m, const LinearArgs& p, const LinearShape& s, int num_sms,
+                          cudaStream_t st);
 
 }  // namespace moe

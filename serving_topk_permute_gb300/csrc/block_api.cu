@@ -73,6 +73,18 @@ bool map_rows(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t row
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// an array of 512-byte scale atoms as a 2-D uint32 tensor [atoms][128], loaded box_atoms at a time;
+// atoms past the last one are filled with zeros
+bool map_atoms(CUtensorMap* m, const void* base, uint64_t atoms, uint32_t box_atoms) {
+    cuuint64_t dims[2] = {ATOM_BYTES / 4, atoms};
+    cuuint64_t strides[1] = {ATOM_BYTES};
+    cuuint32_t box[2] = {ATOM_BYTES / 4, box_atoms};
+    cuuint32_t es[2] = {1, 1};
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 struct moe_linear_plan_s {
@@ -124,27 +136,33 @@ LinLayout lin_layout(const moe_linear_config_t& c, int T) {
 }
 
 int run_linear(moe_linear_plan_t plan, int T, const moe_quant_t& x, const moe_linear_weight_t* w, void* out,
-               int64_t out_stride, void* workspace, bool pdl, cudaStream_t st) {
+               int64_t out_stride, void* workspace, cudaStream_t st) {
     const moe_linear_config_t& c = plan->cfg;
     const uint64_t row_bytes = (uint64_t)fmt_row_bytes(c.format, c.in_features);
-    CUtensorMap ma, mb;
-    if (!map_rows(&ma, x.codes, row_bytes, (uint64_t)T, BM) ||
-        !map_rows(&mb, w->codes, row_bytes, (uint64_t)c.out_features, 256))
+    const int nks = (int)stages_of(c.format, c.in_features), S = fmt_sf_atoms(c.format);
+    const LinearShape shape = linear_shape(T, c.out_features, nks);
+    const int64_t sf_blocks = wt_sf_blocks(c.out_features);
+    LinearMaps m;
+    if (!map_rows(&m.w, w->codes, row_bytes, (uint64_t)c.out_features, BM) ||
+        !map_rows(&m.x, x.codes, row_bytes, (uint64_t)T, shape.bt ? shape.bt : 128))
+        return MOE_ERR_CUDA;
+    if (!shape.bt && (!map_atoms(&m.sfw, w->sf, (uint64_t)(nks * sf_blocks * S), S) ||
+                      !map_atoms(&m.sfx, x.sf, (uint64_t)(ceil_div(T, BM) * nks * S), S)))
         return MOE_ERR_CUDA;
     LinearArgs p{};
     p.sfa = (const uint8_t*)x.sf;
     p.sfb = (const uint8_t*)w->sf;
     p.M = T;
     p.N = c.out_features;
-    p.nks = (int)stages_of(c.format, c.in_features);
-    p.sf_blocks = (int)wt_sf_blocks(c.out_features);
+    p.nks = nks;
+    p.sf_blocks = (int)sf_blocks;
     p.x_scale = x.row_scale;
     p.w_scale = w->global_scale;
     p.out = (__nv_bfloat16*)out;
     p.ldo = out_stride;
     p.err = (int*)((uint8_t*)workspace + lin_layout(c, T).err);
     p.timeout_ns = plan->timeout_ns;
-    CUDA_TRY(launch_linear(c.format, ma, mb, p, plan->num_sms, st, pdl));
+    CUDA_TRY(launch_linear(c.format, m, p, shape, plan->num_sms, st));
     return MOE_OK;
 }
 
@@ -430,7 +448,7 @@ int moe_linear_forward(moe_linear_plan_t plan, int32_t num_tokens, const void* x
     a.n_zero = 1;
     CUDA_TRY(launch_norm(a, st));
     const moe_quant_t q{c.format, MOE_SF_ATOMS, a.codes, a.sf, a.row_scale};
-    return run_linear(plan, num_tokens, q, weight, out, out_stride, workspace, true, st);
+    return run_linear(plan, num_tokens, q, weight, out, out_stride, workspace, st);
 }
 
 int moe_linear_forward_quantized(moe_linear_plan_t plan, int32_t num_tokens, const moe_quant_t* x,
@@ -443,7 +461,7 @@ int moe_linear_forward_quantized(moe_linear_plan_t plan, int32_t num_tokens, con
     if (x->format != plan->cfg.format || x->sf_layout != MOE_SF_ATOMS) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
     CUDA_TRY(cudaMemsetAsync(workspace, 0, 16, st));  // the error word
-    return run_linear(plan, num_tokens, *x, weight, out, out_stride, workspace, false, st);
+    return run_linear(plan, num_tokens, *x, weight, out, out_stride, workspace, st);
 }
 
 int moe_linear_last_status(moe_linear_plan_t plan, void* workspace, void* stream, int32_t* status) {
