@@ -38,6 +38,25 @@ __device__ __forceinline__ bool lin_wait_cl(uint32_t bar, uint32_t parity, uint6
     return false;
 }
 
+// One lane of the warp, always the same. The producer and MMA warps run their loops with all
+// lanes and predicate only the copies and MMAs with this: the loop's addresses and descriptors
+// then stay in uniform registers. (A loop that one thread runs alone moves every operand there
+// for each instruction: measured, 4 MMAs and 12 scale copies took 1085 cycles to issue that way
+// and 408 this way, against 512 that the MMAs need.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// a wait of the whole warp: every lane returns the same
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, const volatile int* abort) {
+    return __all_sync(0xffffffffu, lin_wait(bar, parity, timeout_ns, abort));
+}
+__device__ __forceinline__ bool warp_wait_cl(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                             const volatile int* abort) {
+    return __all_sync(0xffffffffu, lin_wait_cl(bar, parity, timeout_ns, abort));
+}
+
 // One 32-byte K step of a stage: j-th of 4.
 template <int FMT, int GROUP>
 __device__ __forceinline__ void lin_mma(uint32_t d, uint64_t ad, uint64_t bd, int n, int j, uint32_t sfa, uint32_t sfb,
@@ -69,33 +88,25 @@ __device__ __forceinline__ void lin_mma(uint32_t d, uint64_t ad, uint64_t bd, in
 }
 
 // ------------------------------------------------------------------ CTA pairs
-#ifndef LIN_SFW
-#define LIN_SFW 1
-#endif
 template <int FMT>
 struct PairCfg {
     static constexpr int S = fmt_sf_atoms(FMT);
     static constexpr int BT = 256;                         // tokens of a tile
     static constexpr int NB = BT / NBLK;
-    // NVFP4's 12 scale atoms a stage go into tensor memory by four warps of each CTA
-    // (tcgen05.st); the other formats' 3 or 6 by the MMA thread's copies.
-    static constexpr bool SFW = FMT == MOE_FMT_NVFP4 && LIN_SFW;
-    static constexpr int SF_WARPS = SFW ? 4 : 0;
-    static constexpr int THREADS = GEMM_THREADS + 32 * SF_WARPS;
+    static constexpr int THREADS = GEMM_THREADS;
     static constexpr int STAGES = FMT == MOE_FMT_NVFP4 ? 5 : 6;
     static constexpr int A_BYTES = BM * BK_BYTES;         // this CTA's 128 weight rows
     static constexpr int B_BYTES = NBLK * BK_BYTES;       // this CTA's half of the tokens
     static constexpr int SFA_BYTES = S * ATOM_BYTES;
     static constexpr int SFB_BYTES = S * NB * ATOM_BYTES;  // both halves: each CTA's MMA half needs them
-    static constexpr uint32_t DATA_BYTES = A_BYTES + B_BYTES;
-    static constexpr uint32_t SF_BYTES = SFA_BYTES + SFB_BYTES;
-    static constexpr int STAGE_BYTES = (DATA_BYTES + SF_BYTES + 1023) / 1024 * 1024;
+    static constexpr uint32_t TX_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+    static constexpr int STAGE_BYTES = (TX_BYTES + 1023) / 1024 * 1024;
     static constexpr int ACC_COLS = BT;
     static constexpr int SF_COLS = 4 * S * (1 + NB);
-    static constexpr int BAR_BYTES = 512;
+    static constexpr int BAR_BYTES = 256;
     static constexpr int SMEM = STAGES * STAGE_BYTES + BAR_BYTES + 1024;
-    // barriers: full, empty, sf_data, sf_full [STAGES]; tfull, tempty, drain, teardown
-    static constexpr int NUM_BARS = 4 * STAGES + 4;
+    // barriers: full, empty [STAGES]; tfull, tempty, drain, teardown
+    static constexpr int NUM_BARS = 2 * STAGES + 4;
     static_assert(NUM_BARS * 8 + 16 <= BAR_BYTES, "barrier area");
     static_assert(ACC_COLS + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -118,7 +129,6 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
                        const LinearArgs p) {
     using C = PairCfg<FMT>;
     constexpr int S = C::S, NB = C::NB, STAGES = C::STAGES;
-    constexpr bool SFW = C::SFW;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE_BYTES);
@@ -130,17 +140,15 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
-    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, sfd0 = empty0 + 8 * STAGES,
-                   sff0 = sfd0 + 8 * STAGES, tfull_bar = sff0 + 8 * STAGES, tempty_bar = tfull_bar + 8,
-                   drain_bar = tfull_bar + 16, teardown_bar = tfull_bar + 24;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, tfull_bar = empty0 + 8 * STAGES,
+                   tempty_bar = tfull_bar + 8, drain_bar = tfull_bar + 16, teardown_bar = tfull_bar + 24;
+    const uint32_t smem0 = smem_u32(smem);
     const uint64_t tmo = p.timeout_ns;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full0 + 8 * s, leader ? 2 : 1);    // full (the leader's counts): both producers arrive
-            mbar_init(empty0 + 8 * s, 1);                // empty: the leader's commit
-            mbar_init(sfd0 + 8 * s, 1);                  // this CTA's scale atoms have landed
-            mbar_init(sff0 + 8 * s, leader ? 2 * 4 : 1);  // both CTAs' scale warps have written theirs
+            mbar_init(full0 + 8 * s, leader ? 2 : 1);  // full (the leader's counts): both producers arrive
+            mbar_init(empty0 + 8 * s, 1);              // empty: the leader's commit
         }
         mbar_init(tfull_bar, 1);
         mbar_init(tempty_bar, leader ? 2 * EPI_WARPS : EPI_WARPS);
@@ -177,61 +185,53 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            // Both CTAs count their code bytes (and, without scale warps, their scale bytes) on the
-            // leader's full barrier.
-            const uint32_t full_cl0 = mapa_shared(full0, 0);
-            const uint32_t tx = SFW ? C::DATA_BYTES : C::DATA_BYTES + C::SF_BYTES;
-            int stage = 0;
-            uint32_t phase = 0, issued = 0;
-            bool ok = true;
-            for (int tile = pair; ok && tile < total; tile += npairs) {
-                int nt, tt;
-                raster(tile, n_tiles, t_tiles, nt, tt);
-                const int w_blk = 2 * nt + (int)rank, x_blk = 2 * tt + (int)rank;  // this CTA's 128-row blocks
-                for (int ks = 0; ks < p.nks; ++ks) {
-                    const uint32_t empty = empty0 + 8 * stage, full_cl = full_cl0 + 8 * stage;
-                    if (!lin_wait(empty, phase ^ 1, tmo, abort_flag)) {
-                        give_up();
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t st = smem_u32(smem + stage * C::STAGE_BYTES);
-                    const uint32_t sf = st + C::DATA_BYTES;
+        // Both CTAs count their bytes on the leader's full barrier: each arrives on it with its own
+        // transaction count (the follower remotely), and its loads complete on it (cta_group::2).
+        const bool elected = elect_one();
+        const uint32_t full_cl0 = mapa_shared(full0, 0);
+        int stage = 0;
+        uint32_t phase = 0, issued = 0;
+        bool ok = true;
+        for (int tile = pair; ok && tile < total; tile += npairs) {
+            int nt, tt;
+            raster(tile, n_tiles, t_tiles, nt, tt);
+            const int w_blk = 2 * nt + (int)rank, x_blk = 2 * tt + (int)rank;  // this CTA's 128-row blocks
+            for (int ks = 0; ks < p.nks; ++ks) {
+                if (!warp_wait(empty0 + 8 * stage, phase ^ 1, tmo, abort_flag)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                const uint32_t st = smem0 + stage * C::STAGE_BYTES, sf = st + C::A_BYTES + C::B_BYTES;
+                const uint32_t full_cl = full_cl0 + 8 * stage;
+                if (elected) {
                     if (leader)
-                        mbar_arrive_expect_tx(full0 + 8 * stage, tx);
+                        mbar_arrive_expect_tx(full0 + 8 * stage, C::TX_BYTES);
                     else
-                        mbar_arrive_expect_tx_cluster(full_cl, tx);
-                    if constexpr (SFW) {
-                        const uint32_t sfd = sfd0 + 8 * stage;
-                        mbar_arrive_expect_tx(sfd, C::SF_BYTES);
-                        tma_load_2d(sf, &tmSFW, sfd, 0, (ks * p.sf_blocks + w_blk) * S);
-#pragma unroll
-                        for (int b = 0; b < NB; ++b)
-                            tma_load_2d(sf + (1 + b) * C::SFA_BYTES, &tmSFX, sfd, 0, ((NB * tt + b) * p.nks + ks) * S);
-                    }
+                        mbar_arrive_expect_tx_cluster(full_cl, C::TX_BYTES);
                     tma_load_2d_cg2(st, &tmW, full_cl, ks * BK_BYTES, w_blk * BM);
                     tma_load_2d_cg2(st + C::A_BYTES, &tmX, full_cl, ks * BK_BYTES, x_blk * NBLK);
-                    if constexpr (!SFW) {
-                        tma_load_2d_cg2(sf, &tmSFW, full_cl, 0, (ks * p.sf_blocks + w_blk) * S);
+                    tma_load_2d_cg2(sf, &tmSFW, full_cl, 0, (ks * p.sf_blocks + w_blk) * S);
 #pragma unroll
-                        for (int b = 0; b < NB; ++b)
-                            tma_load_2d_cg2(sf + (1 + b) * C::SFA_BYTES, &tmSFX, full_cl, 0,
-                                            ((NB * tt + b) * p.nks + ks) * S);
-                    }
-                    ++issued;
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                    for (int b = 0; b < NB; ++b)
+                        tma_load_2d_cg2(sf + (1 + b) * C::SFA_BYTES, &tmSFX, full_cl, 0,
+                                        ((NB * tt + b) * p.nks + ks) * S);
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
-            // Every load either CTA issued lands before the pair may exit. The follower reports its
-            // count to the leader; for a stage only one CTA issued (one of them gave up), the
-            // leader supplies the missing arrival, so that the stage's phase completes once the
-            // issued bytes have landed. A producer can run at most STAGES stages ahead of the other
-            // one (a slot is reused only after the MMA consumed it, which needs both arrivals), so
-            // each slot is touched once.
+        }
+        // Every load either CTA issued lands before the pair may exit. The follower reports its
+        // count to the leader; for a stage only one CTA issued (one of them gave up), the
+        // leader supplies the missing arrival, so that the stage's phase completes once the
+        // issued bytes have landed. A producer can run at most STAGES stages ahead of the other
+        // one (a slot is reused only after the MMA consumed it, which needs both arrivals), so
+        // each slot is touched once.
+        if (elected) {
             if (!leader) {
                 st_cluster_u32(mapa_shared(smem_u32((const void*)peer_issued), 0), issued);
                 mbar_arrive_release_cluster(mapa_shared(teardown_bar, 0));
@@ -245,43 +245,31 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
                     mbar_wait(full0 + 8 * s, (last / STAGES) & 1u, DRAIN_TIMEOUT_NS, never);
                 }
             }
-            if constexpr (SFW)
-                for (uint32_t s = 0; s < (uint32_t)STAGES && s < issued; ++s) {
-                    const uint32_t last = s + (issued - 1 - s) / STAGES * STAGES;
-                    mbar_wait(sfd0 + 8 * s, (last / STAGES) & 1u, DRAIN_TIMEOUT_NS, never);
-                }
         }
+        __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
+            const bool elected = elect_one();
             int stage = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, issued = false;
             for (int tile = pair; ok && tile < total; tile += npairs) {
-                if (!lin_wait_cl(tempty_bar, acc_phase ^ 1, tmo, abort_flag)) {
+                if (!warp_wait_cl(tempty_bar, acc_phase ^ 1, tmo, abort_flag)) {
                     give_up();
                     break;
                 }
                 tc_fence_after();
                 for (int ks = 0; ks < p.nks; ++ks) {
-                    const uint32_t full = full0 + 8 * stage, empty = empty0 + 8 * stage;
-                    if (!lin_wait_cl(full, phase, tmo, abort_flag)) {
+                    if (!warp_wait_cl(full0 + 8 * stage, phase, tmo, abort_flag)) {
                         give_up();
                         ok = false;
                         break;
                     }
-                    const uint32_t st = smem_u32(smem + stage * C::STAGE_BYTES);
+                    tc_fence_after();
+                    const uint32_t st = smem0 + stage * C::STAGE_BYTES, sf = st + C::A_BYTES + C::B_BYTES;
                     const uint32_t sfa_col = tmem_base + C::ACC_COLS + stage * C::SF_COLS;
                     const uint32_t sfb_col = sfa_col + 4 * S;
-                    if constexpr (SFW) {
-                        if (!lin_wait_cl(sff0 + 8 * stage, phase, tmo, abort_flag)) {
-                            give_up();
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                    } else {
-                        tc_fence_after();
-                        const uint32_t sf = st + C::DATA_BYTES;
+                    if (elected) {
 #pragma unroll
                         for (int a = 0; a < S; ++a) tc_cp2_sf_atom(sfa_col + 4 * a, sf_atom_desc(sf + a * ATOM_BYTES));
                         // shared memory holds the token atoms as [block][s]; tensor memory wants [s][block]
@@ -291,30 +279,33 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
                             for (int a = 0; a < S; ++a)
                                 tc_cp2_sf_atom(sfb_col + 4 * (a * NB + b),
                                                sf_atom_desc(sf + C::SFA_BYTES + (b * S + a) * ATOM_BYTES));
-                    }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        lin_mma<FMT, 2>(tmem_base, kmajor_sw128_desc(st + j * 32),
-                                        kmajor_sw128_desc(st + C::A_BYTES + j * 32), C::BT, j, sfa_col, sfb_col, NB,
-                                        (ks > 0 || j > 0) ? 1u : 0u);
+                        for (int j = 0; j < 4; ++j)
+                            lin_mma<FMT, 2>(tmem_base, kmajor_sw128_desc(st + j * 32),
+                                            kmajor_sw128_desc(st + C::A_BYTES + j * 32), C::BT, j, sfa_col, sfb_col, NB,
+                                            (ks > 0 || j > 0) ? 1u : 0u);
+                        tc_commit2_mc(empty0 + 8 * stage, 0x3);
+                    }
+                    __syncwarp();
                     issued = true;
-                    tc_commit2_mc(empty, 0x3);
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
                 if (!ok) break;
-                tc_commit2_mc(tfull_bar, 0x3);
+                if (elected) tc_commit2_mc(tfull_bar, 0x3);
+                __syncwarp();
                 acc_phase ^= 1;
             }
             // every MMA and copy issued completes before either CTA frees its tensor memory
             if (issued) {
-                tc_commit2_mc(drain_bar, 0x1);
+                if (elected) tc_commit2_mc(drain_bar, 0x1);
+                __syncwarp();
                 mbar_wait(drain_bar, 0, DRAIN_TIMEOUT_NS, never);
             }
         }
-    } else if (warp < 2 + EPI_WARPS) {
+    } else {
         const int q = warp % 4;         // the lane quarter of tensor memory this warp may read
         const int cg = (warp - 2) / 4;  // its 64 tokens of the tile
         const uint32_t leader_tempty = mapa_shared(tempty_bar, 0);
@@ -356,52 +347,6 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
                         *o = __float2bfloat16_rn(y);
                     }
                     o += p.ldo;
-                }
-            }
-        }
-    } else if constexpr (SFW) {
-        // Scale warps, one per lane quarter of tensor memory: lane i, columns 4a .. 4a + 3 <- bytes
-        // 16 i .. 16 i + 15 of the atom for column 4a (what a 32x128b.warpx4 copy gives). A stage's
-        // columns are written again only after its next atoms have landed, which follows the
-        // commit of the MMAs that read them.
-        const int q = warp % 4;
-        const uint32_t quarter = tmem_base + ((uint32_t)(q * 32) << 16);
-        const uint32_t sff_cl0 = mapa_shared(sff0, 0);
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int tile = pair; ok && tile < total; tile += npairs) {
-            for (int ks = 0; ks < p.nks; ++ks) {
-                if (!__all_sync(0xffffffffu, lin_wait(sfd0 + 8 * stage, phase, tmo, abort_flag))) {
-                    give_up();
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint8_t* sf = smem + stage * C::STAGE_BYTES + C::DATA_BYTES;
-                const uint32_t col = quarter + C::ACC_COLS + stage * C::SF_COLS;
-#pragma unroll
-                for (int a = 0; a < S; ++a)
-                    tmem_st4(col + 4 * a, *reinterpret_cast<const uint4*>(sf + a * ATOM_BYTES + 16 * lane));
-#pragma unroll
-                for (int a = 0; a < S; ++a)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        tmem_st4(col + 4 * S + 4 * (a * NB + b),
-                                 *reinterpret_cast<const uint4*>(sf + C::SFA_BYTES + (b * S + a) * ATOM_BYTES +
-                                                                 16 * lane));
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (leader)
-                        mbar_arrive(sff0 + 8 * stage);
-                    else
-                        mbar_arrive_cluster(sff_cl0 + 8 * stage);
-                }
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1;
                 }
             }
         }
@@ -462,6 +407,7 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT>::THREADS, 2)
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, done_bar = empty0 + 8 * STAGES;
+    const uint32_t smem0 = smem_u32(smem);
     const uint64_t tmo = p.timeout_ns;
     // grid.x = splits (one cluster), grid.y = weight tiles, grid.z = token tiles
     const uint32_t splits = gridDim.x, rank = blockIdx.x;
@@ -492,57 +438,62 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT>::THREADS, 2)
 
     bool complete = true;  // meaningful in the epilogue's warps
     if (warp == 0) {
-        if (lane == 0) {
-            auto load_w = [&](int ks, int stage) {
-                const uint32_t st = smem_u32(smem + stage * C::STAGE_BYTES), full = full0 + 8 * stage;
-                mbar_arrive_expect_tx(full, C::TX_BYTES);
-                tma_load_2d(st, &tmW, full, ks * BK_BYTES, nt * BM);
-                bulk_load(st + C::A_BYTES + C::B_BYTES, p.sfb + ((int64_t)ks * p.sf_blocks + nt) * C::SF_BYTES,
-                          C::SF_BYTES, full);
-            };
-            auto load_x = [&](int ks, int stage) {
-                const uint32_t st = smem_u32(smem + stage * C::STAGE_BYTES), full = full0 + 8 * stage;
-                tma_load_2d(st + C::A_BYTES, &tmX, full, ks * BK_BYTES, tt * BT);
-                // token tiles start at multiples of 128 rows, or there is only one
-                bulk_load(st + C::A_BYTES + C::B_BYTES + C::SF_BYTES,
-                          p.sfa + ((int64_t)(tt * BT / BM) * p.nks + ks) * C::SF_BYTES, C::SF_BYTES, full);
-            };
-            // The weights do not depend on the previous kernel (the quantisation of x): the first
-            // stages' weights are on their way before the wait for it.
-            const int ahead = min(k1 - k0, STAGES);
+        const bool elected = elect_one();
+        auto load_w = [&](int ks, int stage) {
+            const uint32_t st = smem0 + stage * C::STAGE_BYTES, full = full0 + 8 * stage;
+            mbar_arrive_expect_tx(full, C::TX_BYTES);
+            tma_load_2d(st, &tmW, full, ks * BK_BYTES, nt * BM);
+            bulk_load(st + C::A_BYTES + C::B_BYTES, p.sfb + ((int64_t)ks * p.sf_blocks + nt) * C::SF_BYTES, C::SF_BYTES,
+                      full);
+        };
+        auto load_x = [&](int ks, int stage) {
+            const uint32_t st = smem0 + stage * C::STAGE_BYTES, full = full0 + 8 * stage;
+            tma_load_2d(st + C::A_BYTES, &tmX, full, ks * BK_BYTES, tt * BT);
+            // token tiles start at multiples of 128 rows, or there is only one
+            bulk_load(st + C::A_BYTES + C::B_BYTES + C::SF_BYTES,
+                      p.sfa + ((int64_t)(tt * BT / BM) * p.nks + ks) * C::SF_BYTES, C::SF_BYTES, full);
+        };
+        // The weights do not depend on the previous kernel (the quantisation of x): the first
+        // stages' weights are on their way before the wait for it.
+        const int ahead = min(k1 - k0, STAGES);
+        if (elected)
             for (int i = 0; i < ahead; ++i) load_w(k0 + i, i);
-            grid_dep_wait();
-            grid_dep_launch();
+        grid_dep_wait();
+        grid_dep_launch();
+        if (elected)
             for (int i = 0; i < ahead; ++i) load_x(k0 + i, i);
-            int issued = ahead;
-            for (; issued < k1 - k0; ++issued) {
-                const int stage = issued % STAGES;
-                if (!lin_wait(empty0 + 8 * stage, ((issued / STAGES) & 1) ^ 1, tmo, abort_flag)) {
-                    give_up();
-                    break;
-                }
+        __syncwarp();
+        int issued = ahead;
+        for (; issued < k1 - k0; ++issued) {
+            const int stage = issued % STAGES;
+            if (!warp_wait(empty0 + 8 * stage, ((issued / STAGES) & 1) ^ 1, tmo, abort_flag)) {
+                give_up();
+                break;
+            }
+            if (elected) {
                 load_w(k0 + issued, stage);
                 load_x(k0 + issued, stage);
             }
-            // every load this thread issued lands before the CTA may exit or reuse the ring
-            for (int s = 0; s < STAGES && s < issued; ++s) {
-                const int last = s + (issued - 1 - s) / STAGES * STAGES;
-                mbar_wait(full0 + 8 * s, (last / STAGES) & 1, DRAIN_TIMEOUT_NS, never);
-            }
+            __syncwarp();
+        }
+        // every load issued lands before the CTA may exit or reuse the ring
+        for (int s = 0; s < STAGES && s < issued; ++s) {
+            const int last = s + (issued - 1 - s) / STAGES * STAGES;
+            mbar_wait(full0 + 8 * s, (last / STAGES) & 1, DRAIN_TIMEOUT_NS, never);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            grid_dep_wait();
-            for (int i = 0; i < k1 - k0; ++i) {
-                const int stage = i % STAGES;
-                if (!lin_wait(full0 + 8 * stage, (i / STAGES) & 1, tmo, abort_flag)) {
-                    give_up();
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + stage * C::STAGE_BYTES);
-                const uint32_t sfa_col = tmem_base + BT + stage * C::SF_COLS, sfb_col = sfa_col + 4 * S;
-                const uint32_t sf = st + C::A_BYTES + C::B_BYTES;
+        const bool elected = elect_one();
+        grid_dep_wait();
+        for (int i = 0; i < k1 - k0; ++i) {
+            const int stage = i % STAGES;
+            if (!warp_wait(full0 + 8 * stage, (i / STAGES) & 1, tmo, abort_flag)) {
+                give_up();
+                break;
+            }
+            tc_fence_after();
+            const uint32_t st = smem0 + stage * C::STAGE_BYTES, sf = st + C::A_BYTES + C::B_BYTES;
+            const uint32_t sfa_col = tmem_base + BT + stage * C::SF_COLS, sfb_col = sfa_col + 4 * S;
+            if (elected) {
 #pragma unroll
                 for (int a = 0; a < 2 * S; ++a) tc_cp_sf_atom(sfa_col + 4 * a, sf_atom_desc(sf + a * ATOM_BYTES));
 #pragma unroll
@@ -552,10 +503,12 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT>::THREADS, 2)
                                     (i > 0 || j > 0) ? 1u : 0u);
                 tc_commit(empty0 + 8 * stage);
             }
-            // every MMA and copy issued has completed; also the epilogue's signal
-            tc_commit(done_bar);
-            mbar_wait(done_bar, 0, DRAIN_TIMEOUT_NS, never);
+            __syncwarp();
         }
+        // every MMA and copy issued has completed; also the epilogue's signal
+        if (elected) tc_commit(done_bar);
+        __syncwarp();
+        mbar_wait(done_bar, 0, DRAIN_TIMEOUT_NS, never);
     } else {
         grid_dep_wait();
         complete = __all_sync(0xffffffffu, lin_wait(done_bar, 0, tmo, abort_flag));
