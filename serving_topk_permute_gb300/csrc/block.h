@@ -21,6 +21,7 @@ struct NormArgs {
     int64_t ldx, ldr, lds, ldo;  // row strides in elements
     int T, H;
     float eps;
+    float inv_h;                 // 1 / H (set by launch_norm)
     int fmt;                     // -1: no quantised output
     int atoms;                   // 1: scales in atoms, 0: row-major
     int64_t nks;                 // K stages of the atom layout
@@ -74,7 +75,9 @@ cudaError_t launch_router_grad(const RouterGradArgs& a, cudaStream_t st);
 struct LinearArgs {
     const uint8_t* sfa;          // activation scale atoms [row tiles][nks][S][512]
     const uint8_t* sfb;          // weight scale atoms [nks][sf_blocks][S][512]
-    int M, N, nks, sf_blocks;
+    int M, N, K, nks, sf_blocks;
+    const __nv_bfloat16* x;      // quantised by the kernel when set (linear_quantises), rows ldx apart
+    int64_t ldx;
     const float* x_scale;        // NVFP4: fp32 [M]
     const float* w_scale;        // NVFP4: fp32 [1]
     __nv_bfloat16* out;
@@ -85,14 +88,18 @@ struct LinearArgs {
 // weight scale atoms [nks][sf_blocks][S][512] from row-major [N, K/g] bytes, zeros past N and K
 cudaError_t launch_pack_linear_sf(const uint8_t* src, uint8_t* dst, int fmt, int N, int K, cudaStream_t st);
 cudaError_t linear_prepare(int fmt);
-// The kernel for a product of these sizes: bt 0 means CTA pairs, else bt tokens a tile with K split
-// over `splits` CTAs.
+// The kernel for a product of these sizes: bt tokens a tile, K split over `splits` CTAs; splits 0
+// means CTA pairs.
 struct LinearShape {
     int bt, splits;
+    bool deep;  // at most one CTA for each SM: the ring takes all of its shared memory
+    // rows of the token map's box
+    int x_box() const { return splits ? bt : 128; }
 };
-LinearShape linear_shape(int M, int N, int nks);
+LinearShape linear_shape(int M, int N, int nks, int num_sms);
+bool linear_quantises(int fmt, const LinearShape& s, int M, int nks, const void* x, int64_t ldx);
 struct LinearMaps {
-    CUtensorMap w, x;      // code rows, boxes of 128 weight rows, and of bt (pairs: 128) tokens
+    CUtensorMap w, x;      // code rows, boxes of 128 weight rows and of x_box() tokens
     CUtensorMap sfw, sfx;  // scale atoms as uint32 [atoms][128], boxes of S atoms (pairs only)
 };
 cudaError_t launch_linear(int fmt, const LinearMaps& m, const LinearArgs& p, const LinearShape& s, int num_sms,

@@ -135,18 +135,19 @@ LinLayout lin_layout(const moe_linear_config_t& c, int T) {
     return L;
 }
 
-int run_linear(moe_linear_plan_t plan, int T, const moe_quant_t& x, const moe_linear_weight_t* w, void* out,
-               int64_t out_stride, void* workspace, cudaStream_t st) {
+// x: quantised rows, or (codes null) bf16 rows xb that the product quantises itself
+int run_linear(moe_linear_plan_t plan, int T, const moe_quant_t& x, const void* xb, int64_t x_stride,
+               const moe_linear_weight_t* w, void* out, int64_t out_stride, void* workspace, cudaStream_t st) {
     const moe_linear_config_t& c = plan->cfg;
     const uint64_t row_bytes = (uint64_t)fmt_row_bytes(c.format, c.in_features);
     const int nks = (int)stages_of(c.format, c.in_features), S = fmt_sf_atoms(c.format);
-    const LinearShape shape = linear_shape(T, c.out_features, nks);
+    const LinearShape shape = linear_shape(T, c.out_features, nks, plan->num_sms);
     const int64_t sf_blocks = wt_sf_blocks(c.out_features);
-    LinearMaps m;
+    LinearMaps m{};
     if (!map_rows(&m.w, w->codes, row_bytes, (uint64_t)c.out_features, BM) ||
-        !map_rows(&m.x, x.codes, row_bytes, (uint64_t)T, shape.bt ? shape.bt : 128))
+        (x.codes && !map_rows(&m.x, x.codes, row_bytes, (uint64_t)T, shape.x_box())))
         return MOE_ERR_CUDA;
-    if (!shape.bt && (!map_atoms(&m.sfw, w->sf, (uint64_t)(nks * sf_blocks * S), S) ||
+    if (!shape.splits && (!map_atoms(&m.sfw, w->sf, (uint64_t)(nks * sf_blocks * S), S) ||
                       !map_atoms(&m.sfx, x.sf, (uint64_t)(ceil_div(T, BM) * nks * S), S)))
         return MOE_ERR_CUDA;
     LinearArgs p{};
@@ -154,7 +155,10 @@ int run_linear(moe_linear_plan_t plan, int T, const moe_quant_t& x, const moe_li
     p.sfb = (const uint8_t*)w->sf;
     p.M = T;
     p.N = c.out_features;
+    p.K = c.in_features;
     p.nks = nks;
+    p.x = x.codes ? nullptr : (const __nv_bfloat16*)xb;
+    p.ldx = x_stride;
     p.sf_blocks = (int)sf_blocks;
     p.x_scale = x.row_scale;
     p.w_scale = w->global_scale;
@@ -432,6 +436,10 @@ int moe_linear_forward(moe_linear_plan_t plan, int32_t num_tokens, const void* x
     if (!x || !rows_ok(x, x_stride, num_tokens, c.in_features) || x == out) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
     uint8_t* ws = (uint8_t*)workspace;
+    const int64_t nks = stages_of(c.format, c.in_features);
+    if (linear_quantises(c.format, linear_shape(num_tokens, c.out_features, (int)nks, plan->num_sms),
+                         num_tokens, (int)nks, x, x_stride))
+        return run_linear(plan, num_tokens, moe_quant_t{}, x, x_stride, weight, out, out_stride, workspace, st);
     const LinLayout L = lin_layout(c, num_tokens);
     NormArgs a{};
     a.x = (const __nv_bfloat16*)x;
@@ -440,7 +448,7 @@ int moe_linear_forward(moe_linear_plan_t plan, int32_t num_tokens, const void* x
     a.H = c.in_features;
     a.fmt = c.format;
     a.atoms = 1;
-    a.nks = stages_of(c.format, c.in_features);
+    a.nks = nks;
     a.codes = ws + L.codes;
     a.sf = ws + L.sf;
     a.row_scale = c.format == MOE_FMT_NVFP4 ? (float*)(ws + L.scale) : nullptr;
@@ -448,7 +456,7 @@ int moe_linear_forward(moe_linear_plan_t plan, int32_t num_tokens, const void* x
     a.n_zero = 1;
     CUDA_TRY(launch_norm(a, st));
     const moe_quant_t q{c.format, MOE_SF_ATOMS, a.codes, a.sf, a.row_scale};
-    return run_linear(plan, num_tokens, q, weight, out, out_stride, workspace, st);
+    return run_linear(plan, num_tokens, q, nullptr, 0, weight, out, out_stride, workspace, st);
 }
 
 int moe_linear_forward_quantized(moe_linear_plan_t plan, int32_t num_tokens, const moe_quant_t* x,
@@ -461,7 +469,7 @@ int moe_linear_forward_quantized(moe_linear_plan_t plan, int32_t num_tokens, con
     if (x->format != plan->cfg.format || x->sf_layout != MOE_SF_ATOMS) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
     CUDA_TRY(cudaMemsetAsync(workspace, 0, 16, st));  // the error word
-    return run_linear(plan, num_tokens, *x, weight, out, out_stride, workspace, st);
+    return run_linear(plan, num_tokens, *x, nullptr, 0, weight, out, out_stride, workspace, st);
 }
 
 int moe_linear_last_status(moe_linear_plan_t plan, void* workspace, void* stream, int32_t* status) {

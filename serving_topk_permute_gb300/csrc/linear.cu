@@ -57,33 +57,53 @@ __device__ __forceinline__ bool warp_wait_cl(uint32_t bar, uint32_t parity, uint
     return __all_sync(0xffffffffu, lin_wait_cl(bar, parity, timeout_ns, abort));
 }
 
-// One 32-byte K step of a stage: j-th of 4.
-template <int FMT, int GROUP>
-__device__ __forceinline__ void lin_mma(uint32_t d, uint64_t ad, uint64_t bd, int n, int j, uint32_t sfa, uint32_t sfb,
-                                        int sfb_blocks, uint32_t accumulate) {
-    uint32_t id, ca, cb;
-    if constexpr (FMT == MOE_FMT_MXFP4) {
-        id = idesc_mxf4(n, 2u * (j & 1)), ca = sfa + 4 * (j >> 1), cb = sfb + 4 * sfb_blocks * (j >> 1);
-    } else if constexpr (FMT == MOE_FMT_MXFP8) {
-        id = idesc_mxf8(n, j), ca = sfa, cb = sfb;
-    } else {
-        id = idesc_nvf4(n), ca = sfa + 4 * j, cb = sfb + 4 * sfb_blocks * j;
-    }
-    if constexpr (GROUP == 2) {
-        id = idesc_m(id, 2 * BM);
-        if constexpr (FMT == MOE_FMT_MXFP4)
-            mma2_mxf4(d, ad, bd, id, ca, cb, accumulate);
-        else if constexpr (FMT == MOE_FMT_MXFP8)
-            mma2_mxf8(d, ad, bd, id, ca, cb, accumulate);
-        else
-            mma2_nvf4(d, ad, bd, id, ca, cb, accumulate);
-    } else {
-        if constexpr (FMT == MOE_FMT_MXFP4)
-            mma_mxf4(d, ad, bd, id, ca, cb, accumulate);
-        else if constexpr (FMT == MOE_FMT_MXFP8)
-            mma_mxf8(d, ad, bd, id, ca, cb, accumulate);
-        else
-            mma_nvf4(d, ad, bd, id, ca, cb, accumulate);
+// Shared-memory descriptors differ only in their low word: the address / 16 (and, for operand rows,
+// a leading offset of 1 in bits 16 ..). The high words are those of kmajor_sw128_desc and
+// sf_atom_desc.
+__device__ __forceinline__ uint64_t row_desc(uint32_t addr16) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(addr16 | 0x10000u), "n"(0x40004040));
+    return d;
+}
+__device__ __forceinline__ uint64_t atom_desc(uint32_t addr16) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(addr16), "n"(0x4008));
+    return d;
+}
+
+// The 4 K steps of a stage: rows at a and b (addresses / 16), N columns, scale factors in tensor
+// memory at sfa and sfb (of sfb_blocks 128-row blocks). fresh: the first stage of an accumulator.
+template <int FMT, int GROUP, int N>
+__device__ __forceinline__ void lin_stage(uint32_t d, uint32_t a, uint32_t b, uint32_t sfa, uint32_t sfb,
+                                          int sfb_blocks, bool fresh) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t id, ca, cb;
+        if constexpr (FMT == MOE_FMT_MXFP4) {
+            id = idesc_mxf4(N, 2u * (j & 1)), ca = sfa + 4 * (j >> 1), cb = sfb + 4 * sfb_blocks * (j >> 1);
+        } else if constexpr (FMT == MOE_FMT_MXFP8) {
+            id = idesc_mxf8(N, j), ca = sfa, cb = sfb;
+        } else {
+            id = idesc_nvf4(N), ca = sfa + 4 * j, cb = sfb + 4 * sfb_blocks * j;
+        }
+        const uint64_t ad = row_desc(a + 2 * j), bd = row_desc(b + 2 * j);
+        const uint32_t accumulate = j > 0 ? 1u : (fresh ? 0u : 1u);
+        if constexpr (GROUP == 2) {
+            id = idesc_m(id, 2 * BM);
+            if constexpr (FMT == MOE_FMT_MXFP4)
+                mma2_mxf4(d, ad, bd, id, ca, cb, accumulate);
+            else if constexpr (FMT == MOE_FMT_MXFP8)
+                mma2_mxf8(d, ad, bd, id, ca, cb, accumulate);
+            else
+                mma2_nvf4(d, ad, bd, id, ca, cb, accumulate);
+        } else {
+            if constexpr (FMT == MOE_FMT_MXFP4)
+                mma_mxf4(d, ad, bd, id, ca, cb, accumulate);
+            else if constexpr (FMT == MOE_FMT_MXFP8)
+                mma_mxf8(d, ad, bd, id, ca, cb, accumulate);
+            else
+                mma_nvf4(d, ad, bd, id, ca, cb, accumulate);
+        }
     }
 }
 
@@ -92,28 +112,27 @@ template <int FMT>
 struct PairCfg {
     static constexpr int S = fmt_sf_atoms(FMT);
     static constexpr int BT = 256;                         // tokens of a tile
-    static constexpr int NB = BT / NBLK;
+    static constexpr int NB = BT / NBLK;                   // 128-token blocks of scale atoms
     static constexpr int THREADS = GEMM_THREADS;
-    static constexpr int STAGES = FMT == MOE_FMT_NVFP4 ? 5 : 6;
-    static constexpr int A_BYTES = BM * BK_BYTES;         // this CTA's 128 weight rows
-    static constexpr int B_BYTES = NBLK * BK_BYTES;       // this CTA's half of the tokens
+    static constexpr int A_BYTES = BM * BK_BYTES;          // this CTA's 128 weight rows
+    static constexpr int B_BYTES = NBLK * BK_BYTES;        // this CTA's half of the tokens
     static constexpr int SFA_BYTES = S * ATOM_BYTES;
     static constexpr int SFB_BYTES = S * NB * ATOM_BYTES;  // both halves: each CTA's MMA half needs them
     static constexpr uint32_t TX_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
     static constexpr int STAGE_BYTES = (TX_BYTES + 1023) / 1024 * 1024;
-    static constexpr int ACC_COLS = BT;
-    static constexpr int SF_COLS = 4 * S * (1 + NB);
+    static constexpr int STAGES = FMT == MOE_FMT_NVFP4 ? 5 : 6;
     static constexpr int BAR_BYTES = 256;
+    static constexpr int SF_COLS = 4 * S * (1 + NB);
     static constexpr int SMEM = STAGES * STAGE_BYTES + BAR_BYTES + 1024;
     // barriers: full, empty [STAGES]; tfull, tempty, drain, teardown
     static constexpr int NUM_BARS = 2 * STAGES + 4;
     static_assert(NUM_BARS * 8 + 16 <= BAR_BYTES, "barrier area");
-    static_assert(ACC_COLS + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
+    static_assert(BT + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-// Tiles in groups of GROUP weight tiles, the tokens inside a group: the clusters that run at the
-// same time share few weight and token tiles.
+// Tiles in groups of 8 weight tiles, the tokens inside a group, so that the clusters that run at
+// the same time share few weight and token tiles.
 constexpr int RASTER_GROUP = 8;
 __device__ __forceinline__ void raster(int tile, int n_tiles, int t_tiles, int& nt, int& tt) {
     const int per = RASTER_GROUP * t_tiles, g = tile / per, rest = tile - g * per;
@@ -128,7 +147,7 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
                        const __grid_constant__ CUtensorMap tmSFW, const __grid_constant__ CUtensorMap tmSFX,
                        const LinearArgs p) {
     using C = PairCfg<FMT>;
-    constexpr int S = C::S, NB = C::NB, STAGES = C::STAGES;
+    constexpr int S = C::S, NB = C::NB, STAGES = C::STAGES, BT = C::BT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE_BYTES);
@@ -176,7 +195,7 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
     grid_dep_launch();
 
     const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
-    const int n_tiles = (p.N + 255) / 256, t_tiles = (p.M + C::BT - 1) / C::BT;
+    const int n_tiles = (p.N + 255) / 256, t_tiles = (p.M + BT - 1) / BT;
     const int total = n_tiles * t_tiles;
 
     auto give_up = [&]() {
@@ -266,24 +285,20 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = smem0 + stage * C::STAGE_BYTES, sf = st + C::A_BYTES + C::B_BYTES;
-                    const uint32_t sfa_col = tmem_base + C::ACC_COLS + stage * C::SF_COLS;
+                    const uint32_t st = (smem0 + stage * C::STAGE_BYTES) / 16, sf = st + (C::A_BYTES + C::B_BYTES) / 16;
+                    const uint32_t sfa_col = tmem_base + BT + stage * C::SF_COLS;
                     const uint32_t sfb_col = sfa_col + 4 * S;
                     if (elected) {
 #pragma unroll
-                        for (int a = 0; a < S; ++a) tc_cp2_sf_atom(sfa_col + 4 * a, sf_atom_desc(sf + a * ATOM_BYTES));
+                        for (int a = 0; a < S; ++a) tc_cp2_sf_atom(sfa_col + 4 * a, atom_desc(sf + a * ATOM_BYTES / 16));
                         // shared memory holds the token atoms as [block][s]; tensor memory wants [s][block]
 #pragma unroll
                         for (int b = 0; b < NB; ++b)
 #pragma unroll
                             for (int a = 0; a < S; ++a)
                                 tc_cp2_sf_atom(sfb_col + 4 * (a * NB + b),
-                                               sf_atom_desc(sf + C::SFA_BYTES + (b * S + a) * ATOM_BYTES));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            lin_mma<FMT, 2>(tmem_base, kmajor_sw128_desc(st + j * 32),
-                                            kmajor_sw128_desc(st + C::A_BYTES + j * 32), C::BT, j, sfa_col, sfb_col, NB,
-                                            (ks > 0 || j > 0) ? 1u : 0u);
+                                               atom_desc(sf + (C::SFA_BYTES + (b * S + a) * ATOM_BYTES) / 16));
+                        lin_stage<FMT, 2, BT>(tmem_base, st, st + C::A_BYTES / 16, sfa_col, sfb_col, NB, ks == 0);
                         tc_commit2_mc(empty0 + 8 * stage, 0x3);
                     }
                     __syncwarp();
@@ -306,26 +321,27 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
             }
         }
     } else {
+        constexpr int COLS = BT / 4;    // tokens of a warp
         const int q = warp % 4;         // the lane quarter of tensor memory this warp may read
-        const int cg = (warp - 2) / 4;  // its 64 tokens of the tile
+        const int cg = (warp - 2) / 4;  // its tokens of the tile
         const uint32_t leader_tempty = mapa_shared(tempty_bar, 0);
         uint32_t acc_phase = 0;
         for (int tile = pair; tile < total; tile += npairs) {
             // warp-uniform: every lane leaves together (a lane left behind would block in __syncwarp)
-            if (!__all_sync(0xffffffffu, lin_wait(tfull_bar, acc_phase, tmo, abort_flag))) {
+            if (!warp_wait(tfull_bar, acc_phase, tmo, abort_flag)) {
                 give_up();
                 break;
             }
             tc_fence_after();
             int nt, tt;
             raster(tile, n_tiles, t_tiles, nt, tt);
-            const int n = nt * 256 + (int)rank * BM + q * 32 + lane, t0 = tt * C::BT + cg * 64;
-            const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + cg * 64;
-            float v[2][32];
-            tmem_ld32(tacc, v[0]);
-            tmem_ld32(tacc + 32, v[1]);
+            const int n = nt * 256 + (int)rank * BM + q * 32 + lane, t0 = tt * BT + cg * COLS;
+            const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + cg * COLS;
+            // into registers, then the accumulator is handed back, and only then scaled and stored
+            float v[COLS / 32][32];
+#pragma unroll
+            for (int c = 0; c < COLS / 32; ++c) tmem_ld32(tacc + 32 * c, v[c]);
             tmem_ld_wait();
-            // hand the accumulator back as soon as it sits in registers
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -340,7 +356,7 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
                 if constexpr (FMT == MOE_FMT_NVFP4) ws = __ldg(p.w_scale);
                 __nv_bfloat16* o = p.out + (int64_t)t0 * p.ldo + n;
 #pragma unroll
-                for (int j = 0; j < 64; ++j) {
+                for (int j = 0; j < COLS; ++j) {
                     if (t0 + j < p.M) {
                         float y = v[j / 32][j % 32];
                         if constexpr (FMT == MOE_FMT_NVFP4) y *= __ldg(p.x_scale + t0 + j) * ws;
@@ -362,67 +378,94 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
 // ------------------------------------------------------------------ clusters that split K
 constexpr int MAX_SPLITS = 8;  // the portable cluster size
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-template <int FMT, int BT>
+// QUANT: the kernel quantises its slice of x itself, straight into the operand layout in shared
+// memory (all its K stages at once), instead of loading quantised rows.
+// DEEP: one CTA on an SM with a ring as deep as fits (grids of at most one CTA for each SM); else
+// two CTAs share an SM.
+template <int FMT, int BT, bool QUANT, bool DEEP>
 struct SplitCfg {
     static constexpr int S = fmt_sf_atoms(FMT);
-    static constexpr int STAGES = BT <= 32 || (BT <= 64 && S < 4) ? 4 : 3;  // two CTAs fit on an SM
-    static constexpr int EPI = 4;                     // epilogue warps, one for each lane quarter
+    static constexpr int EPI = 8;                       // epilogue warps, two for each lane quarter
     static constexpr int THREADS = 64 + 32 * EPI;
     static constexpr int A_BYTES = BM * BK_BYTES;
     static constexpr int B_BYTES = BT * BK_BYTES;
-    static constexpr int SF_BYTES = S * ATOM_BYTES;    // of either side
-    static constexpr uint32_t TX_BYTES = A_BYTES + B_BYTES + 2 * SF_BYTES;
-    static constexpr int STAGE_BYTES = (TX_BYTES + 1023) / 1024 * 1024;
+    static constexpr int SF_BYTES = S * ATOM_BYTES;      // of either side
+    static constexpr int X_STAGE = B_BYTES + SF_BYTES;   // a stage of x
+    static constexpr int X_STAGES = QUANT ? (FMT == MOE_FMT_MXFP8 ? 16 : 8) : 0;
+    // QUANT: x's code rows of every stage (multiples of 1024 bytes), then their atoms
+    static constexpr int X_CODES = X_STAGES * B_BYTES;
+    static constexpr int X_AREA = (X_STAGES * X_STAGE + 1023) / 1024 * 1024;
+    static constexpr uint32_t TX_BYTES = A_BYTES + SF_BYTES + (QUANT ? 0 : X_STAGE);
+    // a stage: weight rows, their atoms, x's atoms, then x's rows at a multiple of 1024 bytes
+    static constexpr int X_PAD = (2 * SF_BYTES + 1023) / 1024 * 1024 - SF_BYTES;
+    static constexpr int STAGE_BYTES =
+        QUANT ? (A_BYTES + SF_BYTES + 1023) / 1024 * 1024 : A_BYTES + SF_BYTES + X_PAD + B_BYTES;
+    // the sums of a tile: an area of their own where they are small, else the ring
+    static constexpr int SUM_BYTES = (BT + MAX_SPLITS) * BM * 4;  // splits * ceil(BT / splits) rows at most
+    static constexpr bool OWN_SUMS = BT <= 16;
+    static constexpr int BAR_BYTES = 256;
+    static constexpr int FIXED = X_AREA + (OWN_SUMS ? SUM_BYTES : 0) + BAR_BYTES + 1024;
+    static constexpr int BUDGET = DEEP ? 232448 : 233472 / 2 - 1024 - 512;
+    static constexpr int STAGES_MAX = (BUDGET - FIXED) / STAGE_BYTES;
+    static constexpr int STAGES = STAGES_MAX < 8 ? STAGES_MAX : 8;
+    static constexpr int SMEM = FIXED + STAGES * STAGE_BYTES;
     static constexpr int SF_COLS = 8 * S;
     static constexpr int COLS = BT + STAGES * SF_COLS;
-    static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
-    static constexpr int BAR_BYTES = 256;
-    static constexpr int SMEM = STAGES * STAGE_BYTES + BAR_BYTES + 1024;
-    static_assert(COLS <= 256, "tensor memory budget of two CTAs");
-    static_assert(2 * (SMEM + 1024) <= 233472, "shared memory budget of two CTAs");
-    static_assert(STAGES * STAGE_BYTES >= BT * BM * 4, "the ring holds the partial sums");
+    static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    static_assert(COLS <= (DEEP ? 512 : 256), "tensor memory budget");
+    static_assert(STAGES >= 3, "shared memory budget");
+    static_assert(OWN_SUMS || STAGES * STAGE_BYTES >= SUM_BYTES, "the ring holds the sums");
 };
 
-template <int FMT, int BT>
-__global__ void __launch_bounds__(SplitCfg<FMT, BT>::THREADS, 2)
+// The codes of 16 elements, unit u of row r of a K stage, where the MMA reads them: a row has 128
+// bytes, its 16-byte pieces numbered XOR r % 8 (the 128-byte swizzle that TMA applies).
+template <int FMT>
+__device__ __forceinline__ void put_unit(uint8_t* s, int r, int u, const uint32_t (&q)[4]) {
+    if constexpr (FMT == MOE_FMT_MXFP8)
+        *reinterpret_cast<uint4*>(s + r * BK_BYTES + ((u ^ (r & 7)) * 16)) = make_uint4(q[0], q[1], q[2], q[3]);
+    else
+        *reinterpret_cast<uint2*>(s + r * BK_BYTES + (((u >> 1) ^ (r & 7)) * 16) + (u & 1) * 8) = make_uint2(q[0], q[1]);
+}
+
+template <int FMT, int BT, bool QUANT, bool DEEP>
+__global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP ? 1 : 2)
     linear_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                         const LinearArgs p) {
-    using C = SplitCfg<FMT, BT>;
+    using C = SplitCfg<FMT, BT, QUANT, DEEP>;
     constexpr int S = C::S, STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE_BYTES);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 1);
+    uint8_t* xs = smem + STAGES * C::STAGE_BYTES;  // QUANT: x's codes and atoms
+    float* sums = reinterpret_cast<float*>(C::OWN_SUMS ? xs + C::X_AREA : smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(xs + C::X_AREA + (C::OWN_SUMS ? C::SUM_BYTES : 0));
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* never = reinterpret_cast<int*>(tmem_slot + 2);
+    __shared__ uint32_t s_amax[BT];  // QUANT, NVFP4: the tokens' magnitudes (bit patterns)
+    __shared__ float s_alpha[BT];    // NVFP4: what a token's sums are multiplied by
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, done_bar = empty0 + 8 * STAGES;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, done_bar = empty0 + 8 * STAGES,
+                   x_bar = done_bar + 8;
     const uint32_t smem0 = smem_u32(smem);
     const uint64_t tmo = p.timeout_ns;
     // grid.x = splits (one cluster), grid.y = weight tiles, grid.z = token tiles
     const uint32_t splits = gridDim.x, rank = blockIdx.x;
     const int nt = blockIdx.y, tt = blockIdx.z;
     const int k0 = (int)((int64_t)p.nks * rank / splits), k1 = (int)((int64_t)p.nks * (rank + 1) / splits);
+    const int tokens = min(BT, p.M - tt * BT);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2 * STAGES; ++s) mbar_init(full0 + 8 * s, 1);
         mbar_init(done_bar, 1);
+        mbar_init(x_bar, C::EPI);
         *abort_flag = 0;
         *never = 0;
         fence_mbar_init();
         prefetch_tmap(&tmW);
-        prefetch_tmap(&tmX);
+        if constexpr (!QUANT) prefetch_tmap(&tmX);
     }
+    if (QUANT && threadIdx.x < BT) s_amax[threadIdx.x] = 0;
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), C::TMEM);
         tmem_relinquish();
@@ -431,10 +474,20 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT>::THREADS, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    // matched just before the first store into another CTA's shared memory: by then it has started
+    if (C::OWN_SUMS && splits > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
     auto give_up = [&]() {
-        set_error(p.err, MOE_ERR_TIMEOUT);
         *abort_flag = 1;
+        // the first CTA of this grid clears the word after the same wait: let it, first
+        if constexpr (QUANT) __nanosleep(100000);
+        set_error(p.err, MOE_ERR_TIMEOUT);
     };
+    if constexpr (QUANT) {
+        // the predecessor may be any kernel: not even the weights are read before the wait
+        grid_dep_wait();
+        grid_dep_launch();
+        if (blockIdx.x == 0 && nt == 0 && tt == 0 && threadIdx.x == 0) *p.err = 0;
+    }
 
     bool complete = true;  // meaningful in the epilogue's warps
     if (warp == 0) {
@@ -443,23 +496,25 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT>::THREADS, 2)
             const uint32_t st = smem0 + stage * C::STAGE_BYTES, full = full0 + 8 * stage;
             mbar_arrive_expect_tx(full, C::TX_BYTES);
             tma_load_2d(st, &tmW, full, ks * BK_BYTES, nt * BM);
-            bulk_load(st + C::A_BYTES + C::B_BYTES, p.sfb + ((int64_t)ks * p.sf_blocks + nt) * C::SF_BYTES, C::SF_BYTES,
-                      full);
+            bulk_load(st + C::A_BYTES, p.sfb + ((int64_t)ks * p.sf_blocks + nt) * C::SF_BYTES, C::SF_BYTES, full);
         };
         auto load_x = [&](int ks, int stage) {
-            const uint32_t st = smem0 + stage * C::STAGE_BYTES, full = full0 + 8 * stage;
-            tma_load_2d(st + C::A_BYTES, &tmX, full, ks * BK_BYTES, tt * BT);
-            // token tiles start at multiples of 128 rows, or there is only one
-            bulk_load(st + C::A_BYTES + C::B_BYTES + C::SF_BYTES,
-                      p.sfa + ((int64_t)(tt * BT / BM) * p.nks + ks) * C::SF_BYTES, C::SF_BYTES, full);
+            if constexpr (!QUANT) {
+                const uint32_t st = smem0 + stage * C::STAGE_BYTES + C::A_BYTES + C::SF_BYTES, full = full0 + 8 * stage;
+                // token tiles start at multiples of 128 rows, or there is only one
+                bulk_load(st, p.sfa + ((int64_t)(tt * BT / BM) * p.nks + ks) * C::SF_BYTES, C::SF_BYTES, full);
+                tma_load_2d(st + C::X_PAD, &tmX, full, ks * BK_BYTES, tt * BT);
+            }
         };
-        // The weights do not depend on the previous kernel (the quantisation of x): the first
-        // stages' weights are on their way before the wait for it.
+        // Without QUANT the previous kernel has quantised x, after a wait of its own for whatever
+        // came before it: the weights, which it does not write, may be read while it runs.
         const int ahead = min(k1 - k0, STAGES);
         if (elected)
             for (int i = 0; i < ahead; ++i) load_w(k0 + i, i);
-        grid_dep_wait();
-        grid_dep_launch();
+        if constexpr (!QUANT) {
+            grid_dep_wait();
+            grid_dep_launch();
+        }
         if (elected)
             for (int i = 0; i < ahead; ++i) load_x(k0 + i, i);
         __syncwarp();
@@ -481,55 +536,156 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT>::THREADS, 2)
             const int last = s + (issued - 1 - s) / STAGES * STAGES;
             mbar_wait(full0 + 8 * s, (last / STAGES) & 1, DRAIN_TIMEOUT_NS, never);
         }
+        __syncwarp();
     } else if (warp == 1) {
         const bool elected = elect_one();
-        grid_dep_wait();
-        for (int i = 0; i < k1 - k0; ++i) {
-            const int stage = i % STAGES;
-            if (!warp_wait(full0 + 8 * stage, (i / STAGES) & 1, tmo, abort_flag)) {
+        bool ok = true;
+        if constexpr (QUANT) {
+            ok = warp_wait(x_bar, 0, tmo, abort_flag);  // x is in shared memory
+            if (!ok) give_up();
+        } else {
+            grid_dep_wait();
+        }
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int i = 0; ok && i < k1 - k0; ++i) {
+            if (!warp_wait(full0 + 8 * stage, phase, tmo, abort_flag)) {
                 give_up();
                 break;
             }
             tc_fence_after();
-            const uint32_t st = smem0 + stage * C::STAGE_BYTES, sf = st + C::A_BYTES + C::B_BYTES;
+            const uint32_t st = (smem0 + stage * C::STAGE_BYTES) / 16, sfw = st + C::A_BYTES / 16;
+            const uint32_t x = QUANT ? smem_u32(xs) / 16 + i * (C::B_BYTES / 16) : sfw + (C::SF_BYTES + C::X_PAD) / 16;
+            const uint32_t sfx = QUANT ? smem_u32(xs) / 16 + (C::X_CODES + i * C::SF_BYTES) / 16 : sfw + C::SF_BYTES / 16;
             const uint32_t sfa_col = tmem_base + BT + stage * C::SF_COLS, sfb_col = sfa_col + 4 * S;
             if (elected) {
 #pragma unroll
-                for (int a = 0; a < 2 * S; ++a) tc_cp_sf_atom(sfa_col + 4 * a, sf_atom_desc(sf + a * ATOM_BYTES));
+                for (int a = 0; a < S; ++a) tc_cp_sf_atom(sfa_col + 4 * a, atom_desc(sfw + a * ATOM_BYTES / 16));
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    lin_mma<FMT, 1>(tmem_base, kmajor_sw128_desc(st + j * 32),
-                                    kmajor_sw128_desc(st + C::A_BYTES + j * 32), BT, j, sfa_col, sfb_col, 1,
-                                    (i > 0 || j > 0) ? 1u : 0u);
+                for (int a = 0; a < S; ++a) tc_cp_sf_atom(sfb_col + 4 * a, atom_desc(sfx + a * ATOM_BYTES / 16));
+                lin_stage<FMT, 1, BT>(tmem_base, st, x, sfa_col, sfb_col, 1, i == 0);
                 tc_commit(empty0 + 8 * stage);
             }
             __syncwarp();
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
         }
         // every MMA and copy issued has completed; also the epilogue's signal
         if (elected) tc_commit(done_bar);
         __syncwarp();
         mbar_wait(done_bar, 0, DRAIN_TIMEOUT_NS, never);
+        __syncwarp();
     } else {
-        grid_dep_wait();
-        complete = __all_sync(0xffffffffu, lin_wait(done_bar, 0, tmo, abort_flag));
+        if constexpr (QUANT) {
+            // Units of 16 elements, one thread each, a token after the other. NVFP4's row scale needs
+            // the whole row's magnitude: every CTA reads the whole rows for it (a few tokens from
+            // L2), which takes less than an exchange between the CTAs.
+            constexpr int UNITS = FMT == MOE_FMT_MXFP8 ? 8 : 16;  // of a stage and token
+            constexpr int NT = 32 * C::EPI;
+            const int tid = threadIdx.x - 64, u0 = k0 * UNITS, per_token = (k1 - k0) * UNITS, uk = p.K / 16;
+            const uint4* x = reinterpret_cast<const uint4*>(p.x);
+            const int64_t row = p.ldx / 8;  // 16-byte pieces between rows
+            if constexpr (FMT == MOE_FMT_NVFP4) {
+                for (int r = 0; r < tokens; ++r) {
+                    float m = 0.0f;
+#pragma unroll 4
+                    for (int u = tid; u < uk; u += NT) m = max_or_nan(m, unit_amax(x[r * row + 2 * u], x[r * row + 2 * u + 1]));
+                    // magnitudes order like their bits, a NaN above infinity
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7FFFFFFFu);
+                    if (lane == 0) atomicMax(&s_amax[r], top);
+                }
+                asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory");
+            }
+            // every lane of a warp takes part in the shuffles: whole warps of units
+            const int total = tokens * per_token;
+            for (int i = tid; i - lane < total; i += NT) {
+                const int at = min(i, total - 1), r = at / per_token, u = at - r * per_token;
+                const bool past = u0 + u >= uk;  // past K: zeros, so that a scale cannot make a NaN of them
+                uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                if (!past) {
+                    a = x[r * row + 2 * (u0 + u)];
+                    b = x[r * row + 2 * (u0 + u) + 1];
+                }
+                float f[2][8];
+                unpack_bf16x8(a, f[0]);
+                unpack_bf16x8(b, f[1]);
+                const float amax = unit_amax(a, b);
+                uint8_t* codes = xs + (u / UNITS) * C::B_BYTES;
+                uint8_t* atoms = xs + C::X_CODES + (u / UNITS) * C::SF_BYTES;
+                const int us = u % UNITS;
+                uint32_t q[4] = {0, 0, 0, 0}, sb;
+                if constexpr (FMT == MOE_FMT_NVFP4) {
+                    const Nvfp4Row nv(nvfp4_row_scale(__uint_as_float(s_amax[r])));
+                    const float eff = nv.block_scale(amax, sb);
+                    uint32_t c[2];
+                    nv.codes<2>(f, eff, c);
+                    q[0] = c[0], q[1] = c[1];
+                } else {
+                    const float m = max_or_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                    const int e = mx_scale<FMT == MOE_FMT_MXFP8>(m, sb);
+                    if constexpr (FMT == MOE_FMT_MXFP8) {
+                        const uint2 lo = e4m3_codes(f[0], e), hi = e4m3_codes(f[1], e);
+                        q[0] = lo.x, q[1] = lo.y, q[2] = hi.x, q[3] = hi.y;
+                    } else {
+                        q[0] = mxfp4_codes(f[0], e), q[1] = mxfp4_codes(f[1], e);
+                    }
+                }
+                if (i >= total) continue;
+                put_unit<FMT>(codes, r, us, q);
+                const int kb = FMT == MOE_FMT_NVFP4 ? us : us / 2;
+                if (FMT == MOE_FMT_NVFP4 || us % 2 == 0)
+                    atoms[(kb / 4) * ATOM_BYTES + (r % 32) * 16 + (r / 32) * 4 + kb % 4] = past ? 0 : (uint8_t)sb;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_bar);
+        } else {
+            grid_dep_wait();
+        }
+        if constexpr (FMT == MOE_FMT_NVFP4) {
+            const int c = (int)threadIdx.x - 64;
+            if (c < tokens)
+                s_alpha[c] = (QUANT ? nvfp4_row_scale(__uint_as_float(s_amax[c])) : p.x_scale[tt * BT + c]) * __ldg(p.w_scale);
+        }
+        complete = warp_wait(done_bar, 0, tmo, abort_flag);
         if (!complete) give_up();
         tc_fence_after();
     }
-    // partial sums [token][128 features] into the ring, which no copy or MMA uses any more
-    __syncthreads();
-    float* part = reinterpret_cast<float*>(smem);
-    const int tokens = min(BT, p.M - tt * BT);
+    // Sums: the tile's tokens are shared out in runs of per_rank, and every CTA sends its
+    // accumulators of a token to its owner (rows of 128 features, one for each rank and token).
+    // The ring, where it serves as that area, is free in all CTAs after the first barrier.
+    const int per_rank = (tokens + (int)splits - 1) / (int)splits;
+    if (splits == 1) {
+        __syncthreads();
+    } else if (C::OWN_SUMS) {
+        __syncthreads();
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    } else {
+        cluster_sync();
+    }
     if (warp >= 2) {
         const int q = warp % 4;
         const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16);
+        const uint32_t mine = smem_u32(sums + (int)rank * per_rank * BM + q * 32 + lane);
+        constexpr int STEP = BT >= 32 ? 32 : 16;
 #pragma unroll 1
-        for (int c0 = 0; c0 < tokens; c0 += 32) {
+        for (int c0 = (warp - 2) / 4 * STEP; c0 < tokens; c0 += 2 * STEP) {
             float v[32];
             tmem_ld32(tacc + c0, v);  // for BT = 16 the upper columns hold scales: not kept
             tmem_ld_wait();
+            int owner = c0 / per_rank, left = (owner + 1) * per_rank - c0;  // tokens until the next owner
+            uint32_t at = mapa_shared(mine + (c0 - owner * per_rank) * (BM * 4), owner);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (c0 + j < BT) part[(c0 + j) * BM + q * 32 + lane] = v[j];
+            for (int j = 0; j < STEP; ++j) {
+                if (c0 + j < tokens) st_cluster_u32(at, __float_as_uint(v[j]));
+                at += BM * 4;
+                if (--left == 0 && c0 + j + 1 < tokens) {
+                    at = mapa_shared(mine, ++owner);
+                    left = per_rank;
+                }
+            }
         }
         tc_fence_before();
     }
@@ -537,31 +693,26 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT>::THREADS, 2)
         cluster_sync();
     else
         __syncthreads();
-    // The CTA of rank r adds the tokens r, r + splits, ... in rank order: a warp takes a token, a
-    // lane 4 features, with the loads of all ranks in flight.
+    // This CTA's tokens: a warp takes a token, a lane 4 features, the ranks added in order.
     if (warp >= 2 && complete) {
-        const int n = nt * BM + 4 * lane;
-        float ws = 1.0f;
-        if constexpr (FMT == MOE_FMT_NVFP4) ws = __ldg(p.w_scale);
-        for (int c = (int)(rank + splits * (warp - 2)); c < tokens; c += (int)splits * C::EPI) {
-            const uint32_t at = smem_u32(part + c * BM + 4 * lane);
-            float4 u[MAX_SPLITS];
-#pragma unroll
-            for (int r = 0; r < MAX_SPLITS; ++r) {
-                u[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (r < (int)splits) u[r] = ld_cluster_f32x4(mapa_shared(at, r));
-            }
+        const int n = nt * BM + 4 * lane, first = (int)rank * per_rank, count = min(per_rank, tokens - first);
+        __nv_bfloat16* out = p.out + (int64_t)(tt * BT + first) * p.ldo + n;
+        const bool whole = n + 4 <= p.N && ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(2 * p.ldo)) & 7) == 0;
+#pragma unroll 4
+        for (int i = warp - 2; i < count; i += C::EPI) {
+            const float4* u = reinterpret_cast<const float4*>(sums + i * BM) + lane;
             float4 y = u[0];
-#pragma unroll
-            for (int r = 1; r < MAX_SPLITS; ++r) y.x += u[r].x, y.y += u[r].y, y.z += u[r].z, y.w += u[r].w;
-            const int t = tt * BT + c;
+            for (uint32_t r = 1; r < splits; ++r) {
+                const float4 v = u[r * per_rank * (BM / 4)];
+                y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+            }
             if constexpr (FMT == MOE_FMT_NVFP4) {
-                const float alpha = p.x_scale[t] * ws;
+                const float alpha = s_alpha[first + i];
                 y.x *= alpha, y.y *= alpha, y.z *= alpha, y.w *= alpha;
             }
-            __nv_bfloat16* o = p.out + (int64_t)t * p.ldo + n;
+            __nv_bfloat16* o = out + i * p.ldo;
             const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
-            if (n + 4 <= p.N && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+            if (whole) {
                 *reinterpret_cast<uint2*>(o) =
                     make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
             } else {
@@ -572,10 +723,7 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT>::THREADS, 2)
             }
         }
     }
-    if (splits > 1)
-        cluster_sync();  // no CTA leaves while its sums are read
-    else
-        __syncthreads();
+    __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, C::TMEM);
@@ -607,36 +755,60 @@ cudaError_t launch_pack_linear_sf(const uint8_t* src, uint8_t* dst, int fmt, int
 }
 
 // ------------------------------------------------------------------ host side
-#ifndef LIN_PAIR_TILES
-#define LIN_PAIR_TILES 76
-#endif
-#ifndef LIN_CTAS
-#define LIN_CTAS 304
-#endif
-LinearShape linear_shape(int M, int N, int nks) {
+// Pairs from one tile for each of them on. Below, K is split in powers of two (clusters of 3 or 5 find
+// fewer places: 300 x 2048 x 4096 NVFP4 13.5 us in threes, 12.0 in fours) over at most one CTA for
+// each SM: 128 x 7168 x 4096 NVFP4 9.9 us, 11.7 with up to two; 333 x 4100 x 2080 MXFP4 9.5 us, 11.0
+// with up to two. With few tokens and long slices the MMA thread's issue bounds a CTA, and two on
+// an SM are faster: 1 x 7168 x 7168 MXFP8 11.8 us against 13.9.
+LinearShape linear_shape(int M, int N, int nks, int num_sms) {
     LinearShape s{};
-    const int64_t pair_tiles = ceil_div(M, 256) * ceil_div(N, 256);
-    if (M > 128 && pair_tiles >= LIN_PAIR_TILES) return s;
-    s.bt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const int64_t pairs = num_sms / 2;
+    if (M > 128 && ceil_div(M, 256) * ceil_div(N, 256) >= pairs) {
+        s.bt = 256;  // splits = 0
+        return s;
+    }
+    s.bt = M <= 16 ? 16 : M <= 64 ? 64 : 128;
     const int64_t tiles = ceil_div(M, s.bt) * ceil_div(N, BM);
-    s.splits = 1;
-    while (s.splits < MAX_SPLITS && tiles * s.splits * 2 <= LIN_CTAS && nks >= s.splits * 2) s.splits *= 2;
+    auto most = [&](int64_t slots) {
+        int k = 1;
+        while (2 * k <= MAX_SPLITS && tiles * 2 * k <= slots && 4 * k <= nks) k *= 2;
+        return k;
+    };
+    s.splits = most(num_sms);
+    s.deep = tiles * s.splits <= num_sms && s.splits <= 4;  // clusters of 8 with an SM for each CTA find few places
+    if (s.bt == 16 && nks > 10 * s.splits) {
+        s.splits = most(2 * num_sms);
+        s.deep = false;
+    }
     return s;
 }
 
-template <int FMT, int BT>
+// Whether the product can quantise x itself: few tokens, x's stages within the kernel's area,
+// aligned rows. Every CTA then quantises its slice; with 16 tokens that took longer than the
+// separate pass (16 x 7168 x 7168 MXFP4 10.6 against 7.5 us), with up to 4 it saves a launch.
+constexpr int QUANT_TOKENS = 4;
+bool linear_quantises(int fmt, const LinearShape& s, int M, int nks, const void* x, int64_t ldx) {
+    return M <= QUANT_TOKENS && s.bt == 16 && ceil_div(nks, s.splits) <= (fmt == MOE_FMT_MXFP8 ? 16 : 8) &&
+           ((uintptr_t)x | (uintptr_t)(2 * ldx)) % 16 == 0;
+}
+
+template <int FMT, int BT, bool QUANT>
 static cudaError_t split_attr() {
-    return cudaFuncSetAttribute(linear_split_kernel<FMT, BT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                SplitCfg<FMT, BT>::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(linear_split_kernel<FMT, BT, QUANT, true>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               SplitCfg<FMT, BT, QUANT, true>::SMEM);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(linear_split_kernel<FMT, BT, QUANT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                SplitCfg<FMT, BT, QUANT, false>::SMEM);
 }
 template <int FMT>
 static cudaError_t lin_attr() {
     cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          PairCfg<FMT>::SMEM);
-    if (e == cudaSuccess) e = split_attr<FMT, 16>();
-    if (e == cudaSuccess) e = split_attr<FMT, 32>();
-    if (e == cudaSuccess) e = split_attr<FMT, 64>();
-    if (e == cudaSuccess) e = split_attr<FMT, 128>();
+    if (e == cudaSuccess) e = split_attr<FMT, 16, true>();
+    if (e == cudaSuccess) e = split_attr<FMT, 16, false>();
+    if (e == cudaSuccess) e = split_attr<FMT, 64, false>();
+    if (e == cudaSuccess) e = split_attr<FMT, 128, false>();
     return e;
 }
 cudaError_t linear_prepare(int fmt) {
@@ -647,29 +819,37 @@ cudaError_t linear_prepare(int fmt) {
     }
 }
 
-template <int FMT, int BT>
-static cudaError_t split_t(const LinearMaps& m, const LinearArgs& p, int splits, cudaStream_t st) {
-    using C = SplitCfg<FMT, BT>;
+template <int FMT, int BT, bool QUANT, bool DEEP>
+static cudaError_t split_d(const LinearMaps& m, const LinearArgs& p, int splits, cudaStream_t st) {
+    using C = SplitCfg<FMT, BT, QUANT, DEEP>;
     LaunchAttrs at(true, splits);
     cudaLaunchConfig_t cfg = at.config(dim3((unsigned)splits, (unsigned)ceil_div(p.N, BM), (unsigned)ceil_div(p.M, BT)),
                                        dim3(C::THREADS), C::SMEM, st);
-    return cudaLaunchKernelEx(&cfg, linear_split_kernel<FMT, BT>, m.w, m.x, p);
+    return cudaLaunchKernelEx(&cfg, linear_split_kernel<FMT, BT, QUANT, DEEP>, m.w, m.x, p);
+}
+template <int FMT, int BT, bool QUANT = false>
+static cudaError_t split_t(const LinearMaps& m, const LinearArgs& p, const LinearShape& s, cudaStream_t st) {
+    return s.deep ? split_d<FMT, BT, QUANT, true>(m, p, s.splits, st) : split_d<FMT, BT, QUANT, false>(m, p, s.splits, st);
 }
 
 template <int FMT>
-static cudaError_t lin_t(const LinearMaps& m, const LinearArgs& p, const LinearShape& s, int num_sms, cudaStream_t st) {
-    switch (s.bt) {
-        case 16: return split_t<FMT, 16>(m, p, s.splits, st);
-        case 32: return split_t<FMT, 32>(m, p, s.splits, st);
-        case 64: return split_t<FMT, 64>(m, p, s.splits, st);
-        case 128: return split_t<FMT, 128>(m, p, s.splits, st);
-        default: break;
-    }
+static cudaError_t pair_t(const LinearMaps& m, const LinearArgs& p, int num_sms, cudaStream_t st) {
     LaunchAttrs at(true, 2);
     const int64_t tiles = ceil_div(p.M, 256) * ceil_div(p.N, 256), pairs = num_sms / 2;
     cudaLaunchConfig_t cfg = at.config(dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))),
                                        dim3(PairCfg<FMT>::THREADS), PairCfg<FMT>::SMEM, st);
     return cudaLaunchKernelEx(&cfg, linear_pair_kernel<FMT>, m.w, m.x, m.sfw, m.sfx, p);
+}
+
+template <int FMT>
+static cudaError_t lin_t(const LinearMaps& m, const LinearArgs& p, const LinearShape& s, int num_sms, cudaStream_t st) {
+    if (s.splits == 0)
+        return pair_t<FMT>(m, p, num_sms, st);
+    switch (s.bt) {
+        case 16: return p.x ? split_d<FMT, 16, true, false>(m, p, s.splits, st) : split_t<FMT, 16>(m, p, s, st);
+        case 64: return split_t<FMT, 64>(m, p, s, st);
+        default: return split_t<FMT, 128>(m, p, s, st);
+    }
 }
 cudaError_t launch_linear(int fmt, const LinearMaps& m, const LinearArgs& p, const LinearShape& s, int num_sms,
                           cudaStream_t st) {

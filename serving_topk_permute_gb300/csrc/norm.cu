@@ -142,23 +142,48 @@ __device__ __forceinline__ void load_gamma(float (&g)[8], const float* gamma, in
 
 constexpr int NORM_MAX_WARPS = 32;
 
-// Joins the row's warps in order: one value for each row of the CTA.
+// Joins the row's warps (32 at most), in a fixed order: one value for each row of the CTA.
 template <bool MAX>
 __device__ __forceinline__ float row_join(float v, float* s_red) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float u = __shfl_xor_sync(0xffffffffu, v, o);
-        v = MAX ? fmaxf(v, u) : v + u;
+        v = MAX ? max_or_nan(v, u) : v + u;
     }
     const int warps = blockDim.x / 32;
     if (warps == 1) return v;
     float* s = s_red + threadIdx.y * warps;
     if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = v;
     __syncthreads();
-    float t = 0.0f;
-    for (int w = 0; w < warps; ++w) t = MAX ? fmaxf(t, s[w]) : t + s[w];
+    float t = (int)threadIdx.x % 32 < warps ? s[threadIdx.x % 32] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float u = __shfl_xor_sync(0xffffffffu, t, o);
+        t = MAX ? max_or_nan(t, u) : t + u;
+    }
     return t;
 }
+
+// 1 / sqrt(ss / H + eps) as an unevaluated sum hi + lo, good to some 2^-40 of it: an approximation
+// and its Newton correction, whose residual 1 - v hi^2 is taken exactly by FMAs.
+struct Scale {
+    float hi, lo;
+    __device__ __forceinline__ Scale(float ss, float h, float inv_h, float eps) {
+        const float q = ss * inv_h, q_lo = __fmaf_rn(-q, h, ss) * inv_h;  // ss / h = q + q_lo
+        const float v = q + eps, b = v - q;
+        const float v_lo = ((q - (v - b)) + (eps - b)) + q_lo;  // the exact rest of the sum (Knuth's two-sum)
+        hi = rsqrtf(v);
+        const float t = v * hi, e = __fmaf_rn(v, hi, -t);  // v hi = t + e
+        const float r = __fmaf_rn(v_lo * hi, hi, __fmaf_rn(e, hi, __fmaf_rn(t, hi, -1.0f)));
+        lo = v < __uint_as_float(0x7F800000u) && v > 0.0f ? -0.5f * hi * r : 0.0f;
+    }
+    // z (hi + lo) g with one rounding that matters
+    __device__ __forceinline__ float apply(float z, float g) const {
+        const float t = z * hi;
+        const float e = __fmaf_rn(z, lo, __fmaf_rn(z, hi, -t));
+        return __fmaf_rn(t, g, e * g);
+    }
+};
 
 __device__ __forceinline__ void row_barrier() {
     if (blockDim.x == 32)
@@ -197,8 +222,10 @@ __global__ void __launch_bounds__(MAXT, MIN_CTAS) norm_kernel(const NormArgs a, 
 #pragma unroll
             for (int j = 0; j < 8; ++j) z[i][j] += f[j];
         }
+        float sq = 0.0f;  // by chunks: the rounding errors of many short sums average out
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(z[i][j], z[i][j], ss);
+        for (int j = 0; j < 8; ++j) sq = fmaf(z[i][j], z[i][j], sq);
+        ss += sq;
     }
     extern __shared__ uint4 s_rows[];  // RAGGED: [rows][chunks]
     uint4* s_row = s_rows + threadIdx.y * ((H + 7) / 8);
@@ -215,7 +242,11 @@ __global__ void __launch_bounds__(MAXT, MIN_CTAS) norm_kernel(const NormArgs a, 
     };
     if (a.sum) store(a.sum + t * a.lds);
     if (a.gamma) {
-        const float scale = 1.0f / sqrtf(row_join<false>(ss, s_red) / (float)H + a.eps);
+        // Quantised rows get y to about its last bit: where a block's magnitude lies at the edge between
+        // two exponents, an error of a few bits would change all of its codes.
+        const float total = row_join<false>(ss, s_red);
+        const float scale = FMT < 0 ? 1.0f / sqrtf(total / (float)H + a.eps) : 0.0f;
+        const Scale fine(total, (float)H, a.inv_h, a.eps);
 #pragma unroll
         for (int i = 0; i < MAXC; ++i) {
             const int c = tid + i * NT;
@@ -223,7 +254,7 @@ __global__ void __launch_bounds__(MAXT, MIN_CTAS) norm_kernel(const NormArgs a, 
                 float g[8];
                 load_gamma(g, a.gamma, c, H, gamma_aligned);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * scale * g[j];
+                for (int j = 0; j < 8; ++j) z[i][j] = FMT < 0 ? z[i][j] * scale * g[j] : fine.apply(z[i][j], g[j]);
             }
         }
     }
@@ -237,11 +268,12 @@ __global__ void __launch_bounds__(MAXT, MIN_CTAS) norm_kernel(const NormArgs a, 
         if constexpr (FMT == MOE_FMT_NVFP4) {
             float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < MAXC; ++i) m = fmaxf(m, amax_or_inf(z[i]));
+            for (int i = 0; i < MAXC; ++i) m = max_or_nan(m, amax_or_nan(z[i]));
             gs = nvfp4_row_scale(row_join<true>(m, s_red2));
             if (tid == 0 && live) a.row_scale[t] = gs;
         }
         if (!live) return;
+        const Nvfp4Row nv(gs);
         const int nkb = H / G;
         uint8_t* sf = a.atoms ? a.sf + act_sf_offset(t, 0, S, a.nks) : a.sf + t * nkb;
         auto put_sf = [&](int kb, uint32_t b) { sf[a.atoms ? (kb / 4) * ATOM_BYTES + kb % 4 : kb] = (uint8_t)b; };
@@ -255,7 +287,7 @@ __global__ void __launch_bounds__(MAXT, MIN_CTAS) norm_kernel(const NormArgs a, 
                 const uint2 q = quant_mxfp8(z[i], sb);
                 if (in) *reinterpret_cast<uint2*>(a.codes + t * H + c * 8) = q;
             } else {
-                const uint32_t q = FMT == MOE_FMT_MXFP4 ? quant_mxfp4(z[i], sb) : quant_nvfp4(z[i], gs, sb);
+                const uint32_t q = FMT == MOE_FMT_MXFP4 ? quant_mxfp4(z[i], sb) : quant_nvfp4(z[i], nv, sb);
                 if (in) *reinterpret_cast<uint32_t*>(a.codes + t * (H / 2) + c * 4) = q;
             }
             if (in && c % (G / 8) == 0) put_sf(c / (G / 8), sb);
@@ -265,6 +297,83 @@ __global__ void __launch_bounds__(MAXT, MIN_CTAS) norm_kernel(const NormArgs a, 
         if (a.atoms)
             for (int kb = nkb + tid; kb < a.nks * 4 * S; kb += NT) put_sf(kb, 0);
     }
+}
+
+// Quantisation alone, of aligned rows: thread t owns the 16-element units t, t + NT, ... (an NVFP4
+// block; two lanes make an MX block), and the magnitudes are taken on the packed bf16 pairs. This
+// takes half the instructions of the norm's path, which would otherwise bound it: 8192 x 7168 to
+// NVFP4 45.8 us through the norm's path.
+template <int FMT, int MAXU, int MAXT, int MIN_CTAS>
+__global__ void __launch_bounds__(MAXT, MIN_CTAS) quant_kernel(const NormArgs a) {
+    constexpr int S = fmt_sf_atoms(FMT), G = fmt_sf_block(FMT);
+    const int tid = threadIdx.x, NT = blockDim.x;
+    const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool live = t < a.T;  // uniform in a warp; other rows only take part in the barriers
+    const int units = live ? a.H / 16 : 0;
+    __shared__ float s_red[NORM_MAX_WARPS];
+    const uint4* x = reinterpret_cast<const uint4*>(a.x + t * a.ldx);
+    grid_dep_wait();
+    grid_dep_launch();
+    if (t == 0)
+        for (int i = tid; i < a.n_zero; i += NT) a.zero[i] = 0;
+    uint4 v[MAXU][2];
+#pragma unroll
+    for (int i = 0; i < MAXU; ++i) {
+        const int u = tid + i * NT;
+        v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+        if (u < units) {
+            v[i][0] = x[2 * u];
+            v[i][1] = x[2 * u + 1];
+        }
+    }
+    float amax[MAXU], row = 0.0f;
+#pragma unroll
+    for (int i = 0; i < MAXU; ++i) {
+        amax[i] = unit_amax(v[i][0], v[i][1]);
+        row = max_or_nan(row, amax[i]);
+    }
+    float gs = 1.0f;
+    if constexpr (FMT == MOE_FMT_NVFP4) {
+        gs = nvfp4_row_scale(row_join<true>(row, s_red));
+        if (tid == 0 && live) a.row_scale[t] = gs;
+    }
+    if (!live) return;
+    const Nvfp4Row nv(gs);
+    const int nkb = a.H / G;
+    uint8_t* sf = a.atoms ? a.sf + act_sf_offset(t, 0, S, a.nks) : a.sf + t * nkb;
+    auto put_sf = [&](int kb, uint32_t b) { sf[a.atoms ? (kb / 4) * ATOM_BYTES + kb % 4 : kb] = (uint8_t)b; };
+#pragma unroll
+    for (int i = 0; i < MAXU; ++i) {
+        const int u = tid + i * NT;
+        if (i * NT >= units) break;  // uniform across the row
+        const bool in = u < units;
+        float f[2][8];
+        unpack_bf16x8(v[i][0], f[0]);
+        unpack_bf16x8(v[i][1], f[1]);
+        uint32_t sb;
+        if constexpr (FMT == MOE_FMT_NVFP4) {
+            const float eff = nv.block_scale(amax[i], sb);
+            uint32_t q[2];
+            nv.codes<2>(f, eff, q);
+            if (in) {
+                *reinterpret_cast<uint2*>(a.codes + t * (a.H / 2) + u * 8) = make_uint2(q[0], q[1]);
+                put_sf(u, sb);
+            }
+        } else {
+            const float m = max_or_nan(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], 1));
+            const int e = mx_scale<FMT == MOE_FMT_MXFP8>(m, sb);
+            if constexpr (FMT == MOE_FMT_MXFP8) {
+                const uint2 lo = e4m3_codes(f[0], e), hi = e4m3_codes(f[1], e);
+                if (in) *reinterpret_cast<uint4*>(a.codes + t * a.H + u * 16) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+                const uint2 q = make_uint2(mxfp4_codes(f[0], e), mxfp4_codes(f[1], e));
+                if (in) *reinterpret_cast<uint2*>(a.codes + t * (a.H / 2) + u * 8) = q;
+            }
+            if (in && u % 2 == 0) put_sf(u / 2, sb);
+        }
+    }
+    if (a.atoms)
+        for (int kb = nkb + tid; kb < a.nks * 4 * S; kb += NT) put_sf(kb, 0);
 }
 
 constexpr int NORM_CTA = 128;  // rows of fewer threads share a CTA of about this many
@@ -360,13 +469,37 @@ static cudaError_t norm_pairs(const NormArgs& a, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, norm_pairs_kernel<MAXC, MAXT>, a, (uintptr_t)a.gamma % 16 == 0);
 }
 
-cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
+template <int FMT, int MAXU, int MAXT, int MIN_CTAS>
+static cudaError_t quant_t(const NormArgs& a, cudaStream_t st) {
+    const int64_t threads = align_up(ceil_div(a.H / 16, MAXU), 32), rows = threads >= NORM_CTA ? 1 : NORM_CTA / threads;
+    LaunchAttrs at(true);
+    cudaLaunchConfig_t cfg =
+        at.config(dim3((unsigned)ceil_div(a.T, rows)), dim3((unsigned)threads, (unsigned)rows), 0, st);
+    return cudaLaunchKernelEx(&cfg, quant_kernel<FMT, MAXU, MAXT, MIN_CTAS>, a);
+}
+template <int FMT>
+static cudaError_t quant_f(const NormArgs& a, cudaStream_t st) {
+    if (a.T <= 152 && a.H <= 8192) return quant_t<FMT, 1, 512, 1>(a, st);
+    if (a.H <= 8192) return quant_t<FMT, 4, 128, 8>(a, st);
+    return quant_t<FMT, 4, 256, 4>(a, st);  // H <= 16384
+}
+
+cudaError_t launch_norm(const NormArgs& args, cudaStream_t st) {
+    NormArgs a = args;
+    a.inv_h = 1.0f / (float)a.H;
     // whether the sizes, strides and addresses give every row whole, aligned 16-byte pieces
     uintptr_t bits = (uintptr_t)a.x | (uintptr_t)(2 * a.ldx) | (uintptr_t)(2 * a.H);
     if (a.res) bits |= (uintptr_t)a.res | (uintptr_t)(2 * a.ldr);
     if (a.sum) bits |= (uintptr_t)a.sum | (uintptr_t)(2 * a.lds);
     if (a.out) bits |= (uintptr_t)a.out | (uintptr_t)(2 * a.ldo);
     const bool ragged = bits % 16 != 0;
+    if (!a.gamma && !ragged) {
+        switch (a.fmt) {
+            case MOE_FMT_MXFP8: return quant_f<MOE_FMT_MXFP8>(a, st);
+            case MOE_FMT_NVFP4: return quant_f<MOE_FMT_NVFP4>(a, st);
+            default: return quant_f<MOE_FMT_MXFP4>(a, st);
+        }
+    }
     switch (a.fmt) {
         case MOE_FMT_MXFP8: return ragged ? norm_f<MOE_FMT_MXFP8, true>(a, st) : norm_f<MOE_FMT_MXFP8, false>(a, st);
         case MOE_FMT_NVFP4: return ragged ? norm_f<MOE_FMT_NVFP4, true>(a, st) : norm_f<MOE_FMT_NVFP4, false>(a, st);
