@@ -18,6 +18,9 @@ SF_BLOCK = {"mxfp8": 32, "nvfp4": 16, "mxfp4": 32}
 VALUES_PER_BYTE = {"mxfp8": 1, "nvfp4": 2, "mxfp4": 2}
 LOGITS = {torch.float32: 0, torch.bfloat16: 1}
 
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 P, I32, I64, SZ, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 
 
@@ -78,26 +81,34 @@ def _fail(fn: str, status: int):
 def _stream(stream, t: torch.Tensor) -> int:
     """The given stream, or the current one of t's device (its raw handle: a torch.cuda.Stream
     object costs microseconds to make)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
-def _rows(name: str, t: torch.Tensor, dtype, shape=None):
-    """A 2-D CUDA tensor whose rows are contiguous (any row stride)."""
+def _row_stride(name: str, t: torch.Tensor, dtype, shape) -> int:
+    """The row stride of a 2-D CUDA tensor of this type and shape whose rows are contiguous."""
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(1) != 1 and t.shape[1] > 1 and t.shape[0] > 0:
+    if t.shape != shape or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor of shape {tuple(shape)}, got {tuple(t.shape)} on {t.device}")
+    stride = t.stride()
+    if stride[1] != 1 and shape[1] > 1 and shape[0] > 0:
         raise ValueError(f"{name} must have contiguous rows")
+    return stride[0]
+
+
+def _matrix(name: str, t: torch.Tensor):
+    """The shape of a 2-D tensor."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    return shape
 
 
 def _flat(name: str, t: torch.Tensor, dtype, numel: int):
     """A contiguous CUDA tensor of numel elements."""
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous() or t.numel() != numel:
+    if t.numel() != numel or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor of {numel} elements")
 
 
@@ -130,10 +141,11 @@ class Quantized:
             raise ValueError("NVFP4, and only NVFP4, has a scale per row")
         if row_scale is not None:
             _flat("row_scale", row_scale, torch.float32, rows)
-        self.fmt, self.shape, self.sf_layout = fmt, (rows, K), sf_layout
+        self.fmt, self.shape, self.sf_layout = fmt, torch.Size((rows, K)), sf_layout
         self.codes, self.sf, self.row_scale = codes, sf, row_scale
         self._c = QuantC(FORMATS[fmt], SF_LAYOUTS[sf_layout], codes.data_ptr(), sf.data_ptr(),
                          None if row_scale is None else row_scale.data_ptr())
+        self._ref = byref(self._c)
 
     @classmethod
     def alloc(cls, fmt: str, rows: int, K: int, sf_layout: str = "atoms", device=None) -> "Quantized":
@@ -147,13 +159,14 @@ class Quantized:
 def quantize(x: torch.Tensor, fmt: str, sf_layout: str = "atoms", out: Quantized | None = None,
              stream=None) -> Quantized:
     """moe_quantize: the rows of x (bf16 [rows, K]) in a microscaled format."""
-    _rows("x", x, torch.bfloat16)
+    shape = _matrix("x", x)
+    ldx = _row_stride("x", x, _BF16, shape)
     if out is None:
-        out = Quantized.alloc(fmt, x.shape[0], x.shape[1], sf_layout, x.device)
-    elif out.shape != tuple(x.shape) or out.fmt != fmt:
-        raise ValueError(f"out holds {out.fmt} {out.shape}, x is {tuple(x.shape)} for {fmt}")
-    st = _lib().moe_quantize(x.shape[0], x.shape[1], x.data_ptr(), x.stride(0), byref(out._c), _stream(stream, x))
-    if st != MOE_OK:
+        out = Quantized.alloc(fmt, shape[0], shape[1], sf_layout, x.device)
+    elif out.shape != shape or out.fmt != fmt:
+        raise ValueError(f"out holds {out.fmt} {out.shape}, x is {tuple(shape)} for {fmt}")
+    st = (_fns or _lib()).moe_quantize(shape[0], shape[1], x.data_ptr(), ldx, out._ref, _stream(stream, x))
+    if st:
         _fail("moe_quantize", st)
     return out
 
@@ -166,28 +179,30 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residua
     x, residual, sum_out (receives z), out (receives y): bf16 [rows, H]; gamma: fp32 [H];
     quantized: receives y in its format. Without out and quantized, out is allocated.
     Returns out if there is one, else quantized."""
-    _rows("x", x, torch.bfloat16)
-    shape = x.shape
+    shape = _matrix("x", x)
     rows, H = shape
-    _flat("gamma", gamma, torch.float32, H)
-    if out is None:
-        if quantized is None:
-            out = torch.empty((rows, H), dtype=torch.bfloat16, device=x.device)
-    else:
-        _rows("out", out, torch.bfloat16, shape)
+    ldx = _row_stride("x", x, _BF16, shape)
+    _flat("gamma", gamma, _F32, H)
+    if out is None and quantized is None:
+        out = torch.empty((rows, H), dtype=_BF16, device=x.device)
+    po = pr = ps = pq = None
+    ldo = ldr = lds = 0
+    if out is not None:
+        ldo = _row_stride("out", out, _BF16, shape)
+        po = out.data_ptr()
     if residual is not None:
-        _rows("residual", residual, torch.bfloat16, shape)
+        ldr = _row_stride("residual", residual, _BF16, shape)
+        pr = residual.data_ptr()
     if sum_out is not None:
-        _rows("sum_out", sum_out, torch.bfloat16, shape)
-    if quantized is not None and quantized.shape != (rows, H):
-        raise ValueError(f"quantized holds {quantized.shape}, x is {tuple(shape)}")
-    st = _lib().moe_add_rmsnorm(
-        rows, H, x.data_ptr(), x.stride(0), None if residual is None else residual.data_ptr(),
-        0 if residual is None else residual.stride(0), gamma.data_ptr(), eps,
-        None if sum_out is None else sum_out.data_ptr(), 0 if sum_out is None else sum_out.stride(0),
-        None if out is None else out.data_ptr(), 0 if out is None else out.stride(0),
-        None if quantized is None else byref(quantized._c), _stream(stream, x))
-    if st != MOE_OK:
+        lds = _row_stride("sum_out", sum_out, _BF16, shape)
+        ps = sum_out.data_ptr()
+    if quantized is not None:
+        if quantized.shape != shape:
+            raise ValueError(f"quantized holds {quantized.shape}, x is {tuple(shape)}")
+        pq = quantized._ref
+    st = (_fns or _lib()).moe_add_rmsnorm(rows, H, x.data_ptr(), ldx, pr, ldr, gamma.data_ptr(), eps, ps, lds, po, ldo,
+                                          pq, _raw_stream(x.get_device()) if stream is None else stream.cuda_stream)
+    if st:
         _fail("moe_add_rmsnorm", st)
     return out if out is not None else quantized
 
@@ -202,18 +217,35 @@ class RouterConfig:
     balance_coef: float = 0.0
 
 
-@dataclass
 class RouterOutput:
     """Buffers of one Router.forward: topk_ids int32 [T, k] (-1: no expert), topk_weights fp32
     [T, k], counts int32 [E], num_valid int32 [1] and, when training, prob_mean fp32 [E] and
-    loss fp32 [1]."""
-    topk_ids: torch.Tensor
-    topk_weights: torch.Tensor
-    counts: torch.Tensor | None
-    num_valid: torch.Tensor | None
-    prob_mean: torch.Tensor | None
-    loss: torch.Tensor | None
-    workspace: torch.Tensor
+    loss fp32 [1]; workspace uint8. counts, num_valid, prob_mean and loss may be None."""
+
+    def __init__(self, topk_ids: torch.Tensor, topk_weights: torch.Tensor, counts: torch.Tensor | None,
+                 num_valid: torch.Tensor | None, prob_mean: torch.Tensor | None, loss: torch.Tensor | None,
+                 workspace: torch.Tensor):
+        self.topk_ids, self.topk_weights, self.counts, self.num_valid = topk_ids, topk_weights, counts, num_valid
+        self.prob_mean, self.loss, self.workspace = prob_mean, loss, workspace
+
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__["_args"] = None  # checked again by the next forward
+
+    def _check(self, T: int, E: int, k: int):
+        """The library's arguments for T tokens, after checks that hold until a buffer is replaced."""
+        _flat("topk_ids", self.topk_ids, _I32, T * k)
+        _flat("topk_weights", self.topk_weights, _F32, T * k)
+        for name, dtype, n in (("counts", _I32, E), ("num_valid", _I32, 1), ("prob_mean", _F32, E), ("loss", _F32, 1)):
+            t = getattr(self, name)
+            if t is not None:
+                _flat(name, t, dtype, n)
+        if self.workspace.dtype is not _U8 or not self.workspace.is_cuda or not self.workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
+        ptr = [None if t is None else t.data_ptr() for t in
+               (self.topk_ids, self.topk_weights, self.counts, self.num_valid, self.prob_mean, self.loss,
+                self.workspace)]
+        self.__dict__["_args"] = (T, E, k, (*ptr, self.workspace.numel()))
 
 
 class Router:
@@ -224,6 +256,7 @@ class Router:
         self.cfg = cfg
         self._c = {d: RouterConfigC(cfg.num_experts, cfg.top_k, 1 if cfg.renormalize else 0, code, cfg.balance_coef)
                    for d, code in LOGITS.items()}
+        self._ref = {d: byref(c) for d, c in self._c.items()}
         n = SZ()
         st = _lib().moe_router_workspace_size(byref(self._c[torch.float32]), 0, byref(n))
         if st != MOE_OK:
@@ -248,38 +281,35 @@ class Router:
             empty(max(self.workspace_size(T), 1), dtype=torch.uint8, device=device))
 
     def _inputs(self, logits: torch.Tensor, token_mask: torch.Tensor | None):
-        if logits.dtype not in LOGITS:
-            raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
-        _rows("logits", logits, logits.dtype)
-        if logits.shape[1] != self.cfg.num_experts:
-            raise ValueError(f"logits must be [T, {self.cfg.num_experts}], got {tuple(logits.shape)}")
-        if token_mask is not None:
-            if token_mask.dtype not in (torch.bool, torch.uint8):
-                raise ValueError("token_mask must be bool or uint8")
-            _flat("token_mask", token_mask, token_mask.dtype, logits.shape[0])
+        """Number of tokens, the logits' row stride and the mask's address."""
+        shape = _matrix("logits", logits)
+        dtype = logits.dtype
+        if dtype not in LOGITS:
+            raise ValueError(f"logits must be float32 or bfloat16, got {dtype}")
+        ld = _row_stride("logits", logits, dtype, shape)
+        if shape[1] != self.cfg.num_experts:
+            raise ValueError(f"logits must be [T, {self.cfg.num_experts}], got {tuple(shape)}")
+        if token_mask is None:
+            return shape[0], ld, None
+        if token_mask.dtype not in (torch.bool, _U8):
+            raise ValueError("token_mask must be bool or uint8")
+        _flat("token_mask", token_mask, token_mask.dtype, shape[0])
+        return shape[0], ld, token_mask.data_ptr()
 
     def forward(self, logits: torch.Tensor, token_mask: torch.Tensor | None = None, out: RouterOutput | None = None,
                 training: bool = False, stream=None) -> RouterOutput:
         """logits fp32 or bf16 [T, E]; token_mask bool [T] (False: padding). With out, its buffers
         are written (prob_mean and loss when it has them); else they are allocated."""
-        self._inputs(logits, token_mask)
-        T, E, k = logits.shape[0], self.cfg.num_experts, self.cfg.top_k
+        T, ld, mask = self._inputs(logits, token_mask)
+        E, k = self.cfg.num_experts, self.cfg.top_k
         o = self.alloc(T, training, logits.device) if out is None else out
-        if out is not None:
-            _flat("topk_ids", o.topk_ids, torch.int32, T * k)
-            _flat("topk_weights", o.topk_weights, torch.float32, T * k)
-            for name, dtype, n in (("counts", torch.int32, E), ("num_valid", torch.int32, 1),
-                                   ("prob_mean", torch.float32, E), ("loss", torch.float32, 1)):
-                t = getattr(o, name)
-                if t is not None:
-                    _flat(name, t, dtype, n)
-        st = _lib().moe_router_forward(
-            byref(self._c[logits.dtype]), T, logits.data_ptr(), logits.stride(0),
-            None if token_mask is None else token_mask.data_ptr(), o.topk_ids.data_ptr(), o.topk_weights.data_ptr(),
-            None if o.counts is None else o.counts.data_ptr(), None if o.num_valid is None else o.num_valid.data_ptr(),
-            None if o.prob_mean is None else o.prob_mean.data_ptr(), None if o.loss is None else o.loss.data_ptr(),
-            o.workspace.data_ptr(), o.workspace.numel(), _stream(stream, logits))
-        if st != MOE_OK:
+        args = o._args
+        if args is None or args[0] != T or args[1] != E or args[2] != k:
+            o._check(T, E, k)
+            args = o._args
+        st = _fns.moe_router_forward(self._ref[logits.dtype], T, logits.data_ptr(), ld, mask, *args[3],
+                                     _raw_stream(logits.get_device()) if stream is None else stream.cuda_stream)
+        if st:
             _fail("moe_router_forward", st)
         return o
 
@@ -289,28 +319,27 @@ class Router:
                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The gradient of sum(d_weights * topk_weights) + d_loss * loss with respect to logits
         (counts held constant), in the logits' type."""
-        self._inputs(logits, token_mask)
-        T, E, k = logits.shape[0], self.cfg.num_experts, self.cfg.top_k
+        T, ld, mask = self._inputs(logits, token_mask)
+        E, k = self.cfg.num_experts, self.cfg.top_k
         if out is None:
             out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-        else:
-            _rows("out", out, logits.dtype, logits.shape)
-        _flat("topk_ids", topk_ids, torch.int32, T * k)
+        ldo = _row_stride("out", out, logits.dtype, logits.shape)
+        _flat("topk_ids", topk_ids, _I32, T * k)
+        pw = pl = pc = pn = None
         if d_weights is not None:
-            _flat("d_weights", d_weights, torch.float32, T * k)
+            _flat("d_weights", d_weights, _F32, T * k)
+            pw = d_weights.data_ptr()
         if d_loss is not None:
-            _flat("d_loss", d_loss, torch.float32, 1)
             if counts is None or num_valid is None:
                 raise ValueError("the loss's gradient needs counts and num_valid")
-            _flat("counts", counts, torch.int32, E)
-            _flat("num_valid", num_valid, torch.int32, 1)
-        st = _lib().moe_router_backward(
-            byref(self._c[logits.dtype]), T, logits.data_ptr(), logits.stride(0),
-            None if token_mask is None else token_mask.data_ptr(), topk_ids.data_ptr(),
-            None if counts is None else counts.data_ptr(), None if num_valid is None else num_valid.data_ptr(),
-            None if d_weights is None else d_weights.data_ptr(), None if d_loss is None else d_loss.data_ptr(),
-            out.data_ptr(), out.stride(0), _stream(stream, logits))
-        if st != MOE_OK:
+            _flat("d_loss", d_loss, _F32, 1)
+            _flat("counts", counts, _I32, E)
+            _flat("num_valid", num_valid, _I32, 1)
+            pl, pc, pn = d_loss.data_ptr(), counts.data_ptr(), num_valid.data_ptr()
+        st = _fns.moe_router_backward(self._ref[logits.dtype], T, logits.data_ptr(), ld, mask, topk_ids.data_ptr(), pc,
+                                      pn, pw, pl, out.data_ptr(), ldo,
+                                      _raw_stream(out.get_device()) if stream is None else stream.cuda_stream)
+        if st:
             _fail("moe_router_backward", st)
         return out
 
@@ -339,6 +368,7 @@ class LinearWeight:
         self.codes, self.sf, self.global_scale = codes, sf, global_scale
         self._c = LinearWeightC(codes.data_ptr(), sf.data_ptr(),
                                 None if global_scale is None else global_scale.data_ptr())
+        self._ref = byref(self._c)
 
 
 class LinearPlan:
@@ -394,29 +424,29 @@ class LinearPlan:
                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x: bf16 [T, K] (quantised by the call) or a Quantized with scales in atoms; out bf16 [T, N]."""
         c = self.cfg
-        quantized = isinstance(x, Quantized)
-        T, K = x.shape
-        if K != c.in_features:
-            raise ValueError(f"x must be [T, {c.in_features}], got {tuple(x.shape)}")
+        N = c.out_features
+        quantized = type(x) is Quantized
+        shape = x.shape if quantized else _matrix("x", x)
+        T = shape[0]
+        if shape[1] != c.in_features:
+            raise ValueError(f"x must be [T, {c.in_features}], got {tuple(shape)}")
         if not quantized:
-            _rows("x", x, torch.bfloat16)
+            ldx = _row_stride("x", x, _BF16, shape)
         if out is None:
-            out = torch.empty((T, c.out_features), dtype=torch.bfloat16, device=weight.codes.device)
-        else:
-            _rows("out", out, torch.bfloat16, (T, c.out_features))
+            out = torch.empty((T, N), dtype=_BF16, device=weight.codes.device)
+        ldo = _row_stride("out", out, _BF16, (T, N))
         if workspace is None:
             workspace = self.alloc_workspace(T, out.device)
-        elif not workspace.is_cuda or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        elif not workspace.is_cuda or workspace.dtype is not _U8 or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
-        L = _lib()
+        s = _raw_stream(out.get_device()) if stream is None else stream.cuda_stream
         if quantized:
-            st = L.moe_linear_forward_quantized(self._h, T, byref(x._c), byref(weight._c), out.data_ptr(),
-                                                out.stride(0), workspace.data_ptr(), workspace.numel(),
-                                                _stream(stream, out))
+            st = _fns.moe_linear_forward_quantized(self._h, T, x._ref, weight._ref, out.data_ptr(), ldo,
+                                                   workspace.data_ptr(), workspace.numel(), s)
         else:
-            st = L.moe_linear_forward(self._h, T, x.data_ptr(), x.stride(0), byref(weight._c), out.data_ptr(),
-                                      out.stride(0), workspace.data_ptr(), workspace.numel(), _stream(stream, out))
-        if st != MOE_OK:
+            st = _fns.moe_linear_forward(self._h, T, x.data_ptr(), ldx, weight._ref, out.data_ptr(), ldo,
+                                         workspace.data_ptr(), workspace.numel(), s)
+        if st:
             _fail("moe_linear_forward", st)
         return out
 

@@ -271,7 +271,8 @@ int moe_router_workspace_size(const moe_router_config_t* cfg, int32_t num_tokens
     if (v != MOE_OK) return v;
     if (!bytes || num_tokens < 0) return MOE_ERR_INVALID_ARG;
     const int64_t g = router_grid(num_tokens);
-    *bytes = (size_t)(2 * align_up(4 * g * cfg->num_experts, 256) + align_up(4 * g, 256));
+    const int64_t need = 2 * align_up(4 * g * cfg->num_experts, 256) + align_up(4 * g, 256);
+    *bytes = (size_t)(need > 256 ? need : 256);  // never none: one rule for every size
     return MOE_OK;
 }
 
@@ -309,8 +310,8 @@ int moe_router_forward(const moe_router_config_t* cfg, int32_t num_tokens, const
     if (counts || num_valid || a.want_probs) {
         size_t need = 0;
         moe_router_workspace_size(cfg, T, &need);
-        if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
-        if ((need > 0 && !workspace) || !aligned_to(workspace, 256)) return MOE_ERR_INVALID_ARG;
+        if (workspace && workspace_bytes < need) return MOE_ERR_WORKSPACE;
+        if (!workspace || !aligned_to(workspace, 256)) return MOE_ERR_INVALID_ARG;
         const int64_t part = align_up(4 * (int64_t)router_grid(T) * E, 256);
         uint8_t* ws = (uint8_t*)workspace;
         a.part_counts = (int32_t*)ws;
