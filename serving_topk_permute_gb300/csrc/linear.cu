@@ -7,13 +7,22 @@
 //
 //   linear_pair_kernel   many tiles: persistent CTA pairs (cta_group::2), 256 features x 256
 //                        tokens a tile, each CTA staging its 128 weight rows and half of the
-//                        tokens
+//                        tokens: a third less operand traffic for each SM than single CTAs with
+//                        128 x 256 tiles, which L2 could not feed
 //   linear_split_kernel  few tiles (decode, small layers): 128 features x 16 .. 128 tokens a tile,
 //                        K split over the CTAs of a cluster, which add their accumulators
 //                        through distributed shared memory in rank order
 //
-// A K stage is 128 bytes of codes of each row with their scale atoms. Every wait is bounded;
-// a CTA that gives up reports MOE_ERR_TIMEOUT and still waits for its own copies and MMAs.
+// A K stage is 128 bytes of codes of each row with their scale atoms: 4 MMAs, 512 cycles of the
+// tensor pipe in every format. Every wait is bounded; a CTA that gives up reports
+// MOE_ERR_TIMEOUT and still waits for its own copies and MMAs.
+//
+// Measured on GB300: 4096 x 8192 x 4096 MXFP8 in 79 us (3.5 PFLOP/s, twice the chip's sustained bf16
+// rate: power-bound; 2.2 PFLOP/s before the issuing loops ran converged), 8192 x 7168 x 7168 NVFP4 in
+// 123 us (6.8 PFLOP/s) after 30 us of quantisation; with every operand load taken out it takes 113.
+// One token through 4096 x 7168 NVFP4: 5.6 us (16.5 MB of weights, 2.4 us at the copy rate), 128
+// tokens through 7168 x 4096: 9.9 us. There the fixed steps count: 1 us to set up, 1 us until the first stage
+// has landed, 0.2 to 0.3 us to issue each stage (8 scale copies, 4 MMAs), 2 us for the sums.
 #include "block.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -755,7 +764,8 @@ cudaError_t launch_pack_linear_sf(const uint8_t* src, uint8_t* dst, int fmt, int
 }
 
 // ------------------------------------------------------------------ host side
-// Pairs from one tile for each of them on. Below, K is split in powers of two (clusters of 3 or 5 find
+// Pairs once their tiles fill two fifths of them (1024 x 4096 x 4096 MXFP8, 64 tiles: 21.2 us, split kernel
+// 24.3; 256 x 4096 x 8192, 16 tiles: 24.6, split kernel 17.9). Below, K is split in powers of two (clusters of 3 or 5 find
 // fewer places: 300 x 2048 x 4096 NVFP4 13.5 us in threes, 12.0 in fours) over at most one CTA for
 // each SM: 128 x 7168 x 4096 NVFP4 9.9 us, 11.7 with up to two; 333 x 4100 x 2080 MXFP4 9.5 us, 11.0
 // with up to two. With few tokens and long slices the MMA thread's issue bounds a CTA, and two on
@@ -763,7 +773,7 @@ cudaError_t launch_pack_linear_sf(const uint8_t* src, uint8_t* dst, int fmt, int
 LinearShape linear_shape(int M, int N, int nks, int num_sms) {
     LinearShape s{};
     const int64_t pairs = num_sms / 2;
-    if (M > 128 && ceil_div(M, 256) * ceil_div(N, 256) >= pairs) {
+    if (M > 128 && 5 * ceil_div(M, 256) * ceil_div(N, 256) >= 2 * pairs) {
         s.bt = 256;  // splits = 0
         return s;
     }
