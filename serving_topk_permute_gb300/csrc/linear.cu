@@ -422,7 +422,7 @@ struct SplitCfg {
     static constexpr int COLS = BT + STAGES * SF_COLS;
     static constexpr int TMEM = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static_assert(COLS <= (DEEP ? 512 : 256), "tensor memory budget");
-    static_assert(STAGES >= 3, "shared memory budget");
+    static_assert(STAGES >= 3 && (!DEEP || SMEM + 8 * BT <= 232448), "shared memory budget");
     static_assert(OWN_SUMS || STAGES * STAGE_BYTES >= SUM_BYTES, "the ring holds the sums");
 };
 
@@ -674,7 +674,28 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP 
     } else {
         cluster_sync();
     }
-    if (warp >= 2) {
+    // Without a split the accumulators are stored from the registers, a lane its feature of each token
+    // (600 x 2048 x 2048 NVFP4 7.8 us, through shared memory 9.3).
+    if (warp >= 2 && splits == 1) {
+        const int q = warp % 4, n = nt * BM + q * 32 + lane;
+        const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16);
+        constexpr int STEP = BT >= 32 ? 32 : 16;
+#pragma unroll 1
+        for (int c0 = (warp - 2) / 4 * STEP; c0 < tokens; c0 += 2 * STEP) {
+            float v[32];
+            tmem_ld32(tacc + c0, v);  // for BT = 16 the upper columns hold scales: not kept
+            tmem_ld_wait();
+            if (n < p.N && complete) {
+                __nv_bfloat16* o = p.out + (int64_t)(tt * BT + c0) * p.ldo + n;
+#pragma unroll
+                for (int j = 0; j < STEP; ++j) {
+                    if (c0 + j < tokens) *o = __float2bfloat16_rn(FMT == MOE_FMT_NVFP4 ? v[j] * s_alpha[c0 + j] : v[j]);
+                    o += p.ldo;
+                }
+            }
+        }
+        tc_fence_before();
+    } else if (warp >= 2) {
         const int q = warp % 4;
         const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16);
         const uint32_t mine = smem_u32(sums + (int)rank * per_rank * BM + q * 32 + lane);
@@ -698,12 +719,9 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP 
         }
         tc_fence_before();
     }
-    if (splits > 1)
-        cluster_sync();
-    else
-        __syncthreads();
+    if (splits > 1) cluster_sync();
     // This CTA's tokens: a warp takes a token, a lane 4 features, the ranks added in order.
-    if (warp >= 2 && complete) {
+    if (warp >= 2 && complete && splits > 1) {
         const int n = nt * BM + 4 * lane, first = (int)rank * per_rank, count = min(per_rank, tokens - first);
         __nv_bfloat16* out = p.out + (int64_t)(tt * BT + first) * p.ldo + n;
         const bool whole = n + 4 <= p.N && ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(2 * p.ldo)) & 7) == 0;
@@ -764,8 +782,8 @@ cudaError_t launch_pack_linear_sf(const uint8_t* src, uint8_t* dst, int fmt, int
 }
 
 // ------------------------------------------------------------------ host side
-// Pairs once their tiles fill two fifths of them (1024 x 4096 x 4096 MXFP8, 64 tiles: 21.2 us, split kernel
-// 24.3; 256 x 4096 x 8192, 16 tiles: 24.6, split kernel 17.9). Below, K is split in powers of two (clusters of 3 or 5 find
+// Pairs once their tiles fill half of them (1024 x 4096 x 4096 MXFP8, 64 tiles: 21.2 us, split kernel 24.3;
+// 333 x 4100 x 2080 MXFP4, 34 tiles: 9.9, split kernel 9.4; 256 x 4096 x 8192, 16 tiles: 24.6 and 17.9). Below, K is split in powers of two (clusters of 3 or 5 find
 // fewer places: 300 x 2048 x 4096 NVFP4 13.5 us in threes, 12.0 in fours) over at most one CTA for
 // each SM: 128 x 7168 x 4096 NVFP4 9.9 us, 11.7 with up to two; 333 x 4100 x 2080 MXFP4 9.5 us, 11.0
 // with up to two. With few tokens and long slices the MMA thread's issue bounds a CTA, and two on
@@ -773,7 +791,7 @@ cudaError_t launch_pack_linear_sf(const uint8_t* src, uint8_t* dst, int fmt, int
 LinearShape linear_shape(int M, int N, int nks, int num_sms) {
     LinearShape s{};
     const int64_t pairs = num_sms / 2;
-    if (M > 128 && 5 * ceil_div(M, 256) * ceil_div(N, 256) >= 2 * pairs) {
+    if (M > 128 && 2 * ceil_div(M, 256) * ceil_div(N, 256) >= pairs) {
         s.bt = 256;  // splits = 0
         return s;
     }

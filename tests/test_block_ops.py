@@ -648,3 +648,31 @@ def test_linear_wait_limit_reports_and_the_context_survives(pkg):
     got = plan.forward(x, kw, workspace=ws)
     assert plan.last_status(ws) == 0
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt,M,N,K", [("nvfp4", 1, 1024, 8192), ("mxfp8", 3, 520, 4096), ("mxfp4", 40, 2048, 7168),
+                                       ("mxfp8", 700, 4104, 2048), ("nvfp4", 600, 8200, 1056)])
+def test_linear_wait_limit_in_every_kernel(pkg, fmt, M, N, K):
+    """The same for a product that quantises x itself, split ones and CTA pairs."""
+    plan, kw, x, _ = linear_case(pkg, fmt, M, N, K)
+    ws = plan.alloc_workspace(M)
+    want = plan.forward(x, kw, workspace=ws).clone()
+    assert plan.last_status(ws) == 0
+    plan.set_wait_timeout(1)
+    plan.forward(x, kw, workspace=ws)
+    assert plan.last_status(ws) == 7
+    plan.set_wait_timeout(0)
+    got = plan.forward(x, kw, workspace=ws)
+    assert plan.last_status(ws) == 0
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(256, 7960, 96), (300, 8192, 288), (1025, 2100, 1056), (2000, 1031, 64)])
+def test_linear_on_cta_pairs(pkg, fmt, M, N, K):
+    """Sizes whose 256 x 256 tiles go to CTA pairs, with part-full last tiles on every side."""
+    plan, kw, x, wd = linear_case(pkg, fmt, M, N, K)
+    got = plan.forward(x, kw)
+    check_linear(got, x, wd, fmt, f"{M}x{N}x{K}")
+    got2 = plan.forward(pkg.quantize(x, fmt), kw)
+    assert torch.equal(got.view(torch.int16), got2.view(torch.int16))
