@@ -67,7 +67,7 @@ struct RouterGradArgs {
     void* dlogits;
     int64_t ldd;
 };
-int router_grid(int T);  // CTAs that leave partial sums in the workspace
+int router_grid(int T, int E);  // CTAs that leave partial sums in the workspace
 cudaError_t launch_router(const RouterArgs& a, cudaStream_t st);
 cudaError_t launch_router_grad(const RouterGradArgs& a, cudaStream_t st);
 

@@ -270,7 +270,7 @@ int moe_router_workspace_size(const moe_router_config_t* cfg, int32_t num_tokens
     const int v = check_router(cfg);
     if (v != MOE_OK) return v;
     if (!bytes || num_tokens < 0) return MOE_ERR_INVALID_ARG;
-    const int64_t g = router_grid(num_tokens);
+    const int64_t g = router_grid(num_tokens, cfg->num_experts);
     const int64_t need = 2 * align_up(4 * g * cfg->num_experts, 256) + align_up(4 * g, 256);
     *bytes = (size_t)(need > 256 ? need : 256);  // never none: one rule for every size
     return MOE_OK;
@@ -312,7 +312,7 @@ int moe_router_forward(const moe_router_config_t* cfg, int32_t num_tokens, const
         moe_router_workspace_size(cfg, T, &need);
         if (workspace && workspace_bytes < need) return MOE_ERR_WORKSPACE;
         if (!workspace || !aligned_to(workspace, 256)) return MOE_ERR_INVALID_ARG;
-        const int64_t part = align_up(4 * (int64_t)router_grid(T) * E, 256);
+        const int64_t part = align_up(4 * (int64_t)router_grid(T, E) * E, 256);
         uint8_t* ws = (uint8_t*)workspace;
         a.part_counts = (int32_t*)ws;
         a.part_probs = (float*)(ws + part);

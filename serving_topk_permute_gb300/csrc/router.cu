@@ -9,30 +9,46 @@
 // One warp per token row, C experts in each lane.
 //
 // Selection: a logit becomes an order-preserving 32-bit key whose low 9 bits hold 511 - id, so
-// that keys are unique and the larger key is the larger logit, then the lower id. The next
-// pick is the largest key below the last one, m: max over (key - m) mod 2^32, because keys
-// below m wrap to values above all others; one add-max instruction for each expert, one warp
-// reduction. bf16 logits fit the upper 23 bits. fp32 logits lose their last 9 bits there, so the
-// picked logits' exact order is checked (and mended) among themselves, and one more pick tells
-// whether the k-th and the next agree in the upper 23 bits. Such a row, or one with a NaN or
-// +inf, takes the exact way instead: k rounds on full 32-bit keys.
+// that keys are unique and the larger key is the larger logit, then the lower id. Each lane
+// finds the two largest of its C keys; a pick is the warp's maximum of the lanes' largest, and
+// the lane that held it moves its second one up. Only a lane that is picked from a third time
+// looks through its keys again, for the largest below the pick m: max over (key - m) mod 2^32,
+// because keys below m wrap to values above all others. bf16 logits fit the upper 23 bits. fp32
+// logits lose their last 9 bits there: one pick more is made, and neighbours in the order that
+// agree in the upper 23 bits are put in order by their full logits, or, if they are the k-th
+// and the next, the row takes the exact way, as one with a NaN or +inf does: k rounds on
+// full 32-bit keys.
 //
 // Column sums: each warp sums its rows' probabilities in registers, the warps of a CTA join in a
 // fixed order, then the CTAs: small batches run as one cluster, which joins through distributed
 // shared memory, larger ones leave partial sums to a second kernel of one cluster. No floating
 // atomics: every sum has a fixed order.
+//
+// Measured on GB300, 256 experts, fp32, the 8 largest. 32,768 tokens with the loss: 23.4 us, of which 2.5 are the
+// sums' (loss and counts left out: 21.9 with 34,048 tokens, 24.5 with). The bytes would take 5.3 us; instruction issue
+// bounds it: some 410 instructions a row, issued in 63% of the slots. Neither a row's loads one row
+// ahead (23.5 us) nor three CTAs of 40 registers on an SM (28.9) fill more of them. 128 tokens:
+// 4.4 us, a cluster's launch and one row's chain of picks. The gradient of 32,768 tokens: 15.0 us,
+// 4.6 TB/s, 68% of the copy rate: loads that wait for the row before (one row ahead 15.3 to 16.6 us),
+// and issue, 65% of the slots.
 #include "block.h"
 #include "common.cuh"
 #include "kernels.h"
 
 namespace moe {
 
+constexpr int SMS = 152;
 constexpr int ROUTER_WARPS = 16;
 constexpr int ROUTER_THREADS = 32 * ROUTER_WARPS;
-constexpr int ROUTER_MAX_GRID = 152 * 2;
+// CTAs on an SM, the whole grid resident at once. 16 experts a lane: one CTA's registers fill the SM
+// (two of 64 registers, 32,768 x 512 bf16: 33.7 us against 34.2, but 4096 x 512 fp32 11.9 against
+// 10.3).
+constexpr int router_ctas(int E) { return E > 256 ? 1 : 2; }
 constexpr int GRAD_WARPS = 8;
 constexpr int GRAD_THREADS = 32 * GRAD_WARPS;
-constexpr int GRAD_MAX_GRID = 152 * 5;
+// The gradient's: 32,768 x 256 fp32 15.0 us with five, 17.1 with four, 15.1 with six; 32,768 x 512
+// bf16 20.6 with four, 22.2 with five, 22.5 with three, 29.1 with two.
+constexpr int grad_ctas(int C) { return C > 8 ? 4 : 5; }
 constexpr int JOIN_CTAS = 8;
 constexpr int JOIN_THREADS = 1024;
 // Up to this many tokens run as one cluster of at most 8 CTAs of 16 warps, joined in place.
@@ -144,12 +160,14 @@ struct Lanes {
     }
 };
 
-// e^x and a / b to 2 ulp; results below 2^-126 are flushed to zero
-__device__ __forceinline__ float fast_exp(float x) {
+// 2^x, e^x and a / b to 2 ulp; results below 2^-126 are flushed to zero
+constexpr float LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float fast_exp2(float x) {
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float fast_exp(float x) { return fast_exp2(x * LOG2E); }
 __device__ __forceinline__ float fast_div(float a, float b) { return __fdividef(a, b); }
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
@@ -161,6 +179,16 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// both sums: the lower 16 lanes add the first one up, the upper ones the second
+__device__ __forceinline__ void warp_sums(float& a, float& b, int lane) {
+    const bool upper = lane >= 16;
+    float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    a = __shfl_sync(0xffffffffu, v, 0);
+    b = __shfl_sync(0xffffffffu, v, 16);
 }
 
 // The row's largest logit; NaN when the row holds a NaN.
@@ -205,25 +233,31 @@ __device__ __noinline__ void select_exact(const void* logits, int64_t row, int E
 
 constexpr uint32_t PACKED_INF = 0xFF800000u & ~ID_BITS;  // packed keys from here on: +inf or NaN
 
-// The row's packed keys, and the largest of them.
+// The row's packed keys, and the largest two of the lane's (0: none).
 template <bool BF16, int C, int MODE>
-__device__ __forceinline__ uint32_t pack_keys(const float (&v)[C], int E, int lane, uint32_t (&key)[C]) {
+__device__ __forceinline__ void pack_keys(const float (&v)[C], int E, int lane, uint32_t (&key)[C], uint32_t& h1,
+                                          uint32_t& h2) {
     using L = Lanes<BF16, C, MODE>;
-    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int e = L::expert(lane, i);
         key[i] = L::FULL || e < E ? (order_key(v[i]) & ~ID_BITS) | (ID_BITS - (uint32_t)e) : 0u;
-        m = max(m, key[i]);
     }
-    return __reduce_max_sync(0xffffffffu, m);
+    h1 = max(key[0], key[1]);
+    h2 = min(key[0], key[1]);
+#pragma unroll
+    for (int i = 2; i < C; i += 2) {
+        const uint32_t hi = max(key[i], key[i + 1]), lo = min(key[i], key[i + 1]);
+        h2 = __vimax3_u32(min(h1, hi), h2, lo);
+        h1 = max(h1, hi);
+    }
 }
 
-// Ids and logits of the row's top k, slot j in lane j (id -1: none), from its packed keys and
-// the largest of them, m.
+// Ids and logits of the row's top k, slot j in lane j (id -1: none), from its packed keys, the
+// lanes' largest two and the largest of all, m.
 template <bool BF16, int C, int MODE>
-__device__ __forceinline__ void select(const RouterArgs& a, int64_t row, const uint32_t (&key)[C], uint32_t m,
-                                       int lane, int& id, float& l) {
+__device__ __forceinline__ void select(const RouterArgs& a, int64_t row, const uint32_t (&key)[C], uint32_t h1,
+                                       uint32_t h2, uint32_t m, int lane, int& id, float& l) {
     id = -1;
     l = 0.0f;
     if (m >= PACKED_INF) {
@@ -231,34 +265,38 @@ __device__ __forceinline__ void select(const RouterArgs& a, int64_t row, const u
         return;
     }
     uint32_t mine = 0;
+    const int last = BF16 ? a.k - 1 : a.k;  // fp32: one pick more
+#pragma unroll 4
     for (int j = 0;; ++j) {
-        if (lane == j) mine = m;
-        if (j + 1 == a.k) break;
-        uint32_t d = 0;
+        mine = lane == j ? m : mine;
+        if (j == last) break;
+        const bool held = h1 == m;
+        h1 = held ? h2 : h1;
+        h2 = held ? 0 : h2;
+        if constexpr (C > 2) {
+            if (__any_sync(0xffffffffu, held && h1 == 0)) {  // its third, or it has no more
+                uint32_t d = 0;
 #pragma unroll
-        for (int i = 0; i < C; ++i) d = __viaddmax_u32(key[i], 0u - m, d);
-        m += __reduce_max_sync(0xffffffffu, d);
+                for (int i = 0; i < C; ++i) d = __viaddmax_u32(key[i], 0u - m, d);
+                d = m + d < m ? m + d : 0;
+                h1 = held ? d : h1;
+            }
+        }
+        m = __reduce_max_sync(0xffffffffu, h1);
     }
-    if (lane < a.k && mine >= PACKED_FINITE) {
-        id = (int)(ID_BITS - (mine & ID_BITS));
-        l = logit_at<BF16>(a.logits, row + id);
-    }
+    const bool got = lane < a.k && mine >= PACKED_FINITE;
+    id = got ? (int)(ID_BITS - (mine & ID_BITS)) : -1;
+    if (got) l = logit_at<BF16>(a.logits, row + id);
     if constexpr (!BF16) {
-        // the pick after the k-th; one that does not exist gives a key above m, or 0
-        uint32_t d = 0;
-#pragma unroll
-        for (int i = 0; i < C; ++i) d = __viaddmax_u32(key[i], 0u - m, d);
-        const uint32_t next = m + __reduce_max_sync(0xffffffffu, d);
-        if (next < m && next >= PACKED_FINITE && ((next ^ m) & ~ID_BITS) == 0) {  // warp-uniform
+        uint32_t after = __shfl_down_sync(0xffffffffu, mine, 1);
+        if (lane == 31) after = m;  // k = 32: the pick past the last lane's
+        const uint32_t equal =
+            __ballot_sync(0xffffffffu, id >= 0 && after >= PACKED_FINITE && ((after ^ mine) & ~ID_BITS) == 0);
+        if (equal >> (a.k - 1)) {  // warp-uniform
             id = -1;
             select_exact<BF16, C, MODE>(a.logits, row, a.E, a.k, lane, id, l);
-            return;
-        }
-        const uint32_t full = id >= 0 ? order_key(l) : 0u;
-        const uint32_t after = __shfl_down_sync(0xffffffffu, full, 1);
-        const int id_after = __shfl_down_sync(0xffffffffu, id, 1);
-        const bool wrong = lane + 1 < a.k && (after > full || (after == full && id_after < id && id_after >= 0));
-        if (__any_sync(0xffffffffu, wrong)) {
+        } else if (equal) {
+            const uint32_t full = id >= 0 ? order_key(l) : 0u;
             int rank = 0;  // slots that come before mine
             for (int j = 0; j < a.k; ++j) {
                 const uint32_t f = __shfl_sync(0xffffffffu, full, j);
@@ -292,34 +330,43 @@ __device__ __forceinline__ void route_rows(const RouterArgs& a, int* s_counts, f
         L::load(a.logits, t * a.ld, a.E, lane, v);
         const bool masked = a.mask && a.mask[t] == 0;
         uint32_t key[C];
-        const uint32_t m = pack_keys<BF16, C, MODE>(v, a.E, lane, key);
+        uint32_t h1, h2;
+        pack_keys<BF16, C, MODE>(v, a.E, lane, key, h1, h2);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, h1);
         int id = -1;
         float w = 0.0f;
         if (!masked && m >= PACKED_FINITE) {  // warp-uniform
             ++valid_rows;
             // Any value near the largest logit serves as the exponent's offset. The largest key's
             // upper bits are within 2^-14 of it; only for huge logits is that not near enough.
-            float top = key_value(m & ~ID_BITS);
-            if (!(fabsf(top) < 4096.0f)) top = row_max<C>(v);
+            // These are subtracted first; the others' offset enters with the factor log2(e), its
+            // rounding the same for the whole row.
+            float top = key_value(m & ~ID_BITS), huge = 0.0f;
+            if (!(fabsf(top) < 4096.0f)) {
+                huge = row_max<C>(v);
+                top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < C; ++i) v[i] -= huge;
+            }
+            const float offset = -LOG2E * top;
             float l;
-            select<BF16, C, MODE>(a, t * a.ld, key, m, lane, id, l);
-            float sum = 0.0f;
+            select<BF16, C, MODE>(a, t * a.ld, key, h1, h2, m, lane, id, l);
+            w = id >= 0 ? fast_exp2(fmaf(l - huge, LOG2E, offset)) : 0.0f;
+            float sum = 0.0f, picked = w;
             if (a.want_probs || !a.renorm) {
 #pragma unroll
                 for (int i = 0; i < C; ++i) {
-                    v[i] = fast_exp(v[i] - top);  // 0 for -inf
+                    v[i] = fast_exp2(fmaf(v[i], LOG2E, offset));  // 0 for -inf
                     sum += v[i];
                 }
-                sum = warp_sum(sum);
             }
+            warp_sums(sum, picked, lane);
             if (a.want_probs) {
                 const float inv = fast_div(1.0f, sum);
 #pragma unroll
                 for (int i = 0; i < C; ++i) psum[i] = fmaf(v[i], inv, psum[i]);
             }
-            w = id >= 0 ? fast_exp(l - top) : 0.0f;
-            if (a.renorm) sum = warp_sum(w);
-            w = id >= 0 ? fast_div(w, sum) : 0.0f;
+            w = id >= 0 ? fast_div(w, a.renorm ? picked : sum) : 0.0f;
             if (id >= 0) atomicAdd(&s_counts[id], 1);
         }
         if (lane < a.k) {
@@ -401,7 +448,7 @@ __device__ __forceinline__ void cluster_loss(const RouterArgs& a, float term, in
 
 // Larger batches: partial sums of each CTA to memory, joined by router_join_kernel.
 template <bool BF16, int C, int MODE>
-__global__ void __launch_bounds__(ROUTER_THREADS, C <= 8 ? 2 : 1) router_kernel(const RouterArgs a) {
+__global__ void __launch_bounds__(ROUTER_THREADS, router_ctas(32 * C)) router_kernel(const RouterArgs a) {
     extern __shared__ int s_dyn[];
     int* s_counts = s_dyn;                                   // [E]
     float* s_probs = reinterpret_cast<float*>(s_dyn + a.E);  // [warps][E] when probabilities are summed
@@ -521,7 +568,7 @@ __global__ void __launch_bounds__(32 * CLUSTER_WARPS) router_cluster_kernel(cons
 // The gradient: dense part p_e (base_e - dot) for every expert, then the selected experts, whose
 // g holds dw' too, written over it by the lanes that hold the slots.
 template <bool BF16, int C, int MODE>
-__global__ void __launch_bounds__(GRAD_THREADS, C <= 8 ? 5 : 2) router_grad_kernel(const RouterGradArgs a) {
+__global__ void __launch_bounds__(GRAD_THREADS, grad_ctas(C)) router_grad_kernel(const RouterGradArgs a) {
     using L = Lanes<BF16, C, MODE>;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const float inf = __int_as_float(0x7F800000);
@@ -610,15 +657,15 @@ static bool router_joins(const RouterArgs& a) { return a.counts || a.num_valid |
 
 // CTAs that leave partial sums (0: one cluster does everything). A fixed function of the
 // sizes, so that sums keep their order.
-int router_grid(int T) {
+int router_grid(int T, int E) {
     if (T <= CLUSTER_TOKENS) return 0;
-    const int64_t g = ceil_div(T, ROUTER_WARPS);
-    return (int)(g < ROUTER_MAX_GRID ? g : ROUTER_MAX_GRID);
+    const int64_t g = ceil_div(T, ROUTER_WARPS), most = SMS * router_ctas(E);
+    return (int)(g < most ? g : most);
 }
 
 template <bool BF16, int C, int MODE>
 static cudaError_t router_t(const RouterArgs& a, cudaStream_t st) {
-    const int grid = router_grid(a.T);
+    const int grid = router_grid(a.T, a.E);
     if (grid == 0) {
         const int64_t want = ceil_div(a.T, CLUSTER_WARPS);
         const int ctas = want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
@@ -641,10 +688,9 @@ static cudaError_t router_t(const RouterArgs& a, cudaStream_t st) {
 
 template <bool BF16, int C, int MODE>
 static cudaError_t router_grad_t(const RouterGradArgs& a, cudaStream_t st) {
-    const int64_t g = ceil_div(a.T, GRAD_WARPS);
+    const int64_t g = ceil_div(a.T, GRAD_WARPS), most = SMS * grad_ctas(C);
     LaunchAttrs at(true);
-    cudaLaunchConfig_t cfg =
-        at.config(dim3((unsigned)(g < GRAD_MAX_GRID ? g : GRAD_MAX_GRID)), dim3(GRAD_THREADS), 0, st);
+    cudaLaunchConfig_t cfg = at.config(dim3((unsigned)(g < most ? g : most)), dim3(GRAD_THREADS), 0, st);
     return cudaLaunchKernelEx(&cfg, router_grad_kernel<BF16, C, MODE>, a);
 }
 
