@@ -424,7 +424,7 @@ typedef struct moe_router_config {
     float   balance_coef;    /* finite */
 } moe_router_config_t;
 
-/* Bytes of the workspace of moe_router_forward for num_tokens tokens. Host-only. */
+/* Bytes of the workspace of moe_router_forward for num_tokens tokens (never 0). Host-only. */
 int moe_router_workspace_size(const moe_router_config_t* cfg, int32_t num_tokens, size_t* bytes);
 
 /*
@@ -442,7 +442,8 @@ int moe_router_forward(const moe_router_config_t* cfg, int32_t num_tokens, const
 
 /*
  * d_logits [T, E] (stride d_logits_stride) of  sum(d_weights * topk_weights) + d_loss * loss.
- *   topk_ids, counts, num_valid   as moe_router_forward wrote them (counts are constants of the loss)
+ *   topk_ids, counts, num_valid   as moe_router_forward wrote them (a row's ids are distinct or -1; an
+ *                                 id outside [-1, E) counts as -1; counts are constants of the loss)
  *   d_weights   fp32 [T, k] or NULL (no gradient through the weights)
  *   d_loss      fp32 [1] on the device or NULL (no gradient through the loss; counts and num_valid
  *               may then be NULL)

@@ -782,12 +782,12 @@ cudaError_t launch_pack_linear_sf(const uint8_t* src, uint8_t* dst, int fmt, int
 }
 
 // ------------------------------------------------------------------ host side
-// Pairs once their tiles fill half of them (1024 x 4096 x 4096 MXFP8, 64 tiles: 21.2 us, split kernel 24.3;
-// 333 x 4100 x 2080 MXFP4, 34 tiles: 9.9, split kernel 9.4; 256 x 4096 x 8192, 16 tiles: 24.6 and 17.9). Below, K is split in powers of two (clusters of 3 or 5 find
-// fewer places: 300 x 2048 x 4096 NVFP4 13.5 us in threes, 12.0 in fours) over at most one CTA for
-// each SM: 128 x 7168 x 4096 NVFP4 9.9 us, 11.7 with up to two; 333 x 4100 x 2080 MXFP4 9.5 us, 11.0
-// with up to two. With few tokens and long slices the MMA thread's issue bounds a CTA, and two on
-// an SM are faster: 1 x 7168 x 7168 MXFP8 11.8 us against 13.9.
+// Pairs once their tiles fill half of them (1024 x 4096 x 4096 MXFP8, 64 tiles: 21.2 us, split kernel
+// 24.3; 256 x 4096 x 8192, 16 tiles: 24.6 and 17.9). Below, K is split in powers of two (clusters of
+// 3 or 5 find fewer places: 300 x 2048 x 4096 NVFP4 13.5 us in threes, 12.0 in fours) over at most
+// one CTA for each SM: 128 x 7168 x 4096 NVFP4 9.9 us, 11.7 with up to two. With few tokens and long
+// slices the MMA warp's issue bounds a CTA, and two on an SM are faster: 1 x 7168 x 7168 MXFP8
+// 11.8 us against 13.9.
 LinearShape linear_shape(int M, int N, int nks, int num_sms) {
     LinearShape s{};
     const int64_t pairs = num_sms / 2;
@@ -820,23 +820,22 @@ bool linear_quantises(int fmt, const LinearShape& s, int M, int nks, const void*
            ((uintptr_t)x | (uintptr_t)(2 * ldx)) % 16 == 0;
 }
 
-template <int FMT, int BT, bool QUANT>
+template <int FMT, int BT, bool QUANT, bool DEEP>
 static cudaError_t split_attr() {
-    const cudaError_t e = cudaFuncSetAttribute(linear_split_kernel<FMT, BT, QUANT, true>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               SplitCfg<FMT, BT, QUANT, true>::SMEM);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(linear_split_kernel<FMT, BT, QUANT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                SplitCfg<FMT, BT, QUANT, false>::SMEM);
+    return cudaFuncSetAttribute(linear_split_kernel<FMT, BT, QUANT, DEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                SplitCfg<FMT, BT, QUANT, DEEP>::SMEM);
 }
 template <int FMT>
 static cudaError_t lin_attr() {
     cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          PairCfg<FMT>::SMEM);
-    if (e == cudaSuccess) e = split_attr<FMT, 16, true>();
-    if (e == cudaSuccess) e = split_attr<FMT, 16, false>();
-    if (e == cudaSuccess) e = split_attr<FMT, 64, false>();
-    if (e == cudaSuccess) e = split_attr<FMT, 128, false>();
+    if (e == cudaSuccess) e = split_attr<FMT, 16, true, false>();
+    if (e == cudaSuccess) e = split_attr<FMT, 16, false, false>();
+    if (e == cudaSuccess) e = split_attr<FMT, 16, false, true>();
+    if (e == cudaSuccess) e = split_attr<FMT, 64, false, false>();
+    if (e == cudaSuccess) e = split_attr<FMT, 64, false, true>();
+    if (e == cudaSuccess) e = split_attr<FMT, 128, false, false>();
+    if (e == cudaSuccess) e = split_attr<FMT, 128, false, true>();
     return e;
 }
 cudaError_t linear_prepare(int fmt) {
@@ -855,9 +854,9 @@ static cudaError_t split_d(const LinearMaps& m, const LinearArgs& p, int splits,
                                        dim3(C::THREADS), C::SMEM, st);
     return cudaLaunchKernelEx(&cfg, linear_split_kernel<FMT, BT, QUANT, DEEP>, m.w, m.x, p);
 }
-template <int FMT, int BT, bool QUANT = false>
+template <int FMT, int BT>
 static cudaError_t split_t(const LinearMaps& m, const LinearArgs& p, const LinearShape& s, cudaStream_t st) {
-    return s.deep ? split_d<FMT, BT, QUANT, true>(m, p, s.splits, st) : split_d<FMT, BT, QUANT, false>(m, p, s.splits, st);
+    return s.deep ? split_d<FMT, BT, false, true>(m, p, s.splits, st) : split_d<FMT, BT, false, false>(m, p, s.splits, st);
 }
 
 template <int FMT>
