@@ -6,6 +6,7 @@ the library's CUDA kernels, on the current stream unless one is given.
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 from ctypes import byref
 from dataclasses import dataclass
 
@@ -84,6 +85,12 @@ def _stream(stream, t: torch.Tensor) -> int:
     return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
+def _on(stream):
+    """Where a call allocates what it was not given: memory that is freed then goes back to the
+    stream that uses it."""
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _row_stride(name: str, t: torch.Tensor, dtype, shape) -> int:
     """The row stride of a 2-D CUDA tensor of this type and shape whose rows are contiguous."""
     if t.dtype is not dtype:
@@ -123,9 +130,16 @@ def sf_size(fmt: str, sf_layout: str, rows: int, K: int) -> int:
     return n.value
 
 
+def _set_once(self, name, value):
+    if name in self.__dict__:
+        raise AttributeError(f"{type(self).__name__}.{name} cannot be replaced: make a new one")
+    self.__dict__[name] = value
+
+
 class Quantized:
     """Quantised rows: codes [rows, K / values per byte], block scales and, for NVFP4, one fp32
-    scale per row (moe_quant_t). Codes and scales are byte tensors (uint8 or a float8 type)."""
+    scale per row (moe_quant_t). Codes and scales are byte tensors (uint8 or a float8 type). The
+    tensors cannot be replaced afterwards."""
 
     def __init__(self, fmt: str, shape, codes: torch.Tensor, sf: torch.Tensor, row_scale: torch.Tensor | None,
                  sf_layout: str = "rows"):
@@ -147,6 +161,8 @@ class Quantized:
                          None if row_scale is None else row_scale.data_ptr())
         self._ref = byref(self._c)
 
+    __setattr__ = _set_once
+
     @classmethod
     def alloc(cls, fmt: str, rows: int, K: int, sf_layout: str = "atoms", device=None) -> "Quantized":
         device = device or torch.device("cuda", torch.cuda.current_device())
@@ -162,7 +178,8 @@ def quantize(x: torch.Tensor, fmt: str, sf_layout: str = "atoms", out: Quantized
     shape = _matrix("x", x)
     ldx = _row_stride("x", x, _BF16, shape)
     if out is None:
-        out = Quantized.alloc(fmt, shape[0], shape[1], sf_layout, x.device)
+        with _on(stream):
+            out = Quantized.alloc(fmt, shape[0], shape[1], sf_layout, x.device)
     elif out.shape != shape or out.fmt != fmt:
         raise ValueError(f"out holds {out.fmt} {out.shape}, x is {tuple(shape)} for {fmt}")
     st = (_fns or _lib()).moe_quantize(shape[0], shape[1], x.data_ptr(), ldx, out._ref, _stream(stream, x))
@@ -184,7 +201,8 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residua
     ldx = _row_stride("x", x, _BF16, shape)
     _flat("gamma", gamma, _F32, H)
     if out is None and quantized is None:
-        out = torch.empty((rows, H), dtype=_BF16, device=x.device)
+        with _on(stream):
+            out = torch.empty((rows, H), dtype=_BF16, device=x.device)
     po = pr = ps = pq = None
     ldo = ldr = lds = 0
     if out is not None:
@@ -220,7 +238,8 @@ class RouterConfig:
 class RouterOutput:
     """Buffers of one Router.forward: topk_ids int32 [T, k] (-1: no expert), topk_weights fp32
     [T, k], counts int32 [E], num_valid int32 [1] and, when training, prob_mean fp32 [E] and
-    loss fp32 [1]; workspace uint8. counts, num_valid, prob_mean and loss may be None."""
+    loss fp32 [1]; workspace uint8. counts, num_valid, prob_mean and loss may be None. A buffer is
+    replaced by assigning another tensor."""
 
     def __init__(self, topk_ids: torch.Tensor, topk_weights: torch.Tensor, counts: torch.Tensor | None,
                  num_valid: torch.Tensor | None, prob_mean: torch.Tensor | None, loss: torch.Tensor | None,
@@ -302,7 +321,10 @@ class Router:
         are written (prob_mean and loss when it has them); else they are allocated."""
         T, ld, mask = self._inputs(logits, token_mask)
         E, k = self.cfg.num_experts, self.cfg.top_k
-        o = self.alloc(T, training, logits.device) if out is None else out
+        if out is None:
+            with _on(stream):
+                out = self.alloc(T, training, logits.device)
+        o = out
         args = o._args
         if args is None or args[0] != T or args[1] != E or args[2] != k:
             o._check(T, E, k)
@@ -322,7 +344,8 @@ class Router:
         T, ld, mask = self._inputs(logits, token_mask)
         E, k = self.cfg.num_experts, self.cfg.top_k
         if out is None:
-            out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+            with _on(stream):
+                out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
         ldo = _row_stride("out", out, logits.dtype, logits.shape)
         _flat("topk_ids", topk_ids, _I32, T * k)
         pw = pl = pc = pn = None
@@ -362,7 +385,9 @@ def linear_validate(cfg: LinearConfig) -> int:
 
 
 class LinearWeight:
-    """A weight in the kernel layout (LinearPlan.transform_weight)."""
+    """A weight in the kernel layout (LinearPlan.transform_weight). Its tensors cannot be replaced."""
+
+    __setattr__ = _set_once
 
     def __init__(self, codes: torch.Tensor, sf: torch.Tensor, global_scale: torch.Tensor | None):
         self.codes, self.sf, self.global_scale = codes, sf, global_scale
@@ -413,7 +438,8 @@ class LinearPlan:
         st = _lib().moe_linear_weight_sf_size(self._h, byref(n))
         if st != MOE_OK:
             _fail("moe_linear_weight_sf_size", st)
-        dst = LinearWeight(codes, torch.empty(n.value, dtype=torch.uint8, device=codes.device), global_scale)
+        with _on(stream):
+            dst = LinearWeight(codes, torch.empty(n.value, dtype=torch.uint8, device=codes.device), global_scale)
         src = LinearWeightC(codes.data_ptr(), sf.data_ptr(), None if global_scale is None else global_scale.data_ptr())
         st = _lib().moe_linear_transform_weight(self._h, byref(src), byref(dst._c), _stream(stream, codes))
         if st != MOE_OK:
@@ -433,10 +459,12 @@ class LinearPlan:
         if not quantized:
             ldx = _row_stride("x", x, _BF16, shape)
         if out is None:
-            out = torch.empty((T, N), dtype=_BF16, device=weight.codes.device)
+            with _on(stream):
+                out = torch.empty((T, N), dtype=_BF16, device=weight.codes.device)
         ldo = _row_stride("out", out, _BF16, (T, N))
         if workspace is None:
-            workspace = self.alloc_workspace(T, out.device)
+            with _on(stream):
+                workspace = self.alloc_workspace(T, out.device)
         elif not workspace.is_cuda or workspace.dtype is not _U8 or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
         s = _raw_stream(out.get_device()) if stream is None else stream.cuda_stream
