@@ -811,12 +811,14 @@ LinearShape linear_shape(int M, int N, int nks, int num_sms) {
     return s;
 }
 
-// Whether the product can quantise x itself: few tokens, x's stages within the kernel's area,
-// aligned rows. Every CTA then quantises its slice; with 16 tokens that took longer than the
-// separate pass (16 x 7168 x 7168 MXFP4 10.6 against 7.5 us), with up to 4 it saves a launch.
-constexpr int QUANT_TOKENS = 4;
+// Whether the product quantises x itself: few tokens, x's stages within the kernel's area, aligned
+// rows. It saves a launch, but every CTA then quantises its slice, and for NVFP4 reads the whole
+// rows for their scales. Measured with N = 4096, in the product against separately: MXFP4 8 x 4096
+// 4.7 and 5.4 us, 8 x 7168 both 6.35, 12 x 7168 7.2 and 6.4; MXFP8 8 x 7168 7.7 and 8.5, 16 x 7168 9.0 and
+// 8.7; NVFP4 2 x 7168 6.3 and 6.6, 3 x 7168 7.5 and 6.6, 3 x 2048 5.0 and 4.8.
 bool linear_quantises(int fmt, const LinearShape& s, int M, int nks, const void* x, int64_t ldx) {
-    return M <= QUANT_TOKENS && s.bt == 16 && ceil_div(nks, s.splits) <= (fmt == MOE_FMT_MXFP8 ? 16 : 8) &&
+    return M <= (fmt == MOE_FMT_NVFP4 ? 2 : 8) && s.bt == 16 &&
+           ceil_div(nks, s.splits) <= (fmt == MOE_FMT_MXFP8 ? 16 : 8) &&
            ((uintptr_t)x | (uintptr_t)(2 * ldx)) % 16 == 0;
 }
 

@@ -487,6 +487,18 @@ def test_linear(pkg, fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("K", [96, 2048, 7168, 16384])
+@pytest.mark.parametrize("M", [2, 3, 6, 8, 9])
+def test_linear_around_the_counts_that_are_quantised_inside(pkg, fmt, M, K):
+    """From bf16 rows, and from the same rows quantised by quantize(): the same bits on both ways."""
+    plan, kw, x, wd = linear_case(pkg, fmt, M, 392, K)
+    got = plan.forward(x, kw)
+    check_linear(got, x, wd, fmt, f"{M}x392x{K}")
+    rows = plan.forward(pkg.quantize(x, fmt), kw)
+    assert torch.equal(got.view(torch.int16), rows.view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (7, 96, 96), (40, 300, 2080), (200, 1000, 512)])
 def test_linear_from_quantised_rows(pkg, fmt, M, N, K):
     """Quantised input by quantize() or by the norm gives what the bf16 form gives on the same values."""
