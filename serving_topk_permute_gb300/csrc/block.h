@@ -83,6 +83,7 @@ struct LinearArgs {
     __nv_bfloat16* out;
     int64_t ldo;
     int* err;
+    int first;  // no other kernel of this call came before: clear err, read nothing before the wait
     unsigned long long timeout_ns;
 };
 // weight scale atoms [nks][sf_blocks][S][512] from row-major [N, K/g] bytes, zeros past N and K

@@ -135,8 +135,9 @@ LinLayout lin_layout(const moe_linear_config_t& c, int T) {
     return L;
 }
 
-// x: quantised rows, or (codes null) bf16 rows xb that the product quantises itself
-int run_linear(moe_linear_plan_t plan, int T, const moe_quant_t& x, const void* xb, int64_t x_stride,
+// x: quantised rows, or (codes null) bf16 rows xb that the product quantises itself; first: no other
+// kernel of the call comes before
+int run_linear(moe_linear_plan_t plan, int T, const moe_quant_t& x, bool first, const void* xb, int64_t x_stride,
                const moe_linear_weight_t* w, void* out, int64_t out_stride, void* workspace, cudaStream_t st) {
     const moe_linear_config_t& c = plan->cfg;
     const uint64_t row_bytes = (uint64_t)fmt_row_bytes(c.format, c.in_features);
@@ -165,6 +166,7 @@ int run_linear(moe_linear_plan_t plan, int T, const moe_quant_t& x, const void* 
     p.out = (__nv_bfloat16*)out;
     p.ldo = out_stride;
     p.err = (int*)((uint8_t*)workspace + lin_layout(c, T).err);
+    p.first = first;
     p.timeout_ns = plan->timeout_ns;
     CUDA_TRY(launch_linear(c.format, m, p, shape, plan->num_sms, st));
     return MOE_OK;
@@ -440,7 +442,7 @@ int moe_linear_forward(moe_linear_plan_t plan, int32_t num_tokens, const void* x
     const int64_t nks = stages_of(c.format, c.in_features);
     if (linear_quantises(c.format, linear_shape(num_tokens, c.out_features, (int)nks, plan->num_sms),
                          num_tokens, (int)nks, x, x_stride))
-        return run_linear(plan, num_tokens, moe_quant_t{}, x, x_stride, weight, out, out_stride, workspace, st);
+        return run_linear(plan, num_tokens, moe_quant_t{}, true, x, x_stride, weight, out, out_stride, workspace, st);
     const LinLayout L = lin_layout(c, num_tokens);
     NormArgs a{};
     a.x = (const __nv_bfloat16*)x;
@@ -457,7 +459,7 @@ int moe_linear_forward(moe_linear_plan_t plan, int32_t num_tokens, const void* x
     a.n_zero = 1;
     CUDA_TRY(launch_norm(a, st));
     const moe_quant_t q{c.format, MOE_SF_ATOMS, a.codes, a.sf, a.row_scale};
-    return run_linear(plan, num_tokens, q, nullptr, 0, weight, out, out_stride, workspace, st);
+    return run_linear(plan, num_tokens, q, false, nullptr, 0, weight, out, out_stride, workspace, st);
 }
 
 int moe_linear_forward_quantized(moe_linear_plan_t plan, int32_t num_tokens, const moe_quant_t* x,
@@ -468,9 +470,7 @@ int moe_linear_forward_quantized(moe_linear_plan_t plan, int32_t num_tokens, con
     if (!x) return MOE_ERR_INVALID_ARG;
     if ((v = check_quant(x)) != MOE_OK) return v;
     if (x->format != plan->cfg.format || x->sf_layout != MOE_SF_ATOMS) return MOE_ERR_INVALID_ARG;
-    cudaStream_t st = (cudaStream_t)stream;
-    CUDA_TRY(cudaMemsetAsync(workspace, 0, 16, st));  // the error word
-    return run_linear(plan, num_tokens, *x, nullptr, 0, weight, out, out_stride, workspace, st);
+    return run_linear(plan, num_tokens, *x, true, nullptr, 0, weight, out, out_stride, workspace, (cudaStream_t)stream);
 }
 
 int moe_linear_last_status(moe_linear_plan_t plan, void* workspace, void* stream, int32_t* status) {

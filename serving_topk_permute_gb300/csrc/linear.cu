@@ -57,6 +57,11 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r != 0;
 }
+// where the first CTA of this grid clears the word, after the same wait, let it do so first
+__device__ __forceinline__ void report_timeout(const LinearArgs& p) {
+    if (p.first) __nanosleep(100000);
+    set_error(p.err, MOE_ERR_TIMEOUT);
+}
 // a wait of the whole warp: every lane returns the same
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, const volatile int* abort) {
     return __all_sync(0xffffffffu, lin_wait(bar, parity, timeout_ns, abort));
@@ -202,14 +207,15 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
     grid_dep_wait();  // the set-up above overlaps the previous kernel; everything below reads its output
     grid_dep_launch();
+    if (p.first && blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
 
     const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
     const int n_tiles = (p.N + 255) / 256, t_tiles = (p.M + BT - 1) / BT;
     const int total = n_tiles * t_tiles;
 
     auto give_up = [&]() {
-        set_error(p.err, MOE_ERR_TIMEOUT);
         *abort_flag = 1;
+        report_timeout(p);
     };
 
     if (warp == 0) {
@@ -487,11 +493,9 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP 
     if (C::OWN_SUMS && splits > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
     auto give_up = [&]() {
         *abort_flag = 1;
-        // the first CTA of this grid clears the word after the same wait: let it, first
-        if constexpr (QUANT) __nanosleep(100000);
-        set_error(p.err, MOE_ERR_TIMEOUT);
+        report_timeout(p);
     };
-    if constexpr (QUANT) {
+    if (QUANT || p.first) {
         // the predecessor may be any kernel: not even the weights are read before the wait
         grid_dep_wait();
         grid_dep_launch();
@@ -515,8 +519,8 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP 
                 tma_load_2d(st + C::X_PAD, &tmX, full, ks * BK_BYTES, tt * BT);
             }
         };
-        // Without QUANT the previous kernel has quantised x, after a wait of its own for whatever
-        // came before it: the weights, which it does not write, may be read while it runs.
+        // Behind this call's own quantiser, which has waited for whatever came before it, the weights
+        // may be read while it runs.
         const int ahead = min(k1 - k0, STAGES);
         if (elected)
             for (int i = 0; i < ahead; ++i) load_w(k0 + i, i);

@@ -679,6 +679,23 @@ def test_linear_wait_limit_in_every_kernel(pkg, fmt, M, N, K):
     assert torch.equal(got.view(torch.int16), want.view(torch.int16))
 
 
+@pytest.mark.parametrize("fmt,M,N,K", [("nvfp4", 9, 1024, 8192), ("mxfp8", 130, 520, 4096), ("mxfp4", 700, 8200, 1056)])
+def test_linear_wait_limit_from_quantised_rows(pkg, fmt, M, N, K):
+    """The same from quantised rows, where the product's own kernel clears the status first: a
+    workspace's old contents do not matter, and a wait that runs out is still reported."""
+    plan, kw, x, _ = linear_case(pkg, fmt, M, N, K)
+    rows = pkg.quantize(x, fmt)
+    ws = plan.alloc_workspace(M)
+    want = plan.forward(x, kw).clone()
+    for fill, limit, status in ((0xA5, 0, 0), (0x5A, 1, 7), (0xFF, 0, 0)):
+        ws.fill_(fill)
+        plan.set_wait_timeout(limit)
+        got = plan.forward(rows, kw, workspace=ws)
+        assert plan.last_status(ws) == status
+        if status == 0:
+            assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,N,K", [(256, 7960, 96), (300, 8192, 288), (1025, 2100, 1056), (2000, 1031, 64)])
 def test_linear_on_cta_pairs(pkg, fmt, M, N, K):
