@@ -205,13 +205,45 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
     cluster_sync();  // the peer's barriers exist before anyone arrives on them
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    grid_dep_wait();  // the set-up above overlaps the previous kernel; everything below reads its output
-    grid_dep_launch();
-    if (p.first && blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
 
     const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
     const int n_tiles = (p.N + 255) / 256, t_tiles = (p.M + BT - 1) / BT;
-    const int total = n_tiles * t_tiles;
+    const int total = n_tiles * t_tiles;  // at least one for each pair
+
+    // Both CTAs count their bytes on the leader's full barrier: each arrives on it with its own
+    // transaction count (the follower remotely), and its loads complete on it (cta_group::2).
+    const uint32_t full_cl0 = mapa_shared(full0, 0);
+    auto load_w = [&](int nt, int ks, int stage) {
+        const uint32_t st = smem0 + stage * C::STAGE_BYTES, full_cl = full_cl0 + 8 * stage;
+        const int w_blk = 2 * nt + (int)rank;  // this CTA's 128 weight rows
+        if (leader)
+            mbar_arrive_expect_tx(full0 + 8 * stage, C::TX_BYTES);
+        else
+            mbar_arrive_expect_tx_cluster(full_cl, C::TX_BYTES);
+        tma_load_2d_cg2(st, &tmW, full_cl, ks * BK_BYTES, w_blk * BM);
+        tma_load_2d_cg2(st + C::A_BYTES + C::B_BYTES, &tmSFW, full_cl, 0, (ks * p.sf_blocks + w_blk) * S);
+    };
+    auto load_x = [&](int tt, int ks, int stage) {
+        const uint32_t st = smem0 + stage * C::STAGE_BYTES + C::A_BYTES, sf = st + C::B_BYTES + C::SFA_BYTES;
+        const uint32_t full_cl = full_cl0 + 8 * stage;
+        tma_load_2d_cg2(st, &tmX, full_cl, ks * BK_BYTES, (2 * tt + (int)rank) * NBLK);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            tma_load_2d_cg2(sf + b * C::SFA_BYTES, &tmSFX, full_cl, 0, ((NB * tt + b) * p.nks + ks) * S);
+    };
+    // Behind this call's own quantiser, which has waited for whatever came before it, the weights
+    // may be read while it runs: the first ring of them. All else reads its output.
+    const int ahead = min(p.nks, STAGES);
+    int nt0, tt0;
+    raster(pair, n_tiles, t_tiles, nt0, tt0);
+    if (warp == 0 && !p.first) {
+        if (elect_one())
+            for (int i = 0; i < ahead; ++i) load_w(nt0, i, i);
+        __syncwarp();
+    }
+    grid_dep_wait();
+    grid_dep_launch();
+    if (p.first && blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
 
     auto give_up = [&]() {
         *abort_flag = 1;
@@ -219,37 +251,28 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
     };
 
     if (warp == 0) {
-        // Both CTAs count their bytes on the leader's full barrier: each arrives on it with its own
-        // transaction count (the follower remotely), and its loads complete on it (cta_group::2).
         const bool elected = elect_one();
-        const uint32_t full_cl0 = mapa_shared(full0, 0);
-        int stage = 0;
-        uint32_t phase = 0, issued = 0;
+        if (elected)
+            for (int i = 0; i < ahead; ++i) {
+                if (p.first) load_w(nt0, i, i);
+                load_x(tt0, i, i);
+            }
+        __syncwarp();
+        int stage = ahead % STAGES;
+        uint32_t phase = ahead / STAGES, issued = ahead;
         bool ok = true;
         for (int tile = pair; ok && tile < total; tile += npairs) {
             int nt, tt;
             raster(tile, n_tiles, t_tiles, nt, tt);
-            const int w_blk = 2 * nt + (int)rank, x_blk = 2 * tt + (int)rank;  // this CTA's 128-row blocks
-            for (int ks = 0; ks < p.nks; ++ks) {
+            for (int ks = tile == pair ? ahead : 0; ks < p.nks; ++ks) {
                 if (!warp_wait(empty0 + 8 * stage, phase ^ 1, tmo, abort_flag)) {
                     give_up();
                     ok = false;
                     break;
                 }
-                const uint32_t st = smem0 + stage * C::STAGE_BYTES, sf = st + C::A_BYTES + C::B_BYTES;
-                const uint32_t full_cl = full_cl0 + 8 * stage;
                 if (elected) {
-                    if (leader)
-                        mbar_arrive_expect_tx(full0 + 8 * stage, C::TX_BYTES);
-                    else
-                        mbar_arrive_expect_tx_cluster(full_cl, C::TX_BYTES);
-                    tma_load_2d_cg2(st, &tmW, full_cl, ks * BK_BYTES, w_blk * BM);
-                    tma_load_2d_cg2(st + C::A_BYTES, &tmX, full_cl, ks * BK_BYTES, x_blk * NBLK);
-                    tma_load_2d_cg2(sf, &tmSFW, full_cl, 0, (ks * p.sf_blocks + w_blk) * S);
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        tma_load_2d_cg2(sf + (1 + b) * C::SFA_BYTES, &tmSFX, full_cl, 0,
-                                        ((NB * tt + b) * p.nks + ks) * S);
+                    load_w(nt, ks, stage);
+                    load_x(tt, ks, stage);
                 }
                 __syncwarp();
                 ++issued;
@@ -342,15 +365,25 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
         const uint32_t leader_tempty = mapa_shared(tempty_bar, 0);
         uint32_t acc_phase = 0;
         for (int tile = pair; tile < total; tile += npairs) {
+            int nt, tt;
+            raster(tile, n_tiles, t_tiles, nt, tt);
+            const int n = nt * 256 + (int)rank * BM + q * 32 + lane, t0 = tt * BT + cg * COLS;
+            // Of token t0 + 32 c + lane, on its way while the MMAs run, and handed round by shuffles: 256
+            // loads of one word each in the epilogue made it 1 us longer (2048 x 4096 x 4096 23.9 us, 22.2
+            // so). Through shared memory they take less, but 4 KB more of it delay the quantiser of a
+            // call that follows (23.2).
+            float scale[COLS / 32];
+            if constexpr (FMT == MOE_FMT_NVFP4) {
+#pragma unroll
+                for (int c = 0; c < COLS / 32; ++c)
+                    scale[c] = t0 + 32 * c + lane < p.M ? __ldg(p.x_scale + t0 + 32 * c + lane) * __ldg(p.w_scale) : 0.0f;
+            }
             // warp-uniform: every lane leaves together (a lane left behind would block in __syncwarp)
             if (!warp_wait(tfull_bar, acc_phase, tmo, abort_flag)) {
                 give_up();
                 break;
             }
             tc_fence_after();
-            int nt, tt;
-            raster(tile, n_tiles, t_tiles, nt, tt);
-            const int n = nt * 256 + (int)rank * BM + q * 32 + lane, t0 = tt * BT + cg * COLS;
             const uint32_t tacc = tmem_base + ((uint32_t)(q * 32) << 16) + cg * COLS;
             // into registers, then the accumulator is handed back, and only then scaled and stored
             float v[COLS / 32][32];
@@ -366,17 +399,16 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
                     mbar_arrive_cluster(leader_tempty);
             }
             acc_phase ^= 1;
+            if constexpr (FMT == MOE_FMT_NVFP4) {
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) v[j / 32][j % 32] *= __shfl_sync(0xffffffffu, scale[j / 32], j % 32);
+            }
             if (n < p.N) {
-                float ws = 1.0f;
-                if constexpr (FMT == MOE_FMT_NVFP4) ws = __ldg(p.w_scale);
                 __nv_bfloat16* o = p.out + (int64_t)t0 * p.ldo + n;
 #pragma unroll
                 for (int j = 0; j < COLS; ++j) {
-                    if (t0 + j < p.M) {
-                        float y = v[j / 32][j % 32];
-                        if constexpr (FMT == MOE_FMT_NVFP4) y *= __ldg(p.x_scale + t0 + j) * ws;
-                        *o = __float2bfloat16_rn(y);
-                    }
+                    float y = v[j / 32][j % 32];
+                    if (t0 + j < p.M) *o = __float2bfloat16_rn(y);
                     o += p.ldo;
                 }
             }
