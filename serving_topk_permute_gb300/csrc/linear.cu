@@ -17,12 +17,15 @@
 // tensor pipe in every format. Every wait is bounded; a CTA that gives up reports
 // MOE_ERR_TIMEOUT and still waits for its own copies and MMAs.
 //
-// Measured on GB300: 4096 x 8192 x 4096 MXFP8 in 79 us (3.5 PFLOP/s, twice the chip's sustained bf16
+// Measured on GB300: 4096 x 8192 x 4096 MXFP8 in 78 us (3.5 PFLOP/s, twice the chip's sustained bf16
 // rate: power-bound; 2.2 PFLOP/s before the issuing loops ran converged), 8192 x 7168 x 7168 NVFP4 in
-// 123 us (6.8 PFLOP/s) after 30 us of quantisation; with every operand load taken out it takes 113.
+// 123 us (6.8 PFLOP/s) after 28 us of quantisation; with every operand load taken out it takes 113.
+// Where one wave of tiles does it, the fixed steps count: 1024 x 4096 x 4096 NVFP4 9.9 us, of which 0.8
+// until the first stage has landed, 0.3 for each of 16 stages (the MMAs alone 0.27), 0.6 until the
+// last one is through, 1.6 to store a tile and 0.7 to leave.
 // One token through 4096 x 7168 NVFP4: 5.6 us (16.5 MB of weights, 2.4 us at the copy rate), 128
-// tokens through 7168 x 4096: 9.9 us. There the fixed steps count: 1 us to set up, 1 us until the first stage
-// has landed, 0.2 to 0.3 us to issue each stage (8 scale copies, 4 MMAs), 2 us for the sums.
+// tokens through 7168 x 4096: 9.8 us, 8.3 from quantised rows. There 1 us goes to set up, 1 us until the
+// first stage has landed, 0.2 to 0.3 us to issue each stage (8 scale copies, 4 MMAs), 2 us for the sums.
 #include "block.h"
 #include "common.cuh"
 #include "kernels.h"

@@ -16,8 +16,8 @@
 // Memory bounds all of them once there are rows enough. Measured on GB300: 8192 x 7168 with a residual
 // to the sum and MXFP8 64.0 us (6.45 TB/s, 95% of the copy rate); 16 x 7168 2.7 us, the launch and one
 // trip to memory; 2999 x 2050 rows of 4-byte alignment 7.3 us (3.4 TB/s: four times the load and
-// store instructions). Quantisation alone of 8192 x 7168: MXFP8 27.2, MXFP4 23.9, NVFP4 30.0 us (6.6, 6.2 and
-// 5.0 TB/s).
+// store instructions). Quantisation alone of 8192 x 7168: MXFP8 27.2, MXFP4 24.0, NVFP4 28.5 us (6.5, 6.2 and
+// 5.3 TB/s).
 #include "block.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -484,11 +484,18 @@ static cudaError_t quant_t(const NormArgs& a, cudaStream_t st) {
         at.config(dim3((unsigned)ceil_div(a.T, rows)), dim3((unsigned)threads, (unsigned)rows), 0, st);
     return cudaLaunchKernelEx(&cfg, quant_kernel<FMT, MAXU, MAXT, MIN_CTAS>, a);
 }
+// Units per thread: one for few rows, as in the norm. MX formats: two up to 6144 elements (8192 x 2048
+// MXFP8 9.1 us, 9.9 with four), four above (8192 x 7168 27.2 and 27.3, MXFP4 24.0 and 24.6). NVFP4, whose
+// rows wait for their magnitude: four, so that there are fewer warps to join (8192 x 7168 28.5 us, 32.3
+// with two), but two where four would not fill a warp (16384 x 1024 9.8, 11.2 with four); seven CTAs
+// on an SM, as eight of 64 registers spill (29.6).
 template <int FMT>
 static cudaError_t quant_f(const NormArgs& a, cudaStream_t st) {
+    constexpr bool NV = FMT == MOE_FMT_NVFP4;
     if (a.T <= 152 && a.H <= 8192) return quant_t<FMT, 1, 512, 1>(a, st);
-    if (a.H <= 8192) return quant_t<FMT, 4, 128, 8>(a, st);
-    return quant_t<FMT, 4, 256, 4>(a, st);  // H <= 16384
+    if (a.H <= (NV ? 1024 : 6144)) return quant_t<FMT, 2, 256, 5>(a, st);
+    if (a.H <= 8192) return quant_t<FMT, 4, 128, NV ? 7 : 8>(a, st);
+    return quant_t<FMT, 4, 256, NV ? 3 : 4>(a, st);  // H <= 16384
 }
 
 cudaError_t launch_norm(const NormArgs& args, cudaStream_t st) {

@@ -155,6 +155,22 @@ __device__ __forceinline__ float div_by_reciprocal(float a, float b, float y) {
     return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
 }
 
+// Two of them at once, in the packed instructions: v[0] / b and v[1] / b.
+__device__ __forceinline__ float2 div2_by_reciprocal(float v0, float v1, float b, float y) {
+    float2 r;
+    asm("{\n\t.reg .b64 v, b, y, q, e;\n\t"
+        "mov.b64 v, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %4};\n\t"
+        "mov.b64 y, {%5, %5};\n\t"
+        "mul.rn.f32x2 q, v, y;\n\t"
+        "fma.rn.f32x2 e, q, b, v;\n\t"
+        "fma.rn.f32x2 q, e, y, q;\n\t"
+        "mov.b64 {%0, %1}, q;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(v0), "f"(v1), "f"(-b), "f"(y));
+    return r;
+}
+
 // What a row's NVFP4 blocks share.
 struct Nvfp4Row {
     float gs, gs6, inv6;
@@ -180,7 +196,10 @@ struct Nvfp4Row {
             for (int n = 0; n < N; ++n) {
                 float v[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = div_by_reciprocal(f[n][j], eff, y);
+                for (int j = 0; j < 8; j += 2) {
+                    const float2 r = div2_by_reciprocal(f[n][j], f[n][j + 1], eff, y);
+                    v[j] = r.x, v[j + 1] = r.y;
+                }
                 q[n] = e2m1_codes(v);
             }
         } else {
