@@ -824,9 +824,12 @@ cudaError_t launch_pack_linear_sf(const uint8_t* src, uint8_t* dst, int fmt, int
 // Pairs once their tiles fill half of them (1024 x 4096 x 4096 MXFP8, 64 tiles: 21.2 us, split kernel
 // 24.3; 256 x 4096 x 8192, 16 tiles: 24.6 and 17.9). Below, K is split in powers of two (clusters of
 // 3 or 5 find fewer places: 300 x 2048 x 4096 NVFP4 13.5 us in threes, 12.0 in fours) over at most
-// one CTA for each SM: 128 x 7168 x 4096 NVFP4 9.9 us, 11.7 with up to two. With few tokens and long
-// slices the MMA warp's issue bounds a CTA, and two on an SM are faster: 1 x 7168 x 7168 MXFP8
-// 11.8 us against 13.9.
+// one CTA for each SM (128 x 7168 x 4096 NVFP4 in four parts 11.6 us, in one 8.8).
+// A stage takes 0.24 us, the sums of a split tile some 2.7 us with 128 tokens and 1.7 with 64: a split has
+// to save more stages than that (128 x 4096 x 4096: NVFP4, 16 stages, 8.6 us in one part, 9.6 in two,
+// 8.6 in four; MXFP8, 32 stages, 12.1, 10.8 and 9.6). Eight parts pay with 16 tokens alone (128 x 2048 x
+// 7168 NVFP4 11.3 us in eight, 9.1 in four). With few tokens and long slices the MMA warp's issue bounds a
+// CTA, and two on an SM are faster: 1 x 7168 x 7168 MXFP8 11.8 us against 13.9.
 LinearShape linear_shape(int M, int N, int nks, int num_sms) {
     LinearShape s{};
     const int64_t pairs = num_sms / 2;
@@ -835,11 +838,12 @@ LinearShape linear_shape(int M, int N, int nks, int num_sms) {
         return s;
     }
     s.bt = M <= 16 ? 16 : M <= 64 ? 64 : 128;
+    const int max_splits = s.bt == 16 ? MAX_SPLITS : 4, sum_stages = s.bt == 16 ? 0 : s.bt == 64 ? 7 : 11;
     const int64_t tiles = ceil_div(M, s.bt) * ceil_div(N, BM);
     auto most = [&](int64_t slots) {
         int k = 1;
-        while (2 * k <= MAX_SPLITS && tiles * 2 * k <= slots && 4 * k <= nks) k *= 2;
-        return k;
+        while (2 * k <= max_splits && tiles * 2 * k <= slots && 4 * k <= nks) k *= 2;
+        return nks - nks / k > sum_stages ? k : 1;
     };
     s.splits = most(num_sms);
     s.deep = tiles * s.splits <= num_sms && s.splits <= 4;  // clusters of 8 with an SM for each CTA find few places
