@@ -24,8 +24,9 @@
 // until the first stage has landed, 0.3 for each of 16 stages (the MMAs alone 0.27), 0.6 until the
 // last one is through, 1.6 to store a tile and 0.7 to leave.
 // One token through 4096 x 7168 NVFP4: 5.6 us (16.5 MB of weights, 2.4 us at the copy rate), 128
-// tokens through 7168 x 4096: 9.8 us, 8.3 from quantised rows. There 1 us goes to set up, 1 us until the
-// first stage has landed, 0.2 to 0.3 us to issue each stage (8 scale copies, 4 MMAs), 2 us for the sums.
+// tokens through 7168 x 4096: 8.8 us, 7.2 from quantised rows. There 1 us goes to set up, 1 us until the
+// first stage has landed, 0.24 us to each stage (36 KB, 80 bytes a clock), 1.7 to 2.7 us to the sums of
+// split tiles.
 #include "block.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -821,10 +822,11 @@ cudaError_t launch_pack_linear_sf(const uint8_t* src, uint8_t* dst, int fmt, int
 }
 
 // ------------------------------------------------------------------ host side
-// Pairs once their tiles fill half of them (1024 x 4096 x 4096 MXFP8, 64 tiles: 21.2 us, split kernel
-// 24.3; 256 x 4096 x 8192, 16 tiles: 24.6 and 17.9). Below, K is split in powers of two (clusters of
-// 3 or 5 find fewer places: 300 x 2048 x 4096 NVFP4 13.5 us in threes, 12.0 in fours) over at most
-// one CTA for each SM (128 x 7168 x 4096 NVFP4 in four parts 11.6 us, in one 8.8).
+// Pairs once there are more tiles of 128 x 128 than SMs (1024 x 4096 x 4096 MXFP8, 256 of them: 21.2
+// us, split kernel 24.3; 384 x 6400 x 4096, 150: 16.4 and 14.8, NVFP4 12.2 and 11.5). Below, K is
+// split in powers of two (clusters of 3 or 5 find fewer places: 300 x 2048 x 4096 NVFP4 13.5 us in
+// threes, 12.0 in fours) over at most one CTA for each SM (128 x 7168 x 4096 NVFP4 in four parts 11.6 us,
+// in one 8.8).
 // A stage takes 0.24 us, the sums of a split tile some 2.7 us with 128 tokens and 1.7 with 64: a split has
 // to save more stages than that (128 x 4096 x 4096: NVFP4, 16 stages, 8.6 us in one part, 9.6 in two,
 // 8.6 in four; MXFP8, 32 stages, 12.1, 10.8 and 9.6). Eight parts pay with 16 tokens alone (128 x 2048 x
@@ -832,8 +834,7 @@ cudaError_t launch_pack_linear_sf(const uint8_t* src, uint8_t* dst, int fmt, int
 // CTA, and two on an SM are faster: 1 x 7168 x 7168 MXFP8 11.8 us against 13.9.
 LinearShape linear_shape(int M, int N, int nks, int num_sms) {
     LinearShape s{};
-    const int64_t pairs = num_sms / 2;
-    if (M > 128 && 2 * ceil_div(M, 256) * ceil_div(N, 256) >= pairs) {
+    if (M > 128 && ceil_div(M, 128) * ceil_div(N, BM) > num_sms) {
         s.bt = 256;  // splits = 0
         return s;
     }

@@ -697,6 +697,21 @@ def test_linear_wait_limit_from_quantised_rows(pkg, fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(129, 9800, 96), (257, 12900, 64), (513, 4001, 4128), (1920, 1281, 544), (2049, 1031, 64),
+                                   (384, 6400, 1056), (1216, 2048, 2080)])
+def test_linear_past_and_at_one_wave_of_tiles(pkg, fmt, M, N, K):
+    """More tiles of 128 x 128 than the GPU has SMs, just as many and just fewer; even and odd edges."""
+    plan, kw, x, wd = linear_case(pkg, fmt, M, N, K)
+    ws = plan.alloc_workspace(M)
+    ws.fill_(0xA5)
+    got = plan.forward(x, kw, workspace=ws)
+    assert plan.last_status(ws) == 0
+    check_linear(got, x, wd, fmt, f"{M}x{N}x{K}")
+    rows = plan.forward(pkg.quantize(x, fmt), kw)
+    assert torch.equal(got.view(torch.int16), rows.view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,N,K", [(256, 7960, 96), (300, 8192, 288), (1025, 2100, 1056), (2000, 1031, 64)])
 def test_linear_on_cta_pairs(pkg, fmt, M, N, K):
     """Sizes whose 256 x 256 tiles go to CTA pairs, with part-full last tiles on every side."""
