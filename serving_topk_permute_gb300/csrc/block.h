@@ -28,8 +28,6 @@ struct NormArgs {
     uint8_t* codes;
     uint8_t* sf;
     float* row_scale;
-    int* zero;                   // words zeroed by the first CTA (the product's error word and counters)
-    int n_zero;
 };
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
 
@@ -82,8 +80,8 @@ struct LinearArgs {
     const float* w_scale;        // NVFP4: fp32 [1]
     __nv_bfloat16* out;
     int64_t ldo;
-    int* err;
-    int first;  // no other kernel of this call came before: clear err, read nothing before the wait
+    int* status;  // number of CTAs, then a word of each (linear_max_ctas at most)
+    int first;    // no other kernel of this call came before: read nothing before the wait
     unsigned long long timeout_ns;
 };
 // weight scale atoms [nks][sf_blocks][S][512] from row-major [N, K/g] bytes, zeros past N and K
@@ -98,6 +96,7 @@ struct LinearShape {
     int x_box() const { return splits ? bt : 128; }
 };
 LinearShape linear_shape(int M, int N, int nks, int num_sms);
+int linear_max_ctas(int N, int num_sms);
 bool linear_quantises(int fmt, const LinearShape& s, int M, int nks, const void* x, int64_t ldx);
 struct LinearMaps {
     CUtensorMap w, x;      // code rows, boxes of 128 weight rows and of x_box() tokens

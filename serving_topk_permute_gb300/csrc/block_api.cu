@@ -114,11 +114,13 @@ int check_router(const moe_router_config_t* c) {
     return MOE_OK;
 }
 
-// workspace of the product: error word, then the quantised activations
+// workspace of the product: the CTAs' status words at its start (as many for every T), then the
+// quantised activations
 struct LinLayout {
-    int64_t err, codes, sf, scale, total;
+    int64_t codes, sf, scale, total;
 };
-LinLayout lin_layout(const moe_linear_config_t& c, int T) {
+LinLayout lin_layout(const moe_linear_plan_s* plan, int T) {
+    const moe_linear_config_t& c = plan->cfg;
     LinLayout L{};
     const int S = fmt_sf_atoms(c.format);
     int64_t o = 0;
@@ -127,7 +129,7 @@ LinLayout lin_layout(const moe_linear_config_t& c, int T) {
         o += align_up(bytes, REGION_ALIGN);
         return at;
     };
-    L.err = take(16);
+    take(4 * (1 + (int64_t)linear_max_ctas(c.out_features, plan->num_sms)));
     L.codes = take((int64_t)T * fmt_row_bytes(c.format, c.in_features));
     L.sf = take(ceil_div(T, BM) * stages_of(c.format, c.in_features) * S * ATOM_BYTES);
     L.scale = take(c.format == MOE_FMT_NVFP4 ? 4 * (int64_t)T : 0);
@@ -165,7 +167,7 @@ int run_linear(moe_linear_plan_t plan, int T, const moe_quant_t& x, bool first, 
     p.w_scale = w->global_scale;
     p.out = (__nv_bfloat16*)out;
     p.ldo = out_stride;
-    p.err = (int*)((uint8_t*)workspace + lin_layout(c, T).err);
+    p.status = (int*)workspace;
     p.first = first;
     p.timeout_ns = plan->timeout_ns;
     CUDA_TRY(launch_linear(c.format, m, p, shape, plan->num_sms, st));
@@ -184,7 +186,7 @@ int check_forward(moe_linear_plan_t plan, int T, const moe_linear_weight_t* w, c
         !aligned_to(w->global_scale, 4))
         return MOE_ERR_INVALID_ARG;
     if (!rows_ok(out, out_stride, T, c.out_features)) return MOE_ERR_INVALID_ARG;
-    if (workspace_bytes < (size_t)lin_layout(c, T).total) return MOE_ERR_WORKSPACE;
+    if (workspace_bytes < (size_t)lin_layout(plan, T).total) return MOE_ERR_WORKSPACE;
     return MOE_OK;
 }
 
@@ -426,7 +428,7 @@ int moe_linear_transform_weight(moe_linear_plan_t plan, const moe_linear_weight_
 int moe_linear_workspace_size(moe_linear_plan_t plan, int32_t num_tokens, size_t* bytes) {
     if (!plan || !bytes || num_tokens < 0) return MOE_ERR_INVALID_ARG;
     if (num_tokens > plan->cfg.max_tokens) return MOE_ERR_CAPACITY;
-    *bytes = (size_t)lin_layout(plan->cfg, num_tokens).total;
+    *bytes = (size_t)lin_layout(plan, num_tokens).total;
     return MOE_OK;
 }
 
@@ -443,7 +445,7 @@ int moe_linear_forward(moe_linear_plan_t plan, int32_t num_tokens, const void* x
     if (linear_quantises(c.format, linear_shape(num_tokens, c.out_features, (int)nks, plan->num_sms),
                          num_tokens, (int)nks, x, x_stride))
         return run_linear(plan, num_tokens, moe_quant_t{}, true, x, x_stride, weight, out, out_stride, workspace, st);
-    const LinLayout L = lin_layout(c, num_tokens);
+    const LinLayout L = lin_layout(plan, num_tokens);
     NormArgs a{};
     a.x = (const __nv_bfloat16*)x;
     a.ldx = x_stride;
@@ -455,8 +457,6 @@ int moe_linear_forward(moe_linear_plan_t plan, int32_t num_tokens, const void* x
     a.codes = ws + L.codes;
     a.sf = ws + L.sf;
     a.row_scale = c.format == MOE_FMT_NVFP4 ? (float*)(ws + L.scale) : nullptr;
-    a.zero = (int*)(ws + L.err);
-    a.n_zero = 1;
     CUDA_TRY(launch_norm(a, st));
     const moe_quant_t q{c.format, MOE_SF_ATOMS, a.codes, a.sf, a.row_scale};
     return run_linear(plan, num_tokens, q, false, nullptr, 0, weight, out, out_stride, workspace, st);
@@ -476,9 +476,20 @@ int moe_linear_forward_quantized(moe_linear_plan_t plan, int32_t num_tokens, con
 int moe_linear_last_status(moe_linear_plan_t plan, void* workspace, void* stream, int32_t* status) {
     if (!plan || !workspace || !status) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
-    int v = 0;
-    CUDA_TRY(cudaMemcpyAsync(&v, workspace, sizeof(int), cudaMemcpyDeviceToHost, st));
+    // words[0]: how many CTAs the last product had (bounded: before the first one it may be anything)
+    const int most = linear_max_ctas(plan->cfg.out_features, plan->num_sms);
+    const int* words = (const int*)workspace;
+    int ctas = 0, v = MOE_OK;
+    CUDA_TRY(cudaMemcpyAsync(&ctas, words, sizeof(int), cudaMemcpyDeviceToHost, st));
     CUDA_TRY(cudaStreamSynchronize(st));
+    ctas = ctas < 0 || ctas > most ? most : ctas;
+    int part[512];
+    for (int i = 0; i < ctas && v == MOE_OK; i += 512) {
+        const int n = ctas - i < 512 ? ctas - i : 512;
+        CUDA_TRY(cudaMemcpyAsync(part, words + 1 + i, n * sizeof(int), cudaMemcpyDeviceToHost, st));
+        CUDA_TRY(cudaStreamSynchronize(st));
+        for (int j = 0; j < n && v == MOE_OK; ++j) v = part[j];
+    }
     CUDA_TRY(cudaMemsetAsync(workspace, 0, sizeof(int), st));
     CUDA_TRY(cudaStreamSynchronize(st));
     *status = v;

@@ -15,7 +15,9 @@
 //
 // A K stage is 128 bytes of codes of each row with their scale atoms: 4 MMAs, 512 cycles of the
 // tensor pipe in every format. Every wait is bounded; a CTA that gives up reports
-// MOE_ERR_TIMEOUT and still waits for its own copies and MMAs.
+// MOE_ERR_TIMEOUT and still waits for its own copies and MMAs. Each CTA has a status word of its own,
+// which it writes whatever happened, so that no word depends on the order in which CTAs run and the
+// workspace needs no clearing before the launch.
 //
 // Measured on GB300: 4096 x 8192 x 4096 MXFP8 in 78 us (3.5 PFLOP/s, twice the chip's sustained bf16
 // rate: power-bound; 2.2 PFLOP/s before the issuing loops ran converged), 8192 x 7168 x 7168 NVFP4 in
@@ -61,10 +63,11 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r != 0;
 }
-// where the first CTA of this grid clears the word, after the same wait, let it do so first
-__device__ __forceinline__ void report_timeout(const LinearArgs& p) {
-    if (p.first) __nanosleep(100000);
-    set_error(p.err, MOE_ERR_TIMEOUT);
+// One thread of each CTA, after every warp's last wait: status[0] is the number of CTAs, the words
+// after it are theirs.
+__device__ __forceinline__ void write_status(const LinearArgs& p, uint32_t cta, uint32_t ctas, bool gave_up) {
+    if (cta == 0) p.status[0] = (int)ctas;
+    p.status[1 + cta] = gave_up ? MOE_ERR_TIMEOUT : MOE_OK;
 }
 // a wait of the whole warp: every lane returns the same
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, const volatile int* abort) {
@@ -247,12 +250,8 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
     }
     grid_dep_wait();
     grid_dep_launch();
-    if (p.first && blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
 
-    auto give_up = [&]() {
-        *abort_flag = 1;
-        report_timeout(p);
-    };
+    auto give_up = [&]() { *abort_flag = 1; };
 
     if (warp == 0) {
         const bool elected = elect_one();
@@ -419,6 +418,7 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
         }
     }
     __syncthreads();
+    if (threadIdx.x == 0) write_status(p, blockIdx.x, gridDim.x, *abort_flag != 0);
     cluster_sync();  // both CTAs are done with each other's barriers and the MMAs have drained
     if (warp == 1) {
         tc_fence_after();
@@ -527,15 +527,11 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP 
     const uint32_t tmem_base = *tmem_slot;
     // matched just before the first store into another CTA's shared memory: by then it has started
     if (C::OWN_SUMS && splits > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-    auto give_up = [&]() {
-        *abort_flag = 1;
-        report_timeout(p);
-    };
+    auto give_up = [&]() { *abort_flag = 1; };
     if (QUANT || p.first) {
         // the predecessor may be any kernel: not even the weights are read before the wait
         grid_dep_wait();
         grid_dep_launch();
-        if (blockIdx.x == 0 && nt == 0 && tt == 0 && threadIdx.x == 0) *p.err = 0;
     }
 
     bool complete = true;  // meaningful in the epilogue's warps
@@ -791,6 +787,9 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP 
         }
     }
     __syncthreads();
+    if (threadIdx.x == 0)
+        write_status(p, blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z),
+                     gridDim.x * gridDim.y * gridDim.z, *abort_flag != 0);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, C::TMEM);
@@ -853,6 +852,13 @@ LinearShape linear_shape(int M, int N, int nks, int num_sms) {
         s.deep = false;
     }
     return s;
+}
+
+// Most CTAs of a product with N outputs on any number of tokens: pairs fill the SMs once, and tiles of 128
+// features are only multiplied (by K splits or further token tiles) up to two CTAs for each SM.
+int linear_max_ctas(int N, int num_sms) {
+    const int64_t n_tiles = ceil_div(N, BM);
+    return (int)(n_tiles > 2 * num_sms ? n_tiles : 2 * num_sms);
 }
 
 // Whether the product quantises x itself: few tokens, x's stages within the kernel's area, aligned

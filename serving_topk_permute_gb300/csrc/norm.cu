@@ -212,8 +212,6 @@ __global__ void __launch_bounds__(MAXT, MIN_CTAS) norm_kernel(const NormArgs a, 
     const __nv_bfloat16* r = a.res + t * a.ldr;
     grid_dep_wait();
     grid_dep_launch();
-    if (t == 0)
-        for (int i = tid; i < a.n_zero; i += NT) a.zero[i] = 0;
     // every load of the row is under way before the first value is used
     RowLoad<MAXC, RAGGED> xv, rv;
     xv.issue(a.x, a.ldx, t, a.T, H, nchunks, tid, NT);
@@ -321,8 +319,6 @@ __global__ void __launch_bounds__(MAXT, MIN_CTAS) quant_kernel(const NormArgs a)
     const uint4* x = reinterpret_cast<const uint4*>(a.x + t * a.ldx);
     grid_dep_wait();
     grid_dep_launch();
-    if (t == 0)
-        for (int i = tid; i < a.n_zero; i += NT) a.zero[i] = 0;
     uint4 v[MAXU][2];
 #pragma unroll
     for (int i = 0; i < MAXU; ++i) {
