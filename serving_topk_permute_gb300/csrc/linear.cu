@@ -375,11 +375,13 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
             // loads of one word each in the epilogue made it 1 us longer (2048 x 4096 x 4096 23.9 us, 22.2
             // so). Through shared memory they take less, but 4 KB more of it delay the quantiser of a
             // call that follows (23.2).
+            // Plain loads: the quantiser writes the scales while this kernel is resident already, which the
+            // read-only path does not allow.
             float scale[COLS / 32];
             if constexpr (FMT == MOE_FMT_NVFP4) {
 #pragma unroll
                 for (int c = 0; c < COLS / 32; ++c)
-                    scale[c] = t0 + 32 * c + lane < p.M ? __ldg(p.x_scale + t0 + 32 * c + lane) * __ldg(p.w_scale) : 0.0f;
+                    scale[c] = t0 + 32 * c + lane < p.M ? p.x_scale[t0 + 32 * c + lane] * *p.w_scale : 0.0f;
             }
             // warp-uniform: every lane leaves together (a lane left behind would block in __syncwarp)
             if (!warp_wait(tfull_bar, acc_phase, tmo, abort_flag)) {
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP 
         if constexpr (FMT == MOE_FMT_NVFP4) {
             const int c = (int)threadIdx.x - 64;
             if (c < tokens)
-                s_alpha[c] = (QUANT ? nvfp4_row_scale(__uint_as_float(s_amax[c])) : p.x_scale[tt * BT + c]) * __ldg(p.w_scale);
+                s_alpha[c] = (QUANT ? nvfp4_row_scale(__uint_as_float(s_amax[c])) : p.x_scale[tt * BT + c]) * *p.w_scale;
         }
         complete = warp_wait(done_bar, 0, tmo, abort_flag);
         if (!complete) give_up();

@@ -135,15 +135,17 @@ __device__ __forceinline__ void store_ragged(const uint4* s, __nv_bfloat16* row,
     }
 }
 
+// A plain load, as everywhere here: the kernel may be resident while its predecessor still writes gamma,
+// and the read-only path (__ldg) is for data that no one writes during the kernel's whole life.
 __device__ __forceinline__ void load_gamma(float (&g)[8], const float* gamma, int c, int H, bool aligned) {
     const float* p = gamma + 8 * c;
     if (aligned && 8 * c + 8 <= H) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(p)), v = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
         g[0] = u.x, g[1] = u.y, g[2] = u.z, g[3] = u.w;
         g[4] = v.x, g[5] = v.y, g[6] = v.z, g[7] = v.w;
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = 8 * c + j < H ? __ldg(p + j) : 0.0f;
+        for (int j = 0; j < 8; ++j) g[j] = 8 * c + j < H ? p[j] : 0.0f;
     }
 }
 
@@ -453,10 +455,10 @@ __global__ void __launch_bounds__(MAXT) norm_pairs_kernel(const NormArgs a, cons
         if (c < pairs) {
             float g0, g1;
             if (gamma_aligned) {
-                const float2 g = __ldg(reinterpret_cast<const float2*>(a.gamma) + c);
+                const float2 g = reinterpret_cast<const float2*>(a.gamma)[c];
                 g0 = g.x, g1 = g.y;
             } else {
-                g0 = __ldg(a.gamma + 2 * c), g1 = __ldg(a.gamma + 2 * c + 1);
+                g0 = a.gamma[2 * c], g1 = a.gamma[2 * c + 1];
             }
             o[c] = __floats2bfloat162_rn(z[i][0] * scale * g0, z[i][1] * scale * g1);
         }

@@ -72,3 +72,33 @@ def test_tensors_of_a_handle_cannot_be_replaced(pkg):
     kw = plan.transform_weight(wq.codes, wq.sf.view(N, -1))
     with pytest.raises(AttributeError):
         kw.sf = kw.sf.clone()
+
+
+@pytest.mark.parametrize("M", [40, 600])
+def test_scales_of_rows_are_those_of_this_call(pkg, M):
+    """Rows of very different magnitudes back to back through one workspace: each product takes the row
+    scales that its own quantiser wrote, and the norm the gamma that the kernel before it wrote."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    xs = [(torch.randn((M, H), device="cuda", generator=g) * 4.0 ** i).bfloat16() for i in range(-3, 4)]
+    wq = pkg.quantize(torch.randn((8200, H), device="cuda", generator=g).bfloat16(), "nvfp4", "rows")
+    plan = pkg.LinearPlan(pkg.LinearConfig(8200, H, M, "nvfp4"))
+    kw = plan.transform_weight(wq.codes, wq.sf.view(8200, -1), torch.ones(1, device="cuda"))
+    ws = plan.alloc_workspace(M)
+    want = []
+    for x in xs:
+        want.append(plan.forward(x, kw, workspace=ws))
+        torch.cuda.synchronize()
+    for _ in range(10):
+        got = [plan.forward(x, kw, workspace=ws) for x in xs]
+        for a, b in zip(got, want):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    gammas = [torch.rand(H, device="cuda", generator=g) + 0.5 for _ in xs]
+    want = [pkg.add_rmsnorm(x, gm) for x, gm in zip(xs, gammas)]
+    gamma = torch.empty(H, device="cuda")
+    for _ in range(10):
+        got = []
+        for x, gm in zip(xs, gammas):
+            gamma.copy_(gm)
+            got.append(pkg.add_rmsnorm(x, gamma))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
