@@ -155,7 +155,9 @@ __device__ __forceinline__ float div_by_reciprocal(float a, float b, float y) {
     return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
 }
 
-// Two of them at once, in the packed instructions: v[0] / b and v[1] / b.
+// Two of them at once, in the packed instructions: v[0] / b and v[1] / b. The remainder is exact in any
+// rounding mode; rounding it down makes a zero remainder -0, which leaves the quotient -0 of a -0
+// as it is (a remainder of +0 would turn it into +0, another code).
 __device__ __forceinline__ float2 div2_by_reciprocal(float v0, float v1, float b, float y) {
     float2 r;
     asm("{\n\t.reg .b64 v, b, y, q, e;\n\t"
@@ -163,7 +165,7 @@ __device__ __forceinline__ float2 div2_by_reciprocal(float v0, float v1, float b
         "mov.b64 b, {%4, %4};\n\t"
         "mov.b64 y, {%5, %5};\n\t"
         "mul.rn.f32x2 q, v, y;\n\t"
-        "fma.rn.f32x2 e, q, b, v;\n\t"
+        "fma.rm.f32x2 e, q, b, v;\n\t"
         "fma.rn.f32x2 q, e, y, q;\n\t"
         "mov.b64 {%0, %1}, q;\n\t}"
         : "=f"(r.x), "=f"(r.y)
@@ -191,7 +193,7 @@ struct Nvfp4Row {
     template <int N>
     __device__ __forceinline__ void codes(const float (&f)[N][8], float eff, uint32_t (&q)[N]) const {
         if (ordinary && !all_ones(eff)) {
-            const float y = eff > 0.0f ? reciprocal(eff) : 0.0f;  // a zero scale: all codes are zero
+            const float y = reciprocal(eff);
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 float v[8];
@@ -200,7 +202,7 @@ struct Nvfp4Row {
                     const float2 r = div2_by_reciprocal(f[n][j], f[n][j + 1], eff, y);
                     v[j] = r.x, v[j + 1] = r.y;
                 }
-                q[n] = e2m1_codes(v);
+                q[n] = eff > 0.0f ? e2m1_codes(v) : 0u;  // a zero scale: the code zero, without a sign
             }
         } else {
 #pragma unroll
