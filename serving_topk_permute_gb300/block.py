@@ -227,8 +227,9 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residua
 
 # ----------------------------------------------------------------------------- router
 
-@dataclass
+@dataclass(frozen=True)
 class RouterConfig:
+    """What a Router is built for. It cannot be changed: another coefficient or top_k is another Router."""
     num_experts: int
     top_k: int
     renormalize: bool = True
@@ -272,7 +273,8 @@ class Router:
     (moe_router_forward, moe_router_backward)."""
 
     def __init__(self, cfg: RouterConfig):
-        self.cfg = cfg
+        # buffers are checked by what the library was told, whatever becomes of cfg
+        self._cfg, self._E, self._k = cfg, cfg.num_experts, cfg.top_k
         self._c = {d: RouterConfigC(cfg.num_experts, cfg.top_k, 1 if cfg.renormalize else 0, code, cfg.balance_coef)
                    for d, code in LOGITS.items()}
         self._ref = {d: byref(c) for d, c in self._c.items()}
@@ -280,6 +282,10 @@ class Router:
         st = _lib().moe_router_workspace_size(byref(self._c[torch.float32]), 0, byref(n))
         if st != MOE_OK:
             _fail("moe_router_workspace_size", st)
+
+    @property
+    def cfg(self) -> RouterConfig:
+        return self._cfg
 
     def workspace_size(self, num_tokens: int) -> int:
         n = SZ()
@@ -290,7 +296,7 @@ class Router:
 
     def alloc(self, num_tokens: int, training: bool = False, device=None) -> RouterOutput:
         device = device or torch.device("cuda", torch.cuda.current_device())
-        E, k, T = self.cfg.num_experts, self.cfg.top_k, num_tokens
+        E, k, T = self._E, self._k, num_tokens
         empty = torch.empty
         return RouterOutput(
             empty((T, k), dtype=torch.int32, device=device), empty((T, k), dtype=torch.float32, device=device),
@@ -306,8 +312,8 @@ class Router:
         if dtype not in LOGITS:
             raise ValueError(f"logits must be float32 or bfloat16, got {dtype}")
         ld = _row_stride("logits", logits, dtype, shape)
-        if shape[1] != self.cfg.num_experts:
-            raise ValueError(f"logits must be [T, {self.cfg.num_experts}], got {tuple(shape)}")
+        if shape[1] != self._E:
+            raise ValueError(f"logits must be [T, {self._E}], got {tuple(shape)}")
         if token_mask is None:
             return shape[0], ld, None
         if token_mask.dtype not in (torch.bool, _U8):
@@ -320,7 +326,7 @@ class Router:
         """logits fp32 or bf16 [T, E]; token_mask bool [T] (False: padding). With out, its buffers
         are written (prob_mean and loss when it has them); else they are allocated."""
         T, ld, mask = self._inputs(logits, token_mask)
-        E, k = self.cfg.num_experts, self.cfg.top_k
+        E, k = self._E, self._k
         if out is None:
             with _on(stream):
                 out = self.alloc(T, training, logits.device)
@@ -342,7 +348,7 @@ class Router:
         """The gradient of sum(d_weights * topk_weights) + d_loss * loss with respect to logits
         (counts held constant), in the logits' type."""
         T, ld, mask = self._inputs(logits, token_mask)
-        E, k = self.cfg.num_experts, self.cfg.top_k
+        E, k = self._E, self._k
         if out is None:
             with _on(stream):
                 out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
@@ -369,8 +375,9 @@ class Router:
 
 # ----------------------------------------------------------------------------- linear product
 
-@dataclass
+@dataclass(frozen=True)
 class LinearConfig:
+    """What a LinearPlan is built for. It cannot be changed."""
     out_features: int
     in_features: int
     max_tokens: int
@@ -400,7 +407,8 @@ class LinearPlan:
     """out[t, n] = sum_k x[t, k] W[n, k] with x and W in a microscaled format (moe_linear_*)."""
 
     def __init__(self, cfg: LinearConfig):
-        self.cfg = cfg
+        # tensors are checked by what the library was told, whatever becomes of cfg
+        self._cfg, self._N, self._K, self._fmt = cfg, cfg.out_features, cfg.in_features, cfg.fmt
         h = ctypes.c_void_p()
         st = _lib().moe_linear_plan(byref(cfg.to_c()), byref(h))
         if st != MOE_OK:
@@ -411,6 +419,10 @@ class LinearPlan:
         if getattr(self, "_h", None) and _fns is not None:
             _fns.moe_linear_plan_destroy(self._h)
             self._h = None
+
+    @property
+    def cfg(self) -> LinearConfig:
+        return self._cfg
 
     def workspace_size(self, num_tokens: int) -> int:
         n = SZ()
@@ -427,9 +439,8 @@ class LinearPlan:
                          stream=None) -> LinearWeight:
         """Checkpoint codes [N, K / values per byte] and row-major block scales [N, K / g] (bytes), with
         the NVFP4 global scale (fp32 [1]), in the kernel layout. The codes are shared, not copied."""
-        c = self.cfg
-        N, K = c.out_features, c.in_features
-        for name, t, n in (("codes", codes, N * K // VALUES_PER_BYTE[c.fmt]), ("sf", sf, N * K // SF_BLOCK[c.fmt])):
+        N, K, fmt = self._N, self._K, self._fmt
+        for name, t, n in (("codes", codes, N * K // VALUES_PER_BYTE[fmt]), ("sf", sf, N * K // SF_BLOCK[fmt])):
             if t.element_size() != 1 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
                 raise ValueError(f"{name} must be a contiguous CUDA byte tensor of {n} bytes")
         if global_scale is not None:
@@ -449,13 +460,12 @@ class LinearPlan:
     def forward(self, x, weight: LinearWeight, out: torch.Tensor | None = None,
                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x: bf16 [T, K] (quantised by the call) or a Quantized with scales in atoms; out bf16 [T, N]."""
-        c = self.cfg
-        N = c.out_features
+        N = self._N
         quantized = type(x) is Quantized
         shape = x.shape if quantized else _matrix("x", x)
         T = shape[0]
-        if shape[1] != c.in_features:
-            raise ValueError(f"x must be [T, {c.in_features}], got {tuple(shape)}")
+        if shape[1] != self._K:
+            raise ValueError(f"x must be [T, {self._K}], got {tuple(shape)}")
         if not quantized:
             ldx = _row_stride("x", x, _BF16, shape)
         if out is None:
