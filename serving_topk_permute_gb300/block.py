@@ -392,12 +392,22 @@ def linear_validate(cfg: LinearConfig) -> int:
 
 
 class LinearWeight:
-    """A weight in the kernel layout (LinearPlan.transform_weight). Its tensors cannot be replaced."""
+    """A weight in the kernel layout (LinearPlan.transform_weight): codes, scale atoms (both bytes) and, for
+    NVFP4, the global scale; the format and the shape [N, K] that they were laid out for, where that is
+    known. Its tensors cannot be replaced."""
 
     __setattr__ = _set_once
 
-    def __init__(self, codes: torch.Tensor, sf: torch.Tensor, global_scale: torch.Tensor | None):
+    def __init__(self, codes: torch.Tensor, sf: torch.Tensor, global_scale: torch.Tensor | None,
+                 fmt: str | None = None, shape=None):
+        for name, t in (("codes", codes), ("sf", sf)):
+            if t.element_size() != 1 or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous CUDA byte tensor")
+        if global_scale is not None:
+            _flat("global_scale", global_scale, _F32, 1)
         self.codes, self.sf, self.global_scale = codes, sf, global_scale
+        self.fmt, self.shape = fmt, None if shape is None else tuple(shape)
+        self._bytes = (codes.numel(), sf.numel(), global_scale is not None)
         self._c = LinearWeightC(codes.data_ptr(), sf.data_ptr(),
                                 None if global_scale is None else global_scale.data_ptr())
         self._ref = byref(self._c)
@@ -414,6 +424,12 @@ class LinearPlan:
         if st != MOE_OK:
             _fail("moe_linear_plan", st)
         self._h = h
+        n = SZ()
+        st = _lib().moe_linear_weight_sf_size(h, byref(n))
+        if st != MOE_OK:
+            _fail("moe_linear_weight_sf_size", st)
+        # what a weight of this plan looks like
+        self._weight_bytes = (self._N * self._K // VALUES_PER_BYTE[self._fmt], n.value, self._fmt == "nvfp4")
 
     def __del__(self):
         if getattr(self, "_h", None) and _fns is not None:
@@ -443,19 +459,20 @@ class LinearPlan:
         for name, t, n in (("codes", codes, N * K // VALUES_PER_BYTE[fmt]), ("sf", sf, N * K // SF_BLOCK[fmt])):
             if t.element_size() != 1 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
                 raise ValueError(f"{name} must be a contiguous CUDA byte tensor of {n} bytes")
-        if global_scale is not None:
-            _flat("global_scale", global_scale, torch.float32, 1)
-        n = SZ()
-        st = _lib().moe_linear_weight_sf_size(self._h, byref(n))
-        if st != MOE_OK:
-            _fail("moe_linear_weight_sf_size", st)
         with _on(stream):
-            dst = LinearWeight(codes, torch.empty(n.value, dtype=torch.uint8, device=codes.device), global_scale)
+            dst = LinearWeight(codes, torch.empty(self._weight_bytes[1], dtype=torch.uint8, device=codes.device),
+                               global_scale, fmt, (N, K))
         src = LinearWeightC(codes.data_ptr(), sf.data_ptr(), None if global_scale is None else global_scale.data_ptr())
         st = _lib().moe_linear_transform_weight(self._h, byref(src), byref(dst._c), _stream(stream, codes))
         if st != MOE_OK:
             _fail("moe_linear_transform_weight", st)
         return dst
+
+    def _refuse_weight(self, w: LinearWeight):
+        N, K, fmt = self._N, self._K, self._fmt
+        raise ValueError(f"the weight holds {w.fmt or 'codes'} {w.shape or ''} of {w._bytes[0]} code and {w._bytes[1]} scale "
+                         f"bytes{' with' if w._bytes[2] else ' without'} a global scale; this plan takes {fmt} {(N, K)}, "
+                         f"{self._weight_bytes[0]} and {self._weight_bytes[1]} bytes")
 
     def forward(self, x, weight: LinearWeight, out: torch.Tensor | None = None,
                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -466,6 +483,9 @@ class LinearPlan:
         T = shape[0]
         if shape[1] != self._K:
             raise ValueError(f"x must be [T, {self._K}], got {tuple(shape)}")
+        if weight._bytes != self._weight_bytes or \
+                (weight.shape is not None and (weight.fmt != self._fmt or weight.shape != (N, self._K))):
+            self._refuse_weight(weight)
         if not quantized:
             ldx = _row_stride("x", x, _BF16, shape)
         if out is None:
