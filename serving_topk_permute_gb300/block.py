@@ -136,10 +136,16 @@ def _set_once(self, name, value):
     self.__dict__[name] = value
 
 
+def _places(tensors):
+    """Where the tensors' elements lie and how many there are: what resize_, set_, an assignment to
+    .data and a resized storage change behind a handle's back."""
+    return [(t.data_ptr(), t.numel()) for t in tensors]
+
+
 class Quantized:
     """Quantised rows: codes [rows, K / values per byte], block scales and, for NVFP4, one fp32
     scale per row (moe_quant_t). Codes and scales are byte tensors (uint8 or a float8 type). The
-    tensors cannot be replaced afterwards."""
+    tensors can be neither replaced nor resized afterwards."""
 
     def __init__(self, fmt: str, shape, codes: torch.Tensor, sf: torch.Tensor, row_scale: torch.Tensor | None,
                  sf_layout: str = "rows"):
@@ -157,11 +163,19 @@ class Quantized:
             _flat("row_scale", row_scale, torch.float32, rows)
         self.fmt, self.shape, self.sf_layout = fmt, torch.Size((rows, K)), sf_layout
         self.codes, self.sf, self.row_scale = codes, sf, row_scale
+        self._tensors = (codes, sf) if row_scale is None else (codes, sf, row_scale)
+        self._at = _places(self._tensors)
         self._c = QuantC(FORMATS[fmt], SF_LAYOUTS[sf_layout], codes.data_ptr(), sf.data_ptr(),
                          None if row_scale is None else row_scale.data_ptr())
         self._ref = byref(self._c)
 
     __setattr__ = _set_once
+
+    def _arg(self):
+        """The library's argument."""
+        if _places(self._tensors) != self._at:
+            raise ValueError("a tensor of the Quantized was resized or given other memory: make a new one")
+        return self._ref
 
     @classmethod
     def alloc(cls, fmt: str, rows: int, K: int, sf_layout: str = "atoms", device=None) -> "Quantized":
@@ -182,7 +196,7 @@ def quantize(x: torch.Tensor, fmt: str, sf_layout: str = "atoms", out: Quantized
             out = Quantized.alloc(fmt, shape[0], shape[1], sf_layout, x.device)
     elif out.shape != shape or out.fmt != fmt:
         raise ValueError(f"out holds {out.fmt} {out.shape}, x is {tuple(shape)} for {fmt}")
-    st = (_fns or _lib()).moe_quantize(shape[0], shape[1], x.data_ptr(), ldx, out._ref, _stream(stream, x))
+    st = (_fns or _lib()).moe_quantize(shape[0], shape[1], x.data_ptr(), ldx, out._arg(), _stream(stream, x))
     if st:
         _fail("moe_quantize", st)
     return out
@@ -217,7 +231,7 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residua
     if quantized is not None:
         if quantized.shape != shape:
             raise ValueError(f"quantized holds {quantized.shape}, x is {tuple(shape)}")
-        pq = quantized._ref
+        pq = quantized._arg()
     st = (_fns or _lib()).moe_add_rmsnorm(rows, H, x.data_ptr(), ldx, pr, ldr, gamma.data_ptr(), eps, ps, lds, po, ldo,
                                           pq, _raw_stream(x.get_device()) if stream is None else stream.cuda_stream)
     if st:
@@ -253,7 +267,7 @@ class RouterOutput:
         self.__dict__["_args"] = None  # checked again by the next forward
 
     def _check(self, T: int, E: int, k: int):
-        """The library's arguments for T tokens, after checks that hold until a buffer is replaced."""
+        """The library's arguments for T tokens, after checks that hold while the buffers stay where they are."""
         _flat("topk_ids", self.topk_ids, _I32, T * k)
         _flat("topk_weights", self.topk_weights, _F32, T * k)
         for name, dtype, n in (("counts", _I32, E), ("num_valid", _I32, 1), ("prob_mean", _F32, E), ("loss", _F32, 1)):
@@ -262,10 +276,12 @@ class RouterOutput:
                 _flat(name, t, dtype, n)
         if self.workspace.dtype is not _U8 or not self.workspace.is_cuda or not self.workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
-        ptr = [None if t is None else t.data_ptr() for t in
-               (self.topk_ids, self.topk_weights, self.counts, self.num_valid, self.prob_mean, self.loss,
-                self.workspace)]
-        self.__dict__["_args"] = (T, E, k, (*ptr, self.workspace.numel()))
+        all_of = (self.topk_ids, self.topk_weights, self.counts, self.num_valid, self.prob_mean, self.loss, self.workspace)
+        there = [t for t in all_of if t is not None]
+        if any(t.data_ptr() == 0 and t.numel() for t in there):
+            raise ValueError("a buffer of the RouterOutput has no memory")
+        ptr = [None if t is None else t.data_ptr() for t in all_of]
+        self.__dict__["_args"] = (T, E, k, (*ptr, self.workspace.numel()), there, _places(there))
 
 
 class Router:
@@ -332,7 +348,7 @@ class Router:
                 out = self.alloc(T, training, logits.device)
         o = out
         args = o._args
-        if args is None or args[0] != T or args[1] != E or args[2] != k:
+        if args is None or args[0] != T or args[1] != E or args[2] != k or _places(args[4]) != args[5]:
             o._check(T, E, k)
             args = o._args
         st = _fns.moe_router_forward(self._ref[logits.dtype], T, logits.data_ptr(), ld, mask, *args[3],
@@ -394,7 +410,7 @@ def linear_validate(cfg: LinearConfig) -> int:
 class LinearWeight:
     """A weight in the kernel layout (LinearPlan.transform_weight): codes, scale atoms (both bytes) and, for
     NVFP4, the global scale; the format and the shape [N, K] that they were laid out for, where that is
-    known. Its tensors cannot be replaced."""
+    known. Its tensors can be neither replaced nor resized."""
 
     __setattr__ = _set_once
 
@@ -408,9 +424,17 @@ class LinearWeight:
         self.codes, self.sf, self.global_scale = codes, sf, global_scale
         self.fmt, self.shape = fmt, None if shape is None else tuple(shape)
         self._bytes = (codes.numel(), sf.numel(), global_scale is not None)
+        self._tensors = (codes, sf) if global_scale is None else (codes, sf, global_scale)
+        self._at = _places(self._tensors)
         self._c = LinearWeightC(codes.data_ptr(), sf.data_ptr(),
                                 None if global_scale is None else global_scale.data_ptr())
         self._ref = byref(self._c)
+
+    def _arg(self):
+        """The library's argument."""
+        if _places(self._tensors) != self._at:
+            raise ValueError("a tensor of the LinearWeight was resized or given other memory: make a new one")
+        return self._ref
 
 
 class LinearPlan:
@@ -499,10 +523,10 @@ class LinearPlan:
             raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
         s = _raw_stream(out.get_device()) if stream is None else stream.cuda_stream
         if quantized:
-            st = _fns.moe_linear_forward_quantized(self._h, T, x._ref, weight._ref, out.data_ptr(), ldo,
+            st = _fns.moe_linear_forward_quantized(self._h, T, x._arg(), weight._arg(), out.data_ptr(), ldo,
                                                    workspace.data_ptr(), workspace.numel(), s)
         else:
-            st = _fns.moe_linear_forward(self._h, T, x.data_ptr(), ldx, weight._ref, out.data_ptr(), ldo,
+            st = _fns.moe_linear_forward(self._h, T, x.data_ptr(), ldx, weight._arg(), out.data_ptr(), ldo,
                                          workspace.data_ptr(), workspace.numel(), s)
         if st:
             _fail("moe_linear_forward", st)

@@ -155,3 +155,131 @@ def test_a_weight_of_another_plan_is_refused_by_the_library_at_hand(fmt):
             plan.forward(x, made(N, K)[1])
     same = pkg.LinearWeight(w.codes, w.sf, w.global_scale)  # format and shape not said: told by its bytes
     assert torch.equal(plan.forward(x, same), want)
+
+
+# ----------------------------------------------------------------------------- memory that moves
+
+def moved(t, shape=None):
+    """What resize_, set_ or an assignment to .data does to a tensor that a handle holds."""
+    if shape is not None:
+        t.shape, t._stride = torch.Size(shape), torch.empty(shape, device="meta").stride()
+    t.address += 1 << 30
+
+
+def router_output(T=5, E=8, k=2, device=0, bytes_=4096):
+    return pkg.RouterOutput(Tensor((T, k), I32, device), Tensor((T, k), F32, device), Tensor((E,), I32, device),
+                            Tensor((1,), I32, device), Tensor((E,), F32, device), Tensor((1,), F32, device),
+                            Tensor((bytes_,), U8, device))
+
+
+BUFFERS = ("topk_ids", "topk_weights", "counts", "num_valid", "prob_mean", "loss", "workspace")
+
+
+@pytest.mark.parametrize("name", BUFFERS)
+def test_a_router_follows_a_buffer_that_moved(library, name):
+    router, o, logits = pkg.Router(pkg.RouterConfig(8, 2)), router_output(), Tensor((5, 8), F32)
+    router.forward(logits, out=o)
+    moved(getattr(o, name))
+    router.forward(logits, out=o)
+    args = library.launches()[-1][1]
+    assert list(args[5:12]) == [getattr(o, b).data_ptr() for b in BUFFERS]
+
+
+@pytest.mark.parametrize("name", BUFFERS)
+def test_a_router_refuses_a_buffer_without_memory(library, name):
+    router, o, logits = pkg.Router(pkg.RouterConfig(8, 2)), router_output(), Tensor((5, 8), F32)
+    router.forward(logits, out=o)
+    before = len(library.launches())
+    getattr(o, name).address = 0  # its storage was freed: to the library no buffer at all
+    with pytest.raises(ValueError):
+        router.forward(logits, out=o)
+    assert len(library.launches()) == before
+
+
+@pytest.mark.parametrize("name", BUFFERS[:-1])
+def test_a_router_refuses_a_buffer_that_shrank(library, name):
+    router, o, logits = pkg.Router(pkg.RouterConfig(8, 2)), router_output(), Tensor((5, 8), F32)
+    router.forward(logits, out=o)
+    before = len(library.launches())
+    t = getattr(o, name)
+    t.shape, t._stride = torch.Size((t.numel() - 1,)), (1,)
+    with pytest.raises(ValueError):
+        router.forward(logits, out=o)
+    assert len(library.launches()) == before
+
+
+def test_a_router_passes_on_what_is_left_of_its_workspace(library):
+    router, o, logits = pkg.Router(pkg.RouterConfig(8, 2)), router_output(), Tensor((5, 8), F32)
+    router.forward(logits, out=o)
+    o.workspace.shape = torch.Size((512,))
+    router.forward(logits, out=o)
+    assert library.launches()[-1][1][12] == 512  # which the library then refuses if it is too small
+
+
+def quantized(T=4, K=128, fmt="nvfp4", device=0):
+    return pkg.Quantized(fmt, (T, K), Tensor((T, K // block.VALUES_PER_BYTE[fmt]), device=device),
+                         Tensor((SF_BYTES,), device=device), Tensor((T,), F32, device) if fmt == "nvfp4" else None, "atoms")
+
+
+@pytest.mark.parametrize("shape", [None, (2, 64)])
+@pytest.mark.parametrize("name", ["codes", "sf", "row_scale"])
+def test_quantised_rows_whose_memory_moved_are_refused(library, name, shape):
+    q, x, plan = quantized(), Tensor((4, 128), BF16), linear(library)
+    pkg.quantize(x, "nvfp4", out=q)
+    pkg.add_rmsnorm(x, Tensor((128,), F32), quantized=q)
+    run_linear(plan, weight(), x=q)
+    before = len(library.launches())
+    moved(getattr(q, name), shape)
+    for call in (lambda: pkg.quantize(x, "nvfp4", out=q), lambda: pkg.add_rmsnorm(x, Tensor((128,), F32), quantized=q),
+                 lambda: run_linear(plan, weight(), x=q)):
+        with pytest.raises(ValueError):
+            call()
+    assert len(library.launches()) == before
+
+
+@pytest.mark.parametrize("name", ["codes", "sf", "global_scale"])
+def test_a_weight_whose_memory_moved_is_refused(library, name):
+    w, plan = weight(), linear(library)
+    run_linear(plan, w)
+    before = len(library.launches())
+    moved(getattr(w, name))
+    with pytest.raises(ValueError):
+        run_linear(plan, w)
+    with pytest.raises(ValueError):
+        run_linear(plan, w, x=quantized())
+    assert len(library.launches()) == before
+
+
+@pytest.mark.gpu
+def test_real_tensors_that_move():
+    """resize_, set_, .data and a resized storage, on the device."""
+    router, logits = pkg.Router(pkg.RouterConfig(64, 8)), torch.randn((33, 64), device="cuda")
+    want = router.forward(logits, training=True)
+    taken = []
+    for how in ("set_", "data", "resize_", "storage"):
+        o = router.alloc(33, training=True)
+        router.forward(logits, out=o)
+        for name in BUFFERS:
+            t = getattr(o, name)
+            fresh = torch.zeros_like(t)
+            if how == "set_":
+                t.set_(fresh)
+            elif how == "data":
+                t.data = fresh
+            elif how == "resize_":
+                shape = t.shape
+                t.resize_(1 << 22).resize_(shape).zero_()
+            else:
+                n = t.untyped_storage().nbytes()
+                t.untyped_storage().resize_(0)
+                taken.append(torch.empty(n, dtype=torch.uint8, device="cuda"))  # the old place
+                t.untyped_storage().resize_(n)
+                t.zero_()
+        router.forward(logits, out=o)
+        for name in BUFFERS[:-1]:
+            assert torch.equal(getattr(o, name), getattr(want, name)), (how, name)
+    x = torch.randn((33, 64), device="cuda").bfloat16()
+    q = pkg.quantize(x, "nvfp4")
+    q.codes.set_(torch.zeros_like(q.codes))
+    with pytest.raises(ValueError):
+        pkg.quantize(x, "nvfp4", out=q)
