@@ -21,6 +21,8 @@ LOGITS = {torch.float32: 0, torch.bfloat16: 1}
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_device = torch.cuda.device
 
 P, I32, I64, SZ, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 
@@ -79,10 +81,31 @@ def _fail(fn: str, status: int):
     raise MoeError(fn, status)
 
 
-def _stream(stream, t: torch.Tensor) -> int:
-    """The given stream, or the current one of t's device (its raw handle: a torch.cuda.Stream
+def _launch(fn, dev: int, *args) -> int:
+    """The library's call with that device current: it launches on the current one, whatever device the
+    addresses belong to."""
+    if dev == _current_device():
+        return fn(*args)
+    with _device(dev):
+        return fn(*args)
+
+
+def _stream(stream, dev: int) -> int:
+    """The given stream, or the current one of that device (its raw handle: a torch.cuda.Stream
     object costs microseconds to make)."""
-    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
+    if stream is None:
+        return _raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors are on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _device_of(name: str, t: torch.Tensor) -> int:
+    """The number of the CUDA device that t is on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
+    return dev
 
 
 def _on(stream):
@@ -91,12 +114,13 @@ def _on(stream):
     return nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _row_stride(name: str, t: torch.Tensor, dtype, shape) -> int:
-    """The row stride of a 2-D CUDA tensor of this type and shape whose rows are contiguous."""
+def _row_stride(name: str, t: torch.Tensor, dtype, shape, dev: int) -> int:
+    """The row stride of a 2-D tensor of this type and shape on this device whose rows are contiguous."""
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor of shape {tuple(shape)}, got {tuple(t.shape)} on {t.device}")
+    if t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor of shape {tuple(shape)} on cuda:{dev}, "
+                         f"got {tuple(t.shape)} on {t.device}")
     stride = t.stride()
     if stride[1] != 1 and shape[1] > 1 and shape[0] > 0:
         raise ValueError(f"{name} must have contiguous rows")
@@ -111,12 +135,13 @@ def _matrix(name: str, t: torch.Tensor):
     return shape
 
 
-def _flat(name: str, t: torch.Tensor, dtype, numel: int):
-    """A contiguous CUDA tensor of numel elements."""
+def _flat(name: str, t: torch.Tensor, dtype, numel: int, dev: int):
+    """A contiguous tensor of numel elements on this device."""
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.numel() != numel or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {numel} elements")
+    if t.numel() != numel or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {numel} elements on cuda:{dev}, got {t.numel()} on "
+                         f"{t.device}")
 
 
 # ----------------------------------------------------------------------------- quantised rows
@@ -153,14 +178,16 @@ class Quantized:
         vpb = VALUES_PER_BYTE[fmt]
         if codes.element_size() != 1 or sf.element_size() != 1:
             raise ValueError("codes and scales must be byte tensors")
-        if not codes.is_cuda or not codes.is_contiguous() or codes.numel() != rows * K // vpb:
+        dev = _device_of("codes", codes)
+        if not codes.is_contiguous() or codes.numel() != rows * K // vpb:
             raise ValueError(f"codes must be a contiguous CUDA tensor of {rows * K // vpb} bytes")
-        if not sf.is_cuda or not sf.is_contiguous() or sf.numel() < sf_size(fmt, sf_layout, rows, K):
-            raise ValueError("scales must be a contiguous CUDA tensor of sf_size(...) bytes")
+        if sf.get_device() != dev or not sf.is_contiguous() or sf.numel() < sf_size(fmt, sf_layout, rows, K):
+            raise ValueError(f"scales must be a contiguous tensor of sf_size(...) bytes on cuda:{dev}")
         if (row_scale is not None) != (fmt == "nvfp4"):
             raise ValueError("NVFP4, and only NVFP4, has a scale per row")
         if row_scale is not None:
-            _flat("row_scale", row_scale, torch.float32, rows)
+            _flat("row_scale", row_scale, torch.float32, rows, dev)
+        self._dev = dev
         self.fmt, self.shape, self.sf_layout = fmt, torch.Size((rows, K)), sf_layout
         self.codes, self.sf, self.row_scale = codes, sf, row_scale
         self._tensors = (codes, sf) if row_scale is None else (codes, sf, row_scale)
@@ -171,8 +198,10 @@ class Quantized:
 
     __setattr__ = _set_once
 
-    def _arg(self):
+    def _arg(self, dev: int):
         """The library's argument."""
+        if self._dev != dev:
+            raise ValueError(f"the Quantized is on cuda:{self._dev}, the other tensors are on cuda:{dev}")
         if _places(self._tensors) != self._at:
             raise ValueError("a tensor of the Quantized was resized or given other memory: make a new one")
         return self._ref
@@ -190,13 +219,15 @@ def quantize(x: torch.Tensor, fmt: str, sf_layout: str = "atoms", out: Quantized
              stream=None) -> Quantized:
     """moe_quantize: the rows of x (bf16 [rows, K]) in a microscaled format."""
     shape = _matrix("x", x)
-    ldx = _row_stride("x", x, _BF16, shape)
+    dev = _device_of("x", x)
+    ldx = _row_stride("x", x, _BF16, shape, dev)
     if out is None:
         with _on(stream):
             out = Quantized.alloc(fmt, shape[0], shape[1], sf_layout, x.device)
     elif out.shape != shape or out.fmt != fmt:
         raise ValueError(f"out holds {out.fmt} {out.shape}, x is {tuple(shape)} for {fmt}")
-    st = (_fns or _lib()).moe_quantize(shape[0], shape[1], x.data_ptr(), ldx, out._arg(), _stream(stream, x))
+    st = _launch((_fns or _lib()).moe_quantize, dev, shape[0], shape[1], x.data_ptr(), ldx, out._arg(dev),
+                 _stream(stream, dev))
     if st:
         _fail("moe_quantize", st)
     return out
@@ -212,28 +243,29 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residua
     Returns out if there is one, else quantized."""
     shape = _matrix("x", x)
     rows, H = shape
-    ldx = _row_stride("x", x, _BF16, shape)
-    _flat("gamma", gamma, _F32, H)
+    dev = _device_of("x", x)
+    ldx = _row_stride("x", x, _BF16, shape, dev)
+    _flat("gamma", gamma, _F32, H, dev)
     if out is None and quantized is None:
         with _on(stream):
             out = torch.empty((rows, H), dtype=_BF16, device=x.device)
     po = pr = ps = pq = None
     ldo = ldr = lds = 0
     if out is not None:
-        ldo = _row_stride("out", out, _BF16, shape)
+        ldo = _row_stride("out", out, _BF16, shape, dev)
         po = out.data_ptr()
     if residual is not None:
-        ldr = _row_stride("residual", residual, _BF16, shape)
+        ldr = _row_stride("residual", residual, _BF16, shape, dev)
         pr = residual.data_ptr()
     if sum_out is not None:
-        lds = _row_stride("sum_out", sum_out, _BF16, shape)
+        lds = _row_stride("sum_out", sum_out, _BF16, shape, dev)
         ps = sum_out.data_ptr()
     if quantized is not None:
         if quantized.shape != shape:
             raise ValueError(f"quantized holds {quantized.shape}, x is {tuple(shape)}")
-        pq = quantized._arg()
-    st = (_fns or _lib()).moe_add_rmsnorm(rows, H, x.data_ptr(), ldx, pr, ldr, gamma.data_ptr(), eps, ps, lds, po, ldo,
-                                          pq, _raw_stream(x.get_device()) if stream is None else stream.cuda_stream)
+        pq = quantized._arg(dev)
+    st = _launch((_fns or _lib()).moe_add_rmsnorm, dev, rows, H, x.data_ptr(), ldx, pr, ldr, gamma.data_ptr(), eps, ps,
+                 lds, po, ldo, pq, _stream(stream, dev))
     if st:
         _fail("moe_add_rmsnorm", st)
     return out if out is not None else quantized
@@ -266,22 +298,23 @@ class RouterOutput:
         self.__dict__[name] = value
         self.__dict__["_args"] = None  # checked again by the next forward
 
-    def _check(self, T: int, E: int, k: int):
+    def _check(self, T: int, E: int, k: int, dev: int):
         """The library's arguments for T tokens, after checks that hold while the buffers stay where they are."""
-        _flat("topk_ids", self.topk_ids, _I32, T * k)
-        _flat("topk_weights", self.topk_weights, _F32, T * k)
+        _flat("topk_ids", self.topk_ids, _I32, T * k, dev)
+        _flat("topk_weights", self.topk_weights, _F32, T * k, dev)
         for name, dtype, n in (("counts", _I32, E), ("num_valid", _I32, 1), ("prob_mean", _F32, E), ("loss", _F32, 1)):
             t = getattr(self, name)
             if t is not None:
-                _flat(name, t, dtype, n)
-        if self.workspace.dtype is not _U8 or not self.workspace.is_cuda or not self.workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
-        all_of = (self.topk_ids, self.topk_weights, self.counts, self.num_valid, self.prob_mean, self.loss, self.workspace)
+                _flat(name, t, dtype, n, dev)
+        if self.workspace.dtype is not _U8 or self.workspace.get_device() != dev or not self.workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{dev}")
+        all_of = (self.topk_ids, self.topk_weights, self.counts, self.num_valid, self.prob_mean, self.loss,
+                  self.workspace)
         there = [t for t in all_of if t is not None]
         if any(t.data_ptr() == 0 and t.numel() for t in there):
             raise ValueError("a buffer of the RouterOutput has no memory")
         ptr = [None if t is None else t.data_ptr() for t in all_of]
-        self.__dict__["_args"] = (T, E, k, (*ptr, self.workspace.numel()), there, _places(there))
+        self.__dict__["_args"] = ((T, E, k, dev), (*ptr, self.workspace.numel()), there, _places(there))
 
 
 class Router:
@@ -322,37 +355,38 @@ class Router:
             empty(max(self.workspace_size(T), 1), dtype=torch.uint8, device=device))
 
     def _inputs(self, logits: torch.Tensor, token_mask: torch.Tensor | None):
-        """Number of tokens, the logits' row stride and the mask's address."""
+        """Number of tokens, the logits' device and row stride, and the mask's address."""
         shape = _matrix("logits", logits)
         dtype = logits.dtype
         if dtype not in LOGITS:
             raise ValueError(f"logits must be float32 or bfloat16, got {dtype}")
-        ld = _row_stride("logits", logits, dtype, shape)
+        dev = _device_of("logits", logits)
+        ld = _row_stride("logits", logits, dtype, shape, dev)
         if shape[1] != self._E:
             raise ValueError(f"logits must be [T, {self._E}], got {tuple(shape)}")
         if token_mask is None:
-            return shape[0], ld, None
+            return shape[0], dev, ld, None
         if token_mask.dtype not in (torch.bool, _U8):
             raise ValueError("token_mask must be bool or uint8")
-        _flat("token_mask", token_mask, token_mask.dtype, shape[0])
-        return shape[0], ld, token_mask.data_ptr()
+        _flat("token_mask", token_mask, token_mask.dtype, shape[0], dev)
+        return shape[0], dev, ld, token_mask.data_ptr()
 
     def forward(self, logits: torch.Tensor, token_mask: torch.Tensor | None = None, out: RouterOutput | None = None,
                 training: bool = False, stream=None) -> RouterOutput:
         """logits fp32 or bf16 [T, E]; token_mask bool [T] (False: padding). With out, its buffers
         are written (prob_mean and loss when it has them); else they are allocated."""
-        T, ld, mask = self._inputs(logits, token_mask)
+        T, dev, ld, mask = self._inputs(logits, token_mask)
         E, k = self._E, self._k
         if out is None:
             with _on(stream):
                 out = self.alloc(T, training, logits.device)
         o = out
         args = o._args
-        if args is None or args[0] != T or args[1] != E or args[2] != k or _places(args[4]) != args[5]:
-            o._check(T, E, k)
+        if args is None or args[0] != (T, E, k, dev) or _places(args[2]) != args[3]:
+            o._check(T, E, k, dev)
             args = o._args
-        st = _fns.moe_router_forward(self._ref[logits.dtype], T, logits.data_ptr(), ld, mask, *args[3],
-                                     _raw_stream(logits.get_device()) if stream is None else stream.cuda_stream)
+        st = _launch(_fns.moe_router_forward, dev, self._ref[logits.dtype], T, logits.data_ptr(), ld, mask, *args[1],
+                     _stream(stream, dev))
         if st:
             _fail("moe_router_forward", st)
         return o
@@ -363,27 +397,26 @@ class Router:
                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """The gradient of sum(d_weights * topk_weights) + d_loss * loss with respect to logits
         (counts held constant), in the logits' type."""
-        T, ld, mask = self._inputs(logits, token_mask)
+        T, dev, ld, mask = self._inputs(logits, token_mask)
         E, k = self._E, self._k
         if out is None:
             with _on(stream):
                 out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-        ldo = _row_stride("out", out, logits.dtype, logits.shape)
-        _flat("topk_ids", topk_ids, _I32, T * k)
+        ldo = _row_stride("out", out, logits.dtype, logits.shape, dev)
+        _flat("topk_ids", topk_ids, _I32, T * k, dev)
         pw = pl = pc = pn = None
         if d_weights is not None:
-            _flat("d_weights", d_weights, _F32, T * k)
+            _flat("d_weights", d_weights, _F32, T * k, dev)
             pw = d_weights.data_ptr()
         if d_loss is not None:
             if counts is None or num_valid is None:
                 raise ValueError("the loss's gradient needs counts and num_valid")
-            _flat("d_loss", d_loss, _F32, 1)
-            _flat("counts", counts, _I32, E)
-            _flat("num_valid", num_valid, _I32, 1)
+            _flat("d_loss", d_loss, _F32, 1, dev)
+            _flat("counts", counts, _I32, E, dev)
+            _flat("num_valid", num_valid, _I32, 1, dev)
             pl, pc, pn = d_loss.data_ptr(), counts.data_ptr(), num_valid.data_ptr()
-        st = _fns.moe_router_backward(self._ref[logits.dtype], T, logits.data_ptr(), ld, mask, topk_ids.data_ptr(), pc,
-                                      pn, pw, pl, out.data_ptr(), ldo,
-                                      _raw_stream(out.get_device()) if stream is None else stream.cuda_stream)
+        st = _launch(_fns.moe_router_backward, dev, self._ref[logits.dtype], T, logits.data_ptr(), ld, mask,
+                     topk_ids.data_ptr(), pc, pn, pw, pl, out.data_ptr(), ldo, _stream(stream, dev))
         if st:
             _fail("moe_router_backward", st)
         return out
@@ -416,11 +449,13 @@ class LinearWeight:
 
     def __init__(self, codes: torch.Tensor, sf: torch.Tensor, global_scale: torch.Tensor | None,
                  fmt: str | None = None, shape=None):
+        dev = _device_of("codes", codes)
         for name, t in (("codes", codes), ("sf", sf)):
-            if t.element_size() != 1 or not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous CUDA byte tensor")
+            if t.element_size() != 1 or t.get_device() != dev or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous byte tensor on cuda:{dev}")
         if global_scale is not None:
-            _flat("global_scale", global_scale, _F32, 1)
+            _flat("global_scale", global_scale, _F32, 1, dev)
+        self._dev = dev
         self.codes, self.sf, self.global_scale = codes, sf, global_scale
         self.fmt, self.shape = fmt, None if shape is None else tuple(shape)
         self._bytes = (codes.numel(), sf.numel(), global_scale is not None)
@@ -430,15 +465,18 @@ class LinearWeight:
                                 None if global_scale is None else global_scale.data_ptr())
         self._ref = byref(self._c)
 
-    def _arg(self):
+    def _arg(self, dev: int):
         """The library's argument."""
+        if self._dev != dev:
+            raise ValueError(f"the weight is on cuda:{self._dev}, the plan is for cuda:{dev}")
         if _places(self._tensors) != self._at:
             raise ValueError("a tensor of the LinearWeight was resized or given other memory: make a new one")
         return self._ref
 
 
 class LinearPlan:
-    """out[t, n] = sum_k x[t, k] W[n, k] with x and W in a microscaled format (moe_linear_*)."""
+    """out[t, n] = sum_k x[t, k] W[n, k] with x and W in a microscaled format (moe_linear_*), on the device that
+    is current when the plan is made."""
 
     def __init__(self, cfg: LinearConfig):
         # tensors are checked by what the library was told, whatever becomes of cfg
@@ -447,7 +485,7 @@ class LinearPlan:
         st = _lib().moe_linear_plan(byref(cfg.to_c()), byref(h))
         if st != MOE_OK:
             _fail("moe_linear_plan", st)
-        self._h = h
+        self._h, self._dev = h, _current_device()
         n = SZ()
         st = _lib().moe_linear_weight_sf_size(h, byref(n))
         if st != MOE_OK:
@@ -473,7 +511,7 @@ class LinearPlan:
 
     def alloc_workspace(self, num_tokens: int, device=None) -> torch.Tensor:
         return torch.zeros(max(self.workspace_size(num_tokens), 1), dtype=torch.uint8,
-                           device=device or torch.device("cuda", torch.cuda.current_device()))
+                           device=device or torch.device("cuda", self._dev))
 
     def transform_weight(self, codes: torch.Tensor, sf: torch.Tensor, global_scale: torch.Tensor | None = None,
                          stream=None) -> LinearWeight:
@@ -481,27 +519,28 @@ class LinearPlan:
         the NVFP4 global scale (fp32 [1]), in the kernel layout. The codes are shared, not copied."""
         N, K, fmt = self._N, self._K, self._fmt
         for name, t, n in (("codes", codes, N * K // VALUES_PER_BYTE[fmt]), ("sf", sf, N * K // SF_BLOCK[fmt])):
-            if t.element_size() != 1 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
-                raise ValueError(f"{name} must be a contiguous CUDA byte tensor of {n} bytes")
+            if t.element_size() != 1 or t.get_device() != self._dev or not t.is_contiguous() or t.numel() != n:
+                raise ValueError(f"{name} must be a contiguous byte tensor of {n} bytes on cuda:{self._dev}")
         with _on(stream):
             dst = LinearWeight(codes, torch.empty(self._weight_bytes[1], dtype=torch.uint8, device=codes.device),
                                global_scale, fmt, (N, K))
         src = LinearWeightC(codes.data_ptr(), sf.data_ptr(), None if global_scale is None else global_scale.data_ptr())
-        st = _lib().moe_linear_transform_weight(self._h, byref(src), byref(dst._c), _stream(stream, codes))
+        st = _launch(_lib().moe_linear_transform_weight, self._dev, self._h, byref(src), byref(dst._c),
+                     _stream(stream, self._dev))
         if st != MOE_OK:
             _fail("moe_linear_transform_weight", st)
         return dst
 
     def _refuse_weight(self, w: LinearWeight):
         N, K, fmt = self._N, self._K, self._fmt
-        raise ValueError(f"the weight holds {w.fmt or 'codes'} {w.shape or ''} of {w._bytes[0]} code and {w._bytes[1]} scale "
-                         f"bytes{' with' if w._bytes[2] else ' without'} a global scale; this plan takes {fmt} {(N, K)}, "
-                         f"{self._weight_bytes[0]} and {self._weight_bytes[1]} bytes")
+        raise ValueError(f"the weight holds {w.fmt or 'codes'} {w.shape or ''} of {w._bytes[0]} code and {w._bytes[1]} "
+                         f"scale bytes{' with' if w._bytes[2] else ' without'} a global scale; this plan takes {fmt} "
+                         f"{(N, K)}, {self._weight_bytes[0]} and {self._weight_bytes[1]} bytes")
 
     def forward(self, x, weight: LinearWeight, out: torch.Tensor | None = None,
                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x: bf16 [T, K] (quantised by the call) or a Quantized with scales in atoms; out bf16 [T, N]."""
-        N = self._N
+        N, dev = self._N, self._dev
         quantized = type(x) is Quantized
         shape = x.shape if quantized else _matrix("x", x)
         T = shape[0]
@@ -511,23 +550,23 @@ class LinearPlan:
                 (weight.shape is not None and (weight.fmt != self._fmt or weight.shape != (N, self._K))):
             self._refuse_weight(weight)
         if not quantized:
-            ldx = _row_stride("x", x, _BF16, shape)
+            ldx = _row_stride("x", x, _BF16, shape, dev)
         if out is None:
             with _on(stream):
                 out = torch.empty((T, N), dtype=_BF16, device=weight.codes.device)
-        ldo = _row_stride("out", out, _BF16, (T, N))
+        ldo = _row_stride("out", out, _BF16, (T, N), dev)
         if workspace is None:
             with _on(stream):
                 workspace = self.alloc_workspace(T, out.device)
-        elif not workspace.is_cuda or workspace.dtype is not _U8 or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous uint8 CUDA tensor")
-        s = _raw_stream(out.get_device()) if stream is None else stream.cuda_stream
+        elif workspace.get_device() != dev or workspace.dtype is not _U8 or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{dev}")
+        s = _stream(stream, dev)
         if quantized:
-            st = _fns.moe_linear_forward_quantized(self._h, T, x._arg(), weight._arg(), out.data_ptr(), ldo,
-                                                   workspace.data_ptr(), workspace.numel(), s)
+            st = _launch(_fns.moe_linear_forward_quantized, dev, self._h, T, x._arg(dev), weight._arg(dev),
+                         out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(), s)
         else:
-            st = _fns.moe_linear_forward(self._h, T, x.data_ptr(), ldx, weight._arg(), out.data_ptr(), ldo,
-                                         workspace.data_ptr(), workspace.numel(), s)
+            st = _launch(_fns.moe_linear_forward, dev, self._h, T, x.data_ptr(), ldx, weight._arg(dev), out.data_ptr(),
+                         ldo, workspace.data_ptr(), workspace.numel(), s)
         if st:
             _fail("moe_linear_forward", st)
         return out
@@ -540,7 +579,10 @@ class LinearPlan:
 
     def last_status(self, workspace: torch.Tensor, stream=None) -> int:
         v = I32()
-        st = _lib().moe_linear_last_status(self._h, workspace.data_ptr(), _stream(stream, workspace), byref(v))
+        if workspace.get_device() != self._dev:
+            raise ValueError(f"workspace must be on cuda:{self._dev}, got one on {workspace.device}")
+        st = _launch(_lib().moe_linear_last_status, self._dev, self._h, workspace.data_ptr(),
+                     _stream(stream, self._dev), byref(v))
         if st != MOE_OK:
             _fail("moe_linear_last_status", st)
         return v.value

@@ -1,6 +1,7 @@
 """What the handles of the operators around the experts refuse on the host, before any launch: stand-ins
 take the place of the library and of device tensors, so no GPU is needed."""
 import dataclasses
+from contextlib import contextmanager
 
 import pytest
 import torch
@@ -10,14 +11,16 @@ from serving_topk_permute_gb300 import block
 
 
 class Library:
-    """Stands in for the library: every call succeeds and is recorded; sizes are 4096 bytes."""
+    """Stands in for the library: every call succeeds and is recorded, with the device that was current; sizes
+    are 4096 bytes."""
 
     def __init__(self):
-        self.calls = []
+        self.calls, self.current, self.at = [], 0, []
 
     def __getattr__(self, name):
         def call(*args):
             self.calls.append((name, args))
+            self.at.append(self.current)
             if name.endswith("_size"):
                 args[-1]._obj.value = 4096
             return 0
@@ -33,6 +36,15 @@ def library(monkeypatch):
     lib = Library()
     monkeypatch.setattr(block, "_fns", lib)
     monkeypatch.setattr(block, "_raw_stream", lambda device: 1000 + device)
+    monkeypatch.setattr(block, "_current_device", lambda: lib.current, raising=False)
+
+    @contextmanager
+    def device(index):
+        before, lib.current = lib.current, index
+        yield
+        lib.current = before
+
+    monkeypatch.setattr(block, "_device", device, raising=False)
     return lib
 
 
@@ -64,6 +76,13 @@ def test_buffers_follow_what_the_library_was_told(library):
     assert o.topk_ids.shape == (5, 8) and router._c[torch.float32].top_k == 8
 
 
+def contiguous(shape):
+    strides = [1]
+    for n in reversed(shape[1:]):
+        strides.insert(0, strides[0] * n)
+    return tuple(strides[:len(shape)])
+
+
 class Tensor:
     """Stands in for a contiguous tensor on a device of that number (-1: the host); strides may be given."""
 
@@ -71,7 +90,7 @@ class Tensor:
 
     def __init__(self, shape, dtype=torch.uint8, device=0, stride=None):
         self.shape, self.dtype, self.index = torch.Size(shape), dtype, device
-        self._stride = stride or torch.empty(shape, dtype=dtype, device="meta").stride()
+        self._stride = stride or contiguous(shape)
         self.address = Tensor._next[0]
         Tensor._next[0] += (self.numel() * self.element_size() + 4095) // 4096 * 4096 + 4096
 
@@ -83,7 +102,7 @@ class Tensor:
     def numel(self): return self.shape.numel()
     def element_size(self): return self.dtype.itemsize
     def stride(self): return self._stride
-    def is_contiguous(self): return self._stride == torch.empty(self.shape, device="meta").stride()
+    def is_contiguous(self): return self._stride == contiguous(self.shape)
 
 
 BF16, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
@@ -95,7 +114,8 @@ def linear(library, N=64, K=128, fmt="nvfp4"):
 
 
 def weight(N=64, K=128, fmt="nvfp4", sf_bytes=SF_BYTES, known=True, device=0):
-    return pkg.LinearWeight(Tensor((N, K // block.VALUES_PER_BYTE[fmt]), device=device), Tensor((sf_bytes,), device=device),
+    return pkg.LinearWeight(Tensor((N, K // block.VALUES_PER_BYTE[fmt]), device=device),
+                            Tensor((sf_bytes,), device=device),
                             Tensor((1,), F32, device) if fmt == "nvfp4" else None, *((fmt, (N, K)) if known else ()))
 
 
@@ -162,7 +182,7 @@ def test_a_weight_of_another_plan_is_refused_by_the_library_at_hand(fmt):
 def moved(t, shape=None):
     """What resize_, set_ or an assignment to .data does to a tensor that a handle holds."""
     if shape is not None:
-        t.shape, t._stride = torch.Size(shape), torch.empty(shape, device="meta").stride()
+        t.shape, t._stride = torch.Size(shape), contiguous(shape)
     t.address += 1 << 30
 
 
@@ -218,7 +238,8 @@ def test_a_router_passes_on_what_is_left_of_its_workspace(library):
 
 def quantized(T=4, K=128, fmt="nvfp4", device=0):
     return pkg.Quantized(fmt, (T, K), Tensor((T, K // block.VALUES_PER_BYTE[fmt]), device=device),
-                         Tensor((SF_BYTES,), device=device), Tensor((T,), F32, device) if fmt == "nvfp4" else None, "atoms")
+                         Tensor((SF_BYTES,), device=device), Tensor((T,), F32, device) if fmt == "nvfp4" else None,
+                         "atoms")
 
 
 @pytest.mark.parametrize("shape", [None, (2, 64)])
@@ -249,6 +270,114 @@ def test_a_weight_whose_memory_moved_is_refused(library, name):
         run_linear(plan, w, x=quantized())
     assert len(library.launches()) == before
 
+
+# ----------------------------------------------------------------------------- devices
+
+class Stream:
+    def __init__(self, device):
+        self.device_index, self.cuda_stream = device, 77
+
+
+def calls_on(library, dev, other=None, **kw):
+    """Every launching call with its tensors on device dev; the tensor named `other` on the device after it."""
+    d = lambda name: dev + 1 if name == other else dev  # noqa: E731
+    library.current = dev
+    plan = linear(library)
+    library.current = 0
+    router = pkg.Router(pkg.RouterConfig(8, 2))
+    T, x, logits = 4, Tensor((4, 128), BF16, d("x")), Tensor((4, 8), F32, d("logits"))
+    o = router_output(T, device=dev)
+    if other in BUFFERS:
+        t = getattr(o, other)
+        t.index = dev + 1
+    grad = dict(counts=Tensor((8,), I32, d("counts")), num_valid=Tensor((1,), I32, d("num_valid")),
+                d_weights=Tensor((T, 2), F32, d("d_weights")), d_loss=Tensor((1,), F32, d("d_loss")),
+                token_mask=Tensor((T,), torch.bool, d("mask")), out=Tensor((T, 8), F32, d("out")))
+    src = (Tensor((64, 64), U8, d("w_codes")), Tensor((64, 8), U8, d("w_sf")), Tensor((1,), F32, d("w_scale")))
+    return {
+        "quantize": lambda: pkg.quantize(x, "nvfp4", out=quantized(device=d("q")), **kw),
+        "norm": lambda: pkg.add_rmsnorm(x, Tensor((128,), F32, d("gamma")),
+                                        residual=Tensor((4, 128), BF16, d("residual")),
+                                        sum_out=Tensor((4, 128), BF16, d("sum")), out=Tensor((4, 128), BF16, d("out")),
+                                        quantized=quantized(device=d("q")), **kw),
+        "router": lambda: router.forward(logits, token_mask=Tensor((T,), torch.bool, d("mask")), out=o, **kw),
+        "gradient": lambda: router.backward(logits, Tensor((T, 2), I32, d("ids")), **grad, **kw),
+        "linear": lambda: run_linear(plan, weight(device=d("weight")), x=x, out=Tensor((T, 64), BF16, d("out")),
+                                     workspace=Tensor((SF_BYTES,), U8, d("ws")), **kw),
+        "linear from quantised rows": lambda: run_linear(
+            plan, weight(device=d("weight")), x=quantized(device=d("q")), out=Tensor((T, 64), BF16, d("out")),
+            workspace=Tensor((SF_BYTES,), U8, d("ws")), **kw),
+        "transform": lambda: plan.transform_weight(*src, **kw),
+        "status": lambda: plan.last_status(Tensor((SF_BYTES,), U8, d("ws")), **kw),
+    }
+
+
+NAMES = ("quantize", "norm", "router", "gradient", "linear", "linear from quantised rows", "transform", "status")
+
+
+@pytest.fixture
+def no_allocation(monkeypatch):
+    monkeypatch.setattr(block.torch, "empty", lambda shape, dtype=None, device=None: Tensor(
+        (shape,) if isinstance(shape, int) else shape, dtype or F32, device.index))
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("dev", [0, 1])
+def test_a_call_runs_with_its_tensors_device_current(library, no_allocation, name, dev):
+    """On that device's current stream, and the device that was current is current again afterwards."""
+    calls_on(library, dev)[name]()
+    (_, args), at = library.launches()[-1], library.at[-1]
+    assert at == dev and library.current == 0
+    assert 1000 + dev in args
+
+
+@pytest.mark.parametrize("name,other", [
+    ("quantize", "x"), ("quantize", "q"), ("norm", "x"), ("norm", "gamma"), ("norm", "residual"), ("norm", "sum"),
+    ("norm", "out"), ("norm", "q"), ("router", "logits"), ("router", "mask"), *(("router", b) for b in BUFFERS),
+    ("gradient", "logits"), ("gradient", "ids"), ("gradient", "counts"), ("gradient", "num_valid"),
+    ("gradient", "d_weights"), ("gradient", "d_loss"), ("gradient", "mask"), ("gradient", "out"), ("linear", "x"),
+    ("linear", "weight"), ("linear", "out"), ("linear", "ws"), ("linear from quantised rows", "q"),
+    ("linear from quantised rows", "weight"), ("transform", "w_codes"), ("transform", "w_sf"), ("transform", "w_scale"),
+    ("status", "ws"),
+])
+@pytest.mark.parametrize("dev", [0, 1])
+def test_tensors_on_two_devices_are_refused(library, no_allocation, name, other, dev):
+    call = calls_on(library, dev, other)[name]
+    before = len(library.launches())
+    with pytest.raises(ValueError):
+        call()
+    assert len(library.launches()) == before
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_stream_of_another_device_is_refused(library, no_allocation, monkeypatch, name):
+    monkeypatch.setattr(block, "_on", lambda stream: block.nullcontext())
+    calls_on(library, 1, stream=Stream(1))[name]()
+    assert 77 in library.launches()[-1][1]
+    call = calls_on(library, 1, stream=Stream(0))[name]
+    before = len(library.launches())
+    with pytest.raises(ValueError):
+        call()
+    assert len(library.launches()) == before
+
+
+def test_buffers_that_were_checked_on_one_device_are_not_taken_for_another(library):
+    router, o = pkg.Router(pkg.RouterConfig(8, 2)), router_output()
+    router.forward(Tensor((5, 8), F32), out=o)
+    with pytest.raises(ValueError):
+        router.forward(Tensor((5, 8), F32, 1), out=o)
+
+
+@pytest.mark.parametrize("codes,sf,scale", [(0, 1, 0), (0, 0, 1), (1, 0, 0), (-1, 0, 0), (0, -1, 0)])
+def test_the_tensors_of_a_handle_are_on_one_device(library, codes, sf, scale):
+    c, s, g = Tensor((4, 64), device=codes), Tensor((SF_BYTES,), device=sf), Tensor((4,), F32, scale)
+    with pytest.raises(ValueError):
+        pkg.Quantized("nvfp4", (4, 128), c, s, g, "atoms")
+    with pytest.raises(ValueError):
+        pkg.LinearWeight(c, s, Tensor((1,), F32, scale), "nvfp4", (4, 128))
+
+
+# ----------------------------------------------------------------------------- on the device
 
 @pytest.mark.gpu
 def test_real_tensors_that_move():
