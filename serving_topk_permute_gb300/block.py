@@ -578,9 +578,13 @@ class LinearPlan:
             _fail("moe_linear_set_wait_timeout", st)
 
     def last_status(self, workspace: torch.Tensor, stream=None) -> int:
+        """The status of the last forward in this workspace, which is waited for (moe_linear_last_status)."""
         v = I32()
-        if workspace.get_device() != self._dev:
-            raise ValueError(f"workspace must be on cuda:{self._dev}, got one on {workspace.device}")
+        least = self.workspace_size(0)  # the status words lie at its start, as many for every number of tokens
+        if workspace.get_device() != self._dev or workspace.dtype is not _U8 or not workspace.is_contiguous() or \
+                workspace.numel() < least:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {least} bytes on cuda:{self._dev}, "
+                             f"got {workspace.numel()} {workspace.dtype} on {workspace.device}")
         st = _launch(_lib().moe_linear_last_status, self._dev, self._h, workspace.data_ptr(),
                      _stream(stream, self._dev), byref(v))
         if st != MOE_OK:

@@ -377,6 +377,17 @@ def test_the_tensors_of_a_handle_are_on_one_device(library, codes, sf, scale):
         pkg.LinearWeight(c, s, Tensor((1,), F32, scale), "nvfp4", (4, 128))
 
 
+@pytest.mark.parametrize("workspace", [Tensor((SF_BYTES - 1,)), Tensor((16,)), Tensor((0,)), Tensor((SF_BYTES,), I32),
+                                       Tensor((SF_BYTES,), stride=(2,))])
+def test_a_status_is_read_from_a_whole_workspace_only(library, workspace):
+    plan = linear(library)
+    before = len(library.launches())
+    with pytest.raises(ValueError):
+        plan.last_status(workspace)
+    assert len(library.launches()) == before
+    assert plan.last_status(Tensor((SF_BYTES,))) == 0
+
+
 # ----------------------------------------------------------------------------- on the device
 
 @pytest.mark.gpu
