@@ -78,6 +78,20 @@ __device__ __forceinline__ bool warp_wait_cl(uint32_t bar, uint32_t parity, uint
     return __all_sync(0xffffffffu, lin_wait_cl(bar, parity, timeout_ns, abort));
 }
 
+// What an NVFP4 token's sums are multiplied by, one factor after the other: its scale times the weight's
+// and 1. Where that product leaves the normal range though an output need not (rows or weights around
+// 2^-100), the significands' product with an exponent that keeps every sum (2^-20 .. 2^40, or zero) in
+// range, and the power of two that is left.
+__device__ __forceinline__ float2 token_scale(float xs, float ws) {
+    const float a = xs * ws;
+    if (a >= 0x1p-126f && a <= 0x1.fffffep127f) return make_float2(a, 1.0f);
+    if (!(xs > 0.0f && ws > 0.0f) || isinf(xs) || isinf(ws)) return make_float2(a, 1.0f);  // NaN, zero, infinity
+    int ex, ew;
+    const float m = frexpf(xs, &ex) * frexpf(ws, &ew);
+    const int e = ex + ew, first = min(max(e, -100), 80);
+    return make_float2(ldexpf(m, first), ldexpf(1.0f, min(e - first, 127)));
+}
+
 // Shared-memory descriptors differ only in their low word: the address / 16 (and, for operand rows,
 // a leading offset of 1 in bits 16 ..). The high words are those of kmajor_sw128_desc and
 // sf_atom_desc.
@@ -377,11 +391,12 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
             // call that follows (23.2).
             // Plain loads: the quantiser writes the scales while this kernel is resident already, which the
             // read-only path does not allow.
-            float scale[COLS / 32];
+            float2 scale[COLS / 32];
             if constexpr (FMT == MOE_FMT_NVFP4) {
 #pragma unroll
                 for (int c = 0; c < COLS / 32; ++c)
-                    scale[c] = t0 + 32 * c + lane < p.M ? p.x_scale[t0 + 32 * c + lane] * *p.w_scale : 0.0f;
+                    scale[c] = t0 + 32 * c + lane < p.M ? token_scale(p.x_scale[t0 + 32 * c + lane], *p.w_scale)
+                                                        : make_float2(0.0f, 1.0f);
             }
             // warp-uniform: every lane leaves together (a lane left behind would block in __syncwarp)
             if (!warp_wait(tfull_bar, acc_phase, tmo, abort_flag)) {
@@ -406,7 +421,14 @@ __global__ void __launch_bounds__(PairCfg<FMT>::THREADS, 1)
             acc_phase ^= 1;
             if constexpr (FMT == MOE_FMT_NVFP4) {
 #pragma unroll
-                for (int j = 0; j < COLS; ++j) v[j / 32][j % 32] *= __shfl_sync(0xffffffffu, scale[j / 32], j % 32);
+                for (int j = 0; j < COLS; ++j) v[j / 32][j % 32] *= __shfl_sync(0xffffffffu, scale[j / 32].x, j % 32);
+                bool rest = false;
+#pragma unroll
+                for (int c = 0; c < COLS / 32; ++c) rest |= scale[c].y != 1.0f;
+                if (__any_sync(0xffffffffu, rest)) {
+#pragma unroll
+                    for (int j = 0; j < COLS; ++j) v[j / 32][j % 32] *= __shfl_sync(0xffffffffu, scale[j / 32].y, j % 32);
+                }
             }
             if (n < p.N) {
                 __nv_bfloat16* o = p.out + (int64_t)t0 * p.ldo + n;
@@ -494,8 +516,10 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP 
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* never = reinterpret_cast<int*>(tmem_slot + 2);
-    __shared__ uint32_t s_amax[BT];  // QUANT, NVFP4: the tokens' magnitudes (bit patterns)
-    __shared__ float s_alpha[BT];    // NVFP4: what a token's sums are multiplied by
+    __shared__ uint32_t s_amax[QUANT ? BT : 1];  // NVFP4: the tokens' magnitudes (bit patterns)
+    // NVFP4: what a token's sums are multiplied by (token_scale), and whether any second factor is not 1
+    __shared__ float s_alpha[FMT == MOE_FMT_NVFP4 ? BT : 1], s_rest[FMT == MOE_FMT_NVFP4 ? BT : 1];
+    __shared__ int s_any_rest;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, done_bar = empty0 + 8 * STAGES,
@@ -514,6 +538,7 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP 
         mbar_init(x_bar, C::EPI);
         *abort_flag = 0;
         *never = 0;
+        if constexpr (FMT == MOE_FMT_NVFP4) s_any_rest = 0;
         fence_mbar_init();
         prefetch_tmap(&tmW);
         if constexpr (!QUANT) prefetch_tmap(&tmX);
@@ -693,8 +718,13 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP 
         }
         if constexpr (FMT == MOE_FMT_NVFP4) {
             const int c = (int)threadIdx.x - 64;
-            if (c < tokens)
-                s_alpha[c] = (QUANT ? nvfp4_row_scale(__uint_as_float(s_amax[c])) : p.x_scale[tt * BT + c]) * *p.w_scale;
+            if (c < tokens) {
+                const float2 f = token_scale(QUANT ? nvfp4_row_scale(__uint_as_float(s_amax[c])) : p.x_scale[tt * BT + c],
+                                             *p.w_scale);
+                s_alpha[c] = f.x;
+                s_rest[c] = f.y;
+                if (f.y != 1.0f) s_any_rest = 1;
+            }
         }
         complete = warp_wait(done_bar, 0, tmo, abort_flag);
         if (!complete) give_up();
@@ -723,11 +753,17 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP 
             float v[32];
             tmem_ld32(tacc + c0, v);  // for BT = 16 the upper columns hold scales: not kept
             tmem_ld_wait();
+            const float* last = s_alpha + c0;  // the factor that is applied where a value is stored
+            if (FMT == MOE_FMT_NVFP4 && s_any_rest) {
+#pragma unroll
+                for (int j = 0; j < STEP; ++j) v[j] *= last[j];  // past the tokens: not kept
+                last = s_rest + c0;
+            }
             if (n < p.N && complete) {
                 __nv_bfloat16* o = p.out + (int64_t)(tt * BT + c0) * p.ldo + n;
 #pragma unroll
                 for (int j = 0; j < STEP; ++j) {
-                    if (c0 + j < tokens) *o = __float2bfloat16_rn(FMT == MOE_FMT_NVFP4 ? v[j] * s_alpha[c0 + j] : v[j]);
+                    if (c0 + j < tokens) *o = __float2bfloat16_rn(FMT == MOE_FMT_NVFP4 ? v[j] * last[j] : v[j]);
                     o += p.ldo;
                 }
             }
@@ -772,8 +808,8 @@ __global__ void __launch_bounds__(SplitCfg<FMT, BT, QUANT, DEEP>::THREADS, DEEP 
                 y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
             }
             if constexpr (FMT == MOE_FMT_NVFP4) {
-                const float alpha = s_alpha[first + i];
-                y.x *= alpha, y.y *= alpha, y.z *= alpha, y.w *= alpha;
+                const float alpha = s_alpha[first + i], rest = s_rest[first + i];
+                y.x = y.x * alpha * rest, y.y = y.y * alpha * rest, y.z = y.z * alpha * rest, y.w = y.w * alpha * rest;
             }
             __nv_bfloat16* o = out + i * p.ldo;
             const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);

@@ -67,3 +67,30 @@ def test_norm_gives_blocks_of_scale_zero_the_code_zero(pkg, residual):
     empty = sf == 0
     assert empty[:, 1].all() and int(empty.sum()) < empty.numel() // 2
     assert (codes[empty] == 0).all()
+
+
+@pytest.mark.parametrize("wexp", [-70, 0, 70])
+@pytest.mark.parametrize("M,N,K", [(1, 264, 544), (2, 520, 2080), (9, 264, 544), (60, 1032, 4096), (130, 264, 288),
+                                   (600, 8200, 96)])
+def test_products_of_very_small_and_large_rows(pkg, M, N, K, wexp):
+    """NVFP4 rows and weights at magnitudes where the product of their two scales leaves the normal range of
+    fp32 though the output does not. Tolerance as everywhere: half a bf16 step, and 2^-20 of the terms."""
+    from test_block_ops import assert_within, half_step
+    from oracle import formats as OF
+    rng = np.random.default_rng(M + N + K)
+    exps = np.linspace(-120, 100, M).round() if M > 2 else np.array([-108.0, 95.0])[:M]
+    x = bf16_dev(rng.standard_normal((M, K)) * 2.0 ** exps[:, None])
+    w = (rng.standard_normal((N, K)) * 2.0 ** wexp).astype(np.float32)
+    gs = OF.nvfp4_global_scale(np.abs(w).max()).reshape(1)
+    codes, sf = OF.nvfp4_quantize(w, gs)
+    wd = OF.nvfp4_dequantize(codes, sf, np.broadcast_to(gs, (N,)))
+    plan = pkg.LinearPlan(pkg.LinearConfig(N, K, M, "nvfp4"))
+    kw = plan.transform_weight(torch.from_numpy(codes).cuda(), torch.from_numpy(sf).cuda(),
+                               torch.from_numpy(gs.astype(np.float32)).cuda())
+    xc, xsf, xgs = oracle_quantize(f64(x), "nvfp4")
+    xd = OF.nvfp4_dequantize(xc, xsf, xgs)
+    want, terms = xd @ wd.T, np.abs(xd) @ np.abs(wd).T
+    seen = terms < 1e38  # larger outputs may overflow bf16
+    for rows in (x, pkg.quantize(x, "nvfp4")):
+        got = f64(plan.forward(rows, kw))
+        assert_within(got[seen], want[seen], (half_step(want) * 1.01 + 2.0 ** -20 * terms)[seen], "out")
