@@ -398,6 +398,10 @@ int moe_quantize(int32_t rows, int32_t K, const void* x, int64_t x_stride, const
  *                               is read before it is written); no other overlap
  *   gamma                       fp32 [H], applied verbatim
  *   H                           1 .. 16384; a multiple of 32 with q
+ * mean(z^2) is a sum in fp32: rows whose squares leave its range (|z| above some 2^60) give zeros. The
+ * order of that sum depends on H, the alignment and the number of rows (152 or fewer, or more): the
+ * same row in another batch may differ in y's last bits, and a code whose value lies at a rounding edge
+ * with them. Deterministic for the same call.
  */
 int moe_add_rmsnorm(int32_t rows, int32_t hidden, const void* x, int64_t x_stride, const void* residual,
                     int64_t residual_stride, const float* gamma, float eps, void* sum_out, int64_t sum_stride,
@@ -496,7 +500,11 @@ int moe_linear_workspace_size(moe_linear_plan_t plan, int32_t num_tokens, size_t
  * moe_linear_forward:            x bf16 [T, K], row stride x_stride: quantised by the call.
  * moe_linear_forward_quantized:  x already quantised (moe_quantize or moe_add_rmsnorm with
  *                                MOE_SF_ATOMS) in the plan's format.
- * out bf16 [T, N], row stride out_stride. Deterministic. T == 0 launches nothing.
+ * out bf16 [T, N], row stride out_stride; it overlaps neither x, the weight nor the workspace.
+ * Deterministic; the order of the sums over K depends on T (how many CTAs share them), so that a row
+ * may round otherwise in a batch of another size. The sums are fp32 values, for the MX formats with
+ * the block scales in them: terms below fp32's normal range may be lost there. T == 0 launches nothing.
+ * Every CTA writes a status word of its own at the workspace's start, so its contents do not matter.
  */
 int moe_linear_forward(moe_linear_plan_t plan, int32_t num_tokens, const void* x, int64_t x_stride,
                        const moe_linear_weight_t* weight, void* out, int64_t out_stride, void* workspace,

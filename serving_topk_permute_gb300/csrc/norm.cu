@@ -14,10 +14,11 @@
 // outside a row is written, nothing outside the matrix read.
 //
 // Memory bounds all of them once there are rows enough. Measured on GB300: 8192 x 7168 with a residual
-// to the sum and MXFP8 64.0 us (6.45 TB/s, 95% of the copy rate); 16 x 7168 2.7 us, the launch and one
-// trip to memory; 2999 x 2050 rows of 4-byte alignment 7.3 us (3.4 TB/s: four times the load and
-// store instructions). Quantisation alone of 8192 x 7168: MXFP8 27.2, MXFP4 24.0, NVFP4 28.5 us (6.5, 6.2 and
-// 5.3 TB/s).
+// to the sum and MXFP8 64.0 us (6.45 TB/s, 95% of the copy rate), MXFP4 59.4 and NVFP4 68.5 (their bytes
+// 56.6 and 57.2); 16 x 7168 2.7 us, the launch and one trip to memory; 2999 x 2050 rows of 4-byte alignment
+// 7.3 us (3.4 TB/s: a CTA loads a row, waits for it, reduces and stores, and the CTAs that fit make two to
+// three waves). Quantisation alone of 8192 x 7168: MXFP8 26.8, MXFP4 23.1, NVFP4 27.8 us (6.6, 6.5 and 5.4
+// TB/s).
 #include "block.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -308,8 +309,8 @@ __global__ void __launch_bounds__(MAXT, MIN_CTAS) norm_kernel(const NormArgs a, 
 
 // Quantisation alone, of aligned rows: thread t owns the 16-element units t, t + NT, ... (an NVFP4
 // block; two lanes make an MX block), and the magnitudes are taken on the packed bf16 pairs. This
-// takes half the instructions of the norm's path, which would otherwise bound it: 8192 x 7168 to
-// NVFP4 45.8 us through the norm's path.
+// takes fewer instructions than the norm's path, which would otherwise bound it: 8192 x 7168 to NVFP4,
+// MXFP4 and MXFP8 38.9, 29.6 and 31.2 us through the norm's path, 27.8, 23.1 and 26.8 so.
 template <int FMT, int MAXU, int MAXT, int MIN_CTAS>
 __global__ void __launch_bounds__(MAXT, MIN_CTAS) quant_kernel(const NormArgs a) {
     constexpr int S = fmt_sf_atoms(FMT), G = fmt_sf_block(FMT);
@@ -393,8 +394,9 @@ static cudaError_t norm_t(const NormArgs& a, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, norm_kernel<FMT, MAXC, MAXT, MIN_CTAS, RAGGED>, a, (uintptr_t)a.gamma % 16 == 0);
 }
 
-// Chunks per thread, measured on GB300 (MXFP8, residual): few rows finish soonest with one
-// (16 x 7168: 2.9 against 3.1 us with two); otherwise two up to 4096 elements (4096 x 4096 bf16:
+// Chunks per thread, measured on GB300 (MXFP8, residual): few rows, up to one for each of the 152 SMs,
+// finish soonest with one (16 x 7168: 2.5 against 3.3 us without this rule, 152 x 7168 2.7 and 3.5, but
+// 304 x 7168 4.8 and 4.1, 608 x 7168 10.0 and 6.5); otherwise two up to 4096 elements (4096 x 4096 bf16:
 // 22.3 against 23.6 us with four) and four above (8192 x 7168: 69.5 against 79.6 us with two),
 // where more would leave too few rows in flight.
 template <int FMT, bool RAGGED>
@@ -482,7 +484,8 @@ static cudaError_t quant_t(const NormArgs& a, cudaStream_t st) {
         at.config(dim3((unsigned)ceil_div(a.T, rows)), dim3((unsigned)threads, (unsigned)rows), 0, st);
     return cudaLaunchKernelEx(&cfg, quant_kernel<FMT, MAXU, MAXT, MIN_CTAS>, a);
 }
-// Units per thread: one for few rows, as in the norm. MX formats: two up to 6144 elements (8192 x 2048
+// Units per thread: one for few rows, as in the norm (152 x 7168 NVFP4 2.0 us against 2.2, 304 x 7168 2.7
+// and 2.5). MX formats: two up to 6144 elements (8192 x 2048
 // MXFP8 9.1 us, 9.9 with four), four above (8192 x 7168 27.2 and 27.3, MXFP4 24.0 and 24.6). NVFP4, whose
 // rows wait for their magnitude: four, so that there are fewer warps to join (8192 x 7168 28.5 us, 32.3
 // with two), but two where four would not fill a warp (16384 x 1024 9.8, 11.2 with four); seven CTAs
@@ -518,7 +521,9 @@ cudaError_t launch_norm(const NormArgs& args, cudaStream_t st) {
         case MOE_FMT_MXFP4: return ragged ? norm_f<MOE_FMT_MXFP4, true>(a, st) : norm_f<MOE_FMT_MXFP4, false>(a, st);
         default:
             // 4-byte pieces where they are whole: 4096 x 4098 with residual 27.8 us against 39.2 through
-            // the ragged variant (4096 x 4097: 39.6), 22.3 for aligned 4096 x 4096
+            // the ragged variant (4096 x 4097: 39.6), 22.3 for aligned 4096 x 4096. Five pairs a thread where
+            // 256 threads hold the row so: without a residual 2999 x 2050 7.3 us, with eight 9.4; 3000 x
+            // 2558 8.1 and 10.2; 3000 x 1026 4.9 and 5.6.
             if (ragged && bits % 4 == 0)
                 return a.H <= 2 * 5 * 256 ? norm_pairs<5, 256>(a, st) : norm_pairs<8, 1024>(a, st);
             return ragged ? norm_f<-1, true>(a, st) : norm_f<-1, false>(a, st);

@@ -25,9 +25,10 @@
 // atomics: every sum has a fixed order.
 //
 // Measured on GB300, 256 experts, fp32, the 8 largest. 32,768 tokens with the loss: 23.4 us, of which 2.5 are the
-// sums' (loss and counts left out: 21.9 with 34,048 tokens, 24.5 with). The bytes would take 5.3 us; instruction issue
-// bounds it: some 410 instructions a row, issued in 63% of the slots. Neither a row's loads one row
-// ahead (23.5 us) nor three CTAs of 40 registers on an SM (28.9) fill more of them. 128 tokens:
+// sums' (loss and counts left out: 21.9 with 34,048 tokens, 24.5 with). The bytes would take 5.3 us, the some 410
+// instructions a row at full issue about 11; they fill 63% of the slots. A warp has one row at a time, whose
+// k + 1 picks are a chain of dependent warp reductions, and 32 warps on an SM do not cover it. Neither a
+// row's loads one row ahead (23.5 us) nor three CTAs of 40 registers on an SM (28.9) help. 128 tokens:
 // 4.4 us, a cluster's launch and one row's chain of picks. The gradient of 32,768 tokens: 15.0 us,
 // 4.6 TB/s, 68% of the copy rate: loads that wait for the row before (one row ahead 15.3 to 16.6 us),
 // and issue, 65% of the slots.
@@ -37,6 +38,8 @@
 
 namespace moe {
 
+// SMs of the GPU this is built for. The number of CTAs is part of the sums' order and of the workspace's
+// size, which a caller may ask for without a GPU: a constant, not the device's answer.
 constexpr int SMS = 152;
 constexpr int ROUTER_WARPS = 16;
 constexpr int ROUTER_THREADS = 32 * ROUTER_WARPS;
@@ -160,7 +163,8 @@ struct Lanes {
     }
 };
 
-// 2^x, e^x and a / b to 2 ulp; results below 2^-126 are flushed to zero
+// 2^x and a / b to 2 ulp, e^x to some (2 + |x|) ulp, as the product x log2(e) is rounded; results below
+// 2^-126 are flushed to zero
 constexpr float LOG2E = 1.4426950408889634f;
 __device__ __forceinline__ float fast_exp2(float x) {
     float r;
@@ -472,7 +476,7 @@ __global__ void __launch_bounds__(ROUTER_THREADS, router_ctas(32 * C)) router_ke
 }
 
 // One cluster of JOIN_CTAS CTAs; CTA c takes every JOIN_CTAS-th group of 32 experts. Warp w of a
-// CTA adds the parts w, w + 16, ... of 32 experts (one in each lane), then the warps in order.
+// CTA adds the parts w, w + 32, ... of 32 experts (one in each lane), then the warps in order.
 __global__ void __launch_bounds__(JOIN_THREADS) router_join_kernel(const RouterArgs a, int parts) {
     constexpr int WARPS = JOIN_THREADS / 32;
     __shared__ int s_n[WARPS], s_c[WARPS][32];
