@@ -81,18 +81,18 @@ def _fail(fn: str, status: int):
     raise MoeError(fn, status)
 
 
-def _launch(fn, dev: int, *args) -> int:
+def _at_device(fn, dev: int):
     """The library's call with that device current: it launches on the current one, whatever device the
-    addresses belong to."""
-    if dev == _current_device():
-        return fn(*args)
-    with _device(dev):
-        return fn(*args)
+    addresses belong to. (Calls come here where another one is current.)"""
+    def call(*args):
+        with _device(dev):
+            return fn(*args)
+    return call
 
 
 def _stream(stream, dev: int) -> int:
-    """The given stream, or the current one of that device (its raw handle: a torch.cuda.Stream
-    object costs microseconds to make)."""
+    """The given stream's handle. Where none is given, calls take _raw_stream: a torch.cuda.Stream object
+    costs microseconds to make."""
     if stream is None:
         return _raw_stream(dev)
     if stream.device_index != dev:
@@ -162,9 +162,10 @@ def _set_once(self, name, value):
 
 
 def _places(tensors):
-    """Where the tensors' elements lie and how many there are: what resize_, set_, an assignment to
-    .data and a resized storage change behind a handle's back."""
-    return [(t.data_ptr(), t.numel()) for t in tensors]
+    """Calls that say where the tensors' elements lie and how many there are, and their answers: what
+    resize_, set_, an assignment to .data and a resized storage change behind a handle's back."""
+    ask = [method for t in tensors for method in (t.data_ptr, t.numel)]
+    return ask, [f() for f in ask]
 
 
 class Quantized:
@@ -190,8 +191,7 @@ class Quantized:
         self._dev = dev
         self.fmt, self.shape, self.sf_layout = fmt, torch.Size((rows, K)), sf_layout
         self.codes, self.sf, self.row_scale = codes, sf, row_scale
-        self._tensors = (codes, sf) if row_scale is None else (codes, sf, row_scale)
-        self._at = _places(self._tensors)
+        self._ask, self._at = _places((codes, sf) if row_scale is None else (codes, sf, row_scale))
         self._c = QuantC(FORMATS[fmt], SF_LAYOUTS[sf_layout], codes.data_ptr(), sf.data_ptr(),
                          None if row_scale is None else row_scale.data_ptr())
         self._ref = byref(self._c)
@@ -202,7 +202,7 @@ class Quantized:
         """The library's argument."""
         if self._dev != dev:
             raise ValueError(f"the Quantized is on cuda:{self._dev}, the other tensors are on cuda:{dev}")
-        if _places(self._tensors) != self._at:
+        if [f() for f in self._ask] != self._at:
             raise ValueError("a tensor of the Quantized was resized or given other memory: make a new one")
         return self._ref
 
@@ -226,8 +226,9 @@ def quantize(x: torch.Tensor, fmt: str, sf_layout: str = "atoms", out: Quantized
             out = Quantized.alloc(fmt, shape[0], shape[1], sf_layout, x.device)
     elif out.shape != shape or out.fmt != fmt:
         raise ValueError(f"out holds {out.fmt} {out.shape}, x is {tuple(shape)} for {fmt}")
-    st = _launch((_fns or _lib()).moe_quantize, dev, shape[0], shape[1], x.data_ptr(), ldx, out._arg(dev),
-                 _stream(stream, dev))
+    fn = (_fns or _lib()).moe_quantize
+    call = fn if dev == _current_device() else _at_device(fn, dev)
+    st = call(shape[0], shape[1], x.data_ptr(), ldx, out._arg(dev), _stream(stream, dev))
     if st:
         _fail("moe_quantize", st)
     return out
@@ -264,8 +265,9 @@ def add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, residua
         if quantized.shape != shape:
             raise ValueError(f"quantized holds {quantized.shape}, x is {tuple(shape)}")
         pq = quantized._arg(dev)
-    st = _launch((_fns or _lib()).moe_add_rmsnorm, dev, rows, H, x.data_ptr(), ldx, pr, ldr, gamma.data_ptr(), eps, ps,
-                 lds, po, ldo, pq, _stream(stream, dev))
+    fn = (_fns or _lib()).moe_add_rmsnorm
+    call = fn if dev == _current_device() else _at_device(fn, dev)
+    st = call(rows, H, x.data_ptr(), ldx, pr, ldr, gamma.data_ptr(), eps, ps, lds, po, ldo, pq, _stream(stream, dev))
     if st:
         _fail("moe_add_rmsnorm", st)
     return out if out is not None else quantized
@@ -298,6 +300,9 @@ class RouterOutput:
         self.__dict__[name] = value
         self.__dict__["_args"] = None  # checked again by the next forward
 
+    def __getstate__(self):
+        return {**self.__dict__, "_args": None}  # a copy's buffers are its own
+
     def _check(self, T: int, E: int, k: int, dev: int):
         """The library's arguments for T tokens, after checks that hold while the buffers stay where they are."""
         _flat("topk_ids", self.topk_ids, _I32, T * k, dev)
@@ -314,7 +319,7 @@ class RouterOutput:
         if any(t.data_ptr() == 0 and t.numel() for t in there):
             raise ValueError("a buffer of the RouterOutput has no memory")
         ptr = [None if t is None else t.data_ptr() for t in all_of]
-        self.__dict__["_args"] = ((T, E, k, dev), (*ptr, self.workspace.numel()), there, _places(there))
+        self.__dict__["_args"] = ((T, E, k, dev), (*ptr, self.workspace.numel()), *_places(there))
 
 
 class Router:
@@ -382,11 +387,12 @@ class Router:
                 out = self.alloc(T, training, logits.device)
         o = out
         args = o._args
-        if args is None or args[0] != (T, E, k, dev) or _places(args[2]) != args[3]:
+        if args is None or args[0] != (T, E, k, dev) or [f() for f in args[2]] != args[3]:
             o._check(T, E, k, dev)
             args = o._args
-        st = _launch(_fns.moe_router_forward, dev, self._ref[logits.dtype], T, logits.data_ptr(), ld, mask, *args[1],
-                     _stream(stream, dev))
+        fn = _fns.moe_router_forward
+        call = fn if dev == _current_device() else _at_device(fn, dev)
+        st = call(self._ref[logits.dtype], T, logits.data_ptr(), ld, mask, *args[1], _stream(stream, dev))
         if st:
             _fail("moe_router_forward", st)
         return o
@@ -415,8 +421,10 @@ class Router:
             _flat("counts", counts, _I32, E, dev)
             _flat("num_valid", num_valid, _I32, 1, dev)
             pl, pc, pn = d_loss.data_ptr(), counts.data_ptr(), num_valid.data_ptr()
-        st = _launch(_fns.moe_router_backward, dev, self._ref[logits.dtype], T, logits.data_ptr(), ld, mask,
-                     topk_ids.data_ptr(), pc, pn, pw, pl, out.data_ptr(), ldo, _stream(stream, dev))
+        fn = _fns.moe_router_backward
+        call = fn if dev == _current_device() else _at_device(fn, dev)
+        st = call(self._ref[logits.dtype], T, logits.data_ptr(), ld, mask, topk_ids.data_ptr(), pc, pn, pw, pl,
+                  out.data_ptr(), ldo, _stream(stream, dev))
         if st:
             _fail("moe_router_backward", st)
         return out
@@ -459,8 +467,7 @@ class LinearWeight:
         self.codes, self.sf, self.global_scale = codes, sf, global_scale
         self.fmt, self.shape = fmt, None if shape is None else tuple(shape)
         self._bytes = (codes.numel(), sf.numel(), global_scale is not None)
-        self._tensors = (codes, sf) if global_scale is None else (codes, sf, global_scale)
-        self._at = _places(self._tensors)
+        self._ask, self._at = _places((codes, sf) if global_scale is None else (codes, sf, global_scale))
         self._c = LinearWeightC(codes.data_ptr(), sf.data_ptr(),
                                 None if global_scale is None else global_scale.data_ptr())
         self._ref = byref(self._c)
@@ -469,7 +476,7 @@ class LinearWeight:
         """The library's argument."""
         if self._dev != dev:
             raise ValueError(f"the weight is on cuda:{self._dev}, the plan is for cuda:{dev}")
-        if _places(self._tensors) != self._at:
+        if [f() for f in self._ask] != self._at:
             raise ValueError("a tensor of the LinearWeight was resized or given other memory: make a new one")
         return self._ref
 
@@ -525,8 +532,9 @@ class LinearPlan:
             dst = LinearWeight(codes, torch.empty(self._weight_bytes[1], dtype=torch.uint8, device=codes.device),
                                global_scale, fmt, (N, K))
         src = LinearWeightC(codes.data_ptr(), sf.data_ptr(), None if global_scale is None else global_scale.data_ptr())
-        st = _launch(_lib().moe_linear_transform_weight, self._dev, self._h, byref(src), byref(dst._c),
-                     _stream(stream, self._dev))
+        fn = _lib().moe_linear_transform_weight
+        call = fn if self._dev == _current_device() else _at_device(fn, self._dev)
+        st = call(self._h, byref(src), byref(dst._c), _stream(stream, self._dev))
         if st != MOE_OK:
             _fail("moe_linear_transform_weight", st)
         return dst
@@ -562,11 +570,15 @@ class LinearPlan:
             raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{dev}")
         s = _stream(stream, dev)
         if quantized:
-            st = _launch(_fns.moe_linear_forward_quantized, dev, self._h, T, x._arg(dev), weight._arg(dev),
-                         out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(), s)
+            fn = _fns.moe_linear_forward_quantized
+            call = fn if dev == _current_device() else _at_device(fn, dev)
+            st = call(self._h, T, x._arg(dev), weight._arg(dev), out.data_ptr(), ldo, workspace.data_ptr(),
+                      workspace.numel(), s)
         else:
-            st = _launch(_fns.moe_linear_forward, dev, self._h, T, x.data_ptr(), ldx, weight._arg(dev), out.data_ptr(),
-                         ldo, workspace.data_ptr(), workspace.numel(), s)
+            fn = _fns.moe_linear_forward
+            call = fn if dev == _current_device() else _at_device(fn, dev)
+            st = call(self._h, T, x.data_ptr(), ldx, weight._arg(dev), out.data_ptr(), ldo, workspace.data_ptr(),
+                      workspace.numel(), s)
         if st:
             _fail("moe_linear_forward", st)
         return out
@@ -583,10 +595,11 @@ class LinearPlan:
         least = self.workspace_size(0)  # the status words lie at its start, as many for every number of tokens
         if workspace.get_device() != self._dev or workspace.dtype is not _U8 or not workspace.is_contiguous() or \
                 workspace.numel() < least:
-            raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {least} bytes on cuda:{self._dev}, "
-                             f"got {workspace.numel()} {workspace.dtype} on {workspace.device}")
-        st = _launch(_lib().moe_linear_last_status, self._dev, self._h, workspace.data_ptr(),
-                     _stream(stream, self._dev), byref(v))
+            raise ValueError(f"workspace must be a contiguous uint8 tensor of {least} bytes or more on "
+                             f"cuda:{self._dev}, got {workspace.numel()} {workspace.dtype} on {workspace.device}")
+        fn = _lib().moe_linear_last_status
+        call = fn if self._dev == _current_device() else _at_device(fn, self._dev)
+        st = call(self._h, workspace.data_ptr(), _stream(stream, self._dev), byref(v))
         if st != MOE_OK:
             _fail("moe_linear_last_status", st)
         return v.value

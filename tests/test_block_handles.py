@@ -1,5 +1,6 @@
 """What the handles of the operators around the experts refuse on the host, before any launch: stand-ins
 take the place of the library and of device tensors, so no GPU is needed."""
+import copy
 import dataclasses
 from contextlib import contextmanager
 
@@ -234,6 +235,18 @@ def test_a_router_passes_on_what_is_left_of_its_workspace(library):
     o.workspace.shape = torch.Size((512,))
     router.forward(logits, out=o)
     assert library.launches()[-1][1][12] == 512  # which the library then refuses if it is too small
+
+
+def test_a_copied_router_output_writes_its_own_buffers(library):
+    router, o, logits = pkg.Router(pkg.RouterConfig(8, 2)), router_output(), Tensor((5, 8), F32)
+    router.forward(logits, out=o)
+    twin = copy.deepcopy(o)
+    for b in BUFFERS:
+        moved(getattr(twin, b))
+    router.forward(logits, out=twin)
+    assert list(library.launches()[-1][1][5:12]) == [getattr(twin, b).data_ptr() for b in BUFFERS]
+    router.forward(logits, out=o)
+    assert list(library.launches()[-1][1][5:12]) == [getattr(o, b).data_ptr() for b in BUFFERS]
 
 
 def quantized(T=4, K=128, fmt="nvfp4", device=0):
