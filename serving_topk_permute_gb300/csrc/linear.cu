@@ -21,7 +21,8 @@
 //
 // Measured on GB300: 4096 x 8192 x 4096 MXFP8 in 78 us (3.5 PFLOP/s, twice the chip's sustained bf16
 // rate: power-bound; 2.2 PFLOP/s before the issuing loops ran converged), 8192 x 7168 x 7168 NVFP4 in
-// 123 us (6.8 PFLOP/s) after 28 us of quantisation; with every operand load taken out it takes 113.
+// 121 us (7.0 PFLOP/s) after 28 us of quantisation; with every operand load taken out it takes 113, the rate
+// of the K = 64 MMAs that it issues.
 // Where one wave of tiles does it, the fixed steps count: 1024 x 4096 x 4096 NVFP4 9.9 us, of which 0.8
 // until the first stage has landed, 0.3 for each of 16 stages (the MMAs alone 0.27), 0.6 until the
 // last one is through, 1.6 to store a tile and 0.7 to leave.
