@@ -210,7 +210,7 @@ def work(case):
         if c["op"] == "route":
             moved = T * row + 8 * T * k + 4 * E + (T if c["mask"] else 0) + (4 * E if c["bias"] else 0)
             return {"bytes": moved, "flops": 5 * T * E}
-        dense = c["score"] == "softmax"
+        dense = c["score"] == "softmax" and not c["renorm"]  # else only the picked logits have a gradient
         return {"bytes": T * row * (2 if dense else 1) + T * k * (8 if dense else 8 + row // E),
                 "flops": T * (6 * E if dense else 8 * k)}
     if c["op"] == "norm":
