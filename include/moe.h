@@ -459,6 +459,67 @@ int moe_router_backward(const moe_router_config_t* cfg, int32_t num_tokens, cons
                         int64_t d_logits_stride, void* stream);
 
 /*
+ * Score router: scores s = sigmoid(logits) or softmax(logits), and c = s + bias, by which experts are
+ * chosen: the top_groups of num_groups equal, consecutive groups by their largest c or by the sum of
+ * their two largest (of the one, where no second may be taken; ties to the lowest group), and among
+ * their experts the top_k by descending c (ties to the lowest id). Weights are scale * s, without
+ * the bias, or scale * s / sum of the chosen s (renormalize).
+ * The order is that of the exact scores: rows where 32 bits leave it open are decided with scores good to
+ * some 2^-44, and only values nearer than 2^-40 that come from different logits or biases may be taken
+ * in either order. Without a bias, and when all biases are equal, experts are ordered by their logits.
+ * A token is not valid when its mask byte is 0 or no expert may be taken: its ids are -1, its
+ * weights 0, and it adds to no count. An expert whose logit or bias is -inf is never taken; slots left
+ * over get id -1, weight 0. A NaN logit or bias sorts above every number; weights that a NaN
+ * score, or with softmax a +inf logit, goes into are NaN, ids stay in range and distinct.
+ */
+#define MOE_SCORE_SIGMOID 0
+#define MOE_SCORE_SOFTMAX 1
+#define MOE_GROUP_MAX  0
+#define MOE_GROUP_TOP2 1
+typedef struct moe_score_router_config {
+    int32_t num_experts;     /* 1 .. 512 */
+    int32_t top_k;           /* 1 .. min(32, top_groups * num_experts / num_groups) */
+    int32_t score;           /* MOE_SCORE_* */
+    int32_t num_groups;      /* 1 .. 32, divides num_experts (1: no groups) */
+    int32_t top_groups;      /* 1 .. num_groups */
+    int32_t group_score;     /* MOE_GROUP_* */
+    int32_t renormalize;     /* 0 or 1 */
+    int32_t logits_type;     /* MOE_LOGITS_* of logits and of their gradient */
+    float   scale;           /* finite */
+} moe_score_router_config_t;
+
+/* Bytes of the workspace of moe_score_router_forward for num_tokens tokens (never 0). Host-only. */
+int moe_score_router_workspace_size(const moe_score_router_config_t* cfg, int32_t num_tokens, size_t* bytes);
+
+/*
+ *   logits        [T, E], row stride logits_stride elements
+ *   bias          fp32 [E] or NULL
+ *   token_mask    u8 [T] (0: not valid) or NULL
+ *   topk_ids      int32 [T, k], topk_weights fp32 [T, k], contiguous
+ *   counts        int32 [E], num_valid int32 [1]: each may be NULL; without both no workspace is needed
+ * Deterministic. The workspace's contents do not matter.
+ */
+int moe_score_router_forward(const moe_score_router_config_t* cfg, int32_t num_tokens, const void* logits,
+                             int64_t logits_stride, const float* bias, const uint8_t* token_mask, int32_t* topk_ids,
+                             float* topk_weights, int32_t* counts, int32_t* num_valid, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * d_logits [T, E] (stride d_logits_stride) of sum(d_weights * topk_weights); the choice of experts is held
+ * constant, the bias has no gradient.
+ *   topk_ids    as moe_score_router_forward wrote them (a row's ids are distinct or -1; an id outside
+ *               [-1, E) counts as -1). Rows without an id get zeros, whatever their logits hold.
+ *   d_weights   fp32 [T, k]
+ *   d_logits    does not overlap logits
+ */
+int moe_score_router_backward(const moe_score_router_config_t* cfg, int32_t num_tokens, const void* logits,
+                              int64_t logits_stride, const int32_t* topk_ids, const float* d_weights, void* d_logits,
+                              int64_t d_logits_stride, void* stream);
+
+/* One step towards even loads: bias[e] += rate * sign(mean of counts - counts[e]) for num_experts experts. */
+int moe_score_router_update_bias(int32_t num_experts, const int32_t* counts, float rate, float* bias, void* stream);
+
+/*
  * Linear product in a microscaled format: out[t, n] = bf16(sum_k x[t, k] W[n, k]), with x
  * quantised in the weight's format (MXFP8, NVFP4 or MXFP4) and fp32 accumulation on the tensor
  * cores. out_features 1 .. 2^20, in_features a multiple of 32 up to 16384, max_tokens >= 1.

@@ -4,3 +4,4 @@ from .block import (LinearConfig, LinearPlan, LinearWeight, Quantized, Router, R
                     RouterOutput, add_rmsnorm, linear_validate, quantize, sf_size)
 from .moe import (FORMATS, LayerConfig, MoeError, Plan, config_workspace_size, error_string,  # noqa: F401
                   lib, library_path, permute_noalloc, validate)
+from .score_router import ScoreRouter, ScoreRouterConfig  # noqa: F401

@@ -77,6 +77,22 @@ def _lib():
     return _fns
 
 
+def declare(signatures):
+    """The library with these functions declared, as a function that loads it at its first call."""
+    done = []
+
+    def get():
+        if not done:
+            L = _lib()
+            for name, args in signatures.items():
+                fn = getattr(L, name)
+                fn.argtypes = args
+                fn.restype = ctypes.c_int
+            done.append(L)
+        return done[0]
+    return get
+
+
 def _fail(fn: str, status: int):
     raise MoeError(fn, status)
 

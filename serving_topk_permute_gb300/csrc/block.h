@@ -64,10 +64,48 @@ struct RouterGradArgs {
     const float* dloss;
     void* dlogits;
     int64_t ldd;
+    float dw_scale;   // factor of dw
+    int empty_zero;   // rows without any id get zeros, whatever their logits hold
 };
 int router_grid(int T, int E);  // CTAs that leave partial sums in the workspace
 cudaError_t launch_router(const RouterArgs& a, cudaStream_t st);
 cudaError_t launch_router_grad(const RouterGradArgs& a, cudaStream_t st);
+
+// ------------------------------------------------------------------ score router
+constexpr int SCORE_MAX_EXPERTS = 512;
+constexpr int SCORE_MAX_GROUPS = 32;
+struct ScoreArgs {
+    const void* logits;
+    int64_t ld;
+    int bf16;
+    const float* bias;       // or null
+    const uint8_t* mask;     // or null
+    int T, E, k, sigmoid, groups, top_groups, top2, renorm;
+    float scale;
+    int32_t* ids;
+    float* w;
+    int32_t* counts;         // or null
+    int32_t* num_valid;      // or null
+    int32_t* part_counts;    // [score_grid][E] when counts are joined by a second kernel
+    int32_t* part_valid;     // [score_grid]
+    // a group's lanes (set by launch_score_router): 1 << lane_bits of them, per experts each
+    int lane_bits, per, group_size;
+};
+struct ScoreGradArgs {
+    const void* logits;
+    int64_t ld;
+    int bf16;
+    int T, E, k, sigmoid, renorm;
+    float scale;
+    const int32_t* ids;
+    const float* dw;
+    void* dlogits;
+    int64_t ldd;
+};
+int score_grid(int T, int E);  // CTAs that leave partial counts in the workspace
+cudaError_t launch_score_router(const ScoreArgs& a, cudaStream_t st);
+cudaError_t launch_score_grad(const ScoreGradArgs& a, cudaStream_t st);  // weights whose gradient is sparse
+cudaError_t launch_score_bias(const int32_t* counts, float* bias, int E, float rate, cudaStream_t st);
 
 // ------------------------------------------------------------------ linear product
 struct LinearArgs {

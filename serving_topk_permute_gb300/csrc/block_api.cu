@@ -114,6 +114,22 @@ int check_router(const moe_router_config_t* c) {
     return MOE_OK;
 }
 
+int check_score_router(const moe_score_router_config_t* c) {
+    if (!c) return MOE_ERR_INVALID_ARG;
+    if (c->num_experts < 1 || c->num_experts > MAX_EXPERTS) return MOE_ERR_INVALID_ARG;
+    if (c->score != MOE_SCORE_SIGMOID && c->score != MOE_SCORE_SOFTMAX) return MOE_ERR_UNSUPPORTED;
+    if (c->group_score != MOE_GROUP_MAX && c->group_score != MOE_GROUP_TOP2) return MOE_ERR_UNSUPPORTED;
+    if (c->num_groups < 1 || c->num_groups > SCORE_MAX_GROUPS || c->num_experts % c->num_groups)
+        return MOE_ERR_INVALID_ARG;
+    if (c->top_groups < 1 || c->top_groups > c->num_groups) return MOE_ERR_INVALID_ARG;
+    if (c->top_k < 1 || c->top_k > MAX_TOP_K || c->top_k > c->top_groups * (c->num_experts / c->num_groups))
+        return MOE_ERR_INVALID_ARG;
+    if (c->renormalize != 0 && c->renormalize != 1) return MOE_ERR_INVALID_ARG;
+    if (c->logits_type != MOE_LOGITS_F32 && c->logits_type != MOE_LOGITS_BF16) return MOE_ERR_UNSUPPORTED;
+    if (!isfinite(c->scale)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
 // workspace of the product: the CTAs' status words at its start (as many for every T), then the
 // quantised activations
 struct LinLayout {
@@ -359,7 +375,121 @@ int moe_router_backward(const moe_router_config_t* cfg, int32_t num_tokens, cons
     a.dloss = d_loss;
     a.dlogits = d_logits;
     a.ldd = d_logits_stride;
+    a.dw_scale = 1.0f;
     CUDA_TRY(launch_router_grad(a, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+// ------------------------------------------------------------------ score router
+int moe_score_router_workspace_size(const moe_score_router_config_t* cfg, int32_t num_tokens, size_t* bytes) {
+    const int v = check_score_router(cfg);
+    if (v != MOE_OK) return v;
+    if (!bytes || num_tokens < 0) return MOE_ERR_INVALID_ARG;
+    const int64_t g = score_grid(num_tokens, cfg->num_experts);
+    const int64_t need = align_up(4 * g * cfg->num_experts, 256) + align_up(4 * g, 256);
+    *bytes = (size_t)(need > 256 ? need : 256);  // never none: one rule for every size
+    return MOE_OK;
+}
+
+int moe_score_router_forward(const moe_score_router_config_t* cfg, int32_t num_tokens, const void* logits,
+                             int64_t logits_stride, const float* bias, const uint8_t* token_mask, int32_t* topk_ids,
+                             float* topk_weights, int32_t* counts, int32_t* num_valid, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    const int v = check_score_router(cfg);
+    if (v != MOE_OK) return v;
+    if (num_tokens < 0) return MOE_ERR_INVALID_ARG;
+    const int T = num_tokens, E = cfg->num_experts;
+    const uintptr_t el = cfg->logits_type == MOE_LOGITS_BF16 ? 2 : 4;
+    if (T > 0 && (!logits || !topk_ids || !topk_weights)) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(logits, el) || (T > 1 && logits_stride < E)) return MOE_ERR_INVALID_ARG;
+    for (const void* q : {(const void*)bias, (const void*)topk_ids, (const void*)topk_weights, (const void*)counts,
+                          (const void*)num_valid})
+        if (!aligned_to(q, 4)) return MOE_ERR_INVALID_ARG;
+    ScoreArgs a{};
+    a.logits = logits;
+    a.ld = logits_stride;
+    a.bf16 = cfg->logits_type == MOE_LOGITS_BF16;
+    a.bias = bias;
+    a.mask = token_mask;
+    a.T = T;
+    a.E = E;
+    a.k = cfg->top_k;
+    a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
+    a.groups = cfg->num_groups;
+    a.top_groups = cfg->top_groups;
+    a.top2 = cfg->group_score == MOE_GROUP_TOP2;
+    a.renorm = cfg->renormalize;
+    a.scale = cfg->scale;
+    a.ids = topk_ids;
+    a.w = topk_weights;
+    a.counts = counts;
+    a.num_valid = num_valid;
+    if (counts || num_valid) {
+        size_t need = 0;
+        moe_score_router_workspace_size(cfg, T, &need);
+        if (workspace && workspace_bytes < need) return MOE_ERR_WORKSPACE;
+        if (!workspace || !aligned_to(workspace, 256)) return MOE_ERR_INVALID_ARG;
+        uint8_t* ws = (uint8_t*)workspace;
+        a.part_counts = (int32_t*)ws;
+        a.part_valid = (int32_t*)(ws + align_up(4 * (int64_t)score_grid(T, E) * E, 256));
+    }
+    CUDA_TRY(launch_score_router(a, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+int moe_score_router_backward(const moe_score_router_config_t* cfg, int32_t num_tokens, const void* logits,
+                              int64_t logits_stride, const int32_t* topk_ids, const float* d_weights, void* d_logits,
+                              int64_t d_logits_stride, void* stream) {
+    const int v = check_score_router(cfg);
+    if (v != MOE_OK) return v;
+    if (num_tokens < 0) return MOE_ERR_INVALID_ARG;
+    if (num_tokens == 0) return MOE_OK;
+    const int T = num_tokens, E = cfg->num_experts;
+    const uintptr_t el = cfg->logits_type == MOE_LOGITS_BF16 ? 2 : 4;
+    if (!logits || !topk_ids || !d_weights || !d_logits || logits == d_logits) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(logits, el) || !aligned_to(d_logits, el) || !aligned_to(topk_ids, 4) || !aligned_to(d_weights, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (T > 1 && (logits_stride < E || d_logits_stride < E)) return MOE_ERR_INVALID_ARG;
+    if (cfg->score == MOE_SCORE_SOFTMAX && !cfg->renormalize) {
+        // every expert has a gradient: the softmax router's, of scaled weights
+        RouterGradArgs a{};
+        a.logits = logits;
+        a.ld = logits_stride;
+        a.bf16 = cfg->logits_type == MOE_LOGITS_BF16;
+        a.T = T;
+        a.E = E;
+        a.k = cfg->top_k;
+        a.ids = topk_ids;
+        a.dw = d_weights;
+        a.dlogits = d_logits;
+        a.ldd = d_logits_stride;
+        a.dw_scale = cfg->scale;
+        a.empty_zero = 1;
+        CUDA_TRY(launch_router_grad(a, (cudaStream_t)stream));
+        return MOE_OK;
+    }
+    ScoreGradArgs a{};
+    a.logits = logits;
+    a.ld = logits_stride;
+    a.bf16 = cfg->logits_type == MOE_LOGITS_BF16;
+    a.T = T;
+    a.E = E;
+    a.k = cfg->top_k;
+    a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
+    a.renorm = cfg->renormalize;
+    a.scale = cfg->scale;
+    a.ids = topk_ids;
+    a.dw = d_weights;
+    a.dlogits = d_logits;
+    a.ldd = d_logits_stride;
+    CUDA_TRY(launch_score_grad(a, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+int moe_score_router_update_bias(int32_t num_experts, const int32_t* counts, float rate, float* bias, void* stream) {
+    if (num_experts < 1 || num_experts > MAX_EXPERTS || !isfinite(rate)) return MOE_ERR_INVALID_ARG;
+    if (!counts || !bias || !aligned_to(counts, 4) || !aligned_to(bias, 4)) return MOE_ERR_INVALID_ARG;
+    CUDA_TRY(launch_score_bias(counts, bias, num_experts, rate, (cudaStream_t)stream));
     return MOE_OK;
 }
 

@@ -35,12 +35,10 @@
 #include "block.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "router.cuh"
 
 namespace moe {
 
-// SMs of the GPU this is built for. The number of CTAs is part of the sums' order and of the workspace's
-// size, which a caller may ask for without a GPU: a constant, not the device's answer.
-constexpr int SMS = 152;
 constexpr int ROUTER_WARPS = 16;
 constexpr int ROUTER_THREADS = 32 * ROUTER_WARPS;
 // CTAs on an SM, the whole grid resident at once. 16 experts a lane: one CTA's registers fill the SM
@@ -58,28 +56,8 @@ constexpr int JOIN_THREADS = 1024;
 constexpr int CLUSTER_WARPS = 16;
 constexpr int CLUSTER_TOKENS = 512;
 
-// Unsigned keys in the order of the floats: -inf < ... < +inf < NaN. The addition makes -0 a +0
-// and any NaN the canonical, positive one (0x7FFFFFFF), whose key is the largest.
-__device__ __forceinline__ uint32_t order_key(float v) {
-    const uint32_t u = __float_as_uint(__fadd_rn(v, 0.0f));
-    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-}
-constexpr uint32_t KEY_NEG_INF = 0x007FFFFFu;  // order_key(-inf): the lowest key of a logit
-constexpr uint32_t KEY_NAN = 0xFFFFFFFFu;
-__device__ __forceinline__ float key_value(uint32_t k) {
-    if (k == KEY_NAN) return __uint_as_float(0x7FC00000u);
-    return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
-}
 constexpr uint32_t ID_BITS = 511u;              // E <= 512
 constexpr uint32_t PACKED_FINITE = 0x00800000u;  // packed keys below hold -inf, or no expert
-
-template <bool BF16>
-__device__ __forceinline__ float logit_at(const void* p, int64_t i) {
-    if constexpr (BF16)
-        return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
-    else
-        return reinterpret_cast<const float*>(p)[i];
-}
 
 // Experts of a lane: W consecutive ones (one vector access) every 32 W. MODE 0: W = 1, where rows
 // are not aligned for more; 1: vector accesses; 2: vector accesses and E = 32 C, no bounds.
@@ -162,28 +140,6 @@ struct Lanes {
         }
     }
 };
-
-// 2^x and a / b to 2 ulp, e^x to some (2 + |x|) ulp, as the product x log2(e) is rounded; results below
-// 2^-126 are flushed to zero
-constexpr float LOG2E = 1.4426950408889634f;
-__device__ __forceinline__ float fast_exp2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float fast_exp(float x) { return fast_exp2(x * LOG2E); }
-__device__ __forceinline__ float fast_div(float a, float b) { return __fdividef(a, b); }
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
 
 // both sums: the lower 16 lanes add the first one up, the upper ones the second
 __device__ __forceinline__ void warp_sums(float& a, float& b, int lane) {
@@ -606,6 +562,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, grad_ctas(C)) router_grad_kernel
             id = a.ids[t * a.k + lane];
             dw = a.dw[t * a.k + lane];
             if ((unsigned)id >= (unsigned)a.E) id = -1;
+            dw *= a.dw_scale;
             if (id >= 0) {
                 l = logit_at<BF16>(a.logits, t * a.ld + id);
                 own = a.dloss ? c0 * (float)(a.counts[id] - mean) : 0.0f;
@@ -613,7 +570,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, grad_ctas(C)) router_grad_kernel
         }
         const bool masked = a.mask && a.mask[t] == 0;
         const float top = row_max<C>(v);
-        const bool valid = !masked && top != -inf;  // warp-uniform
+        bool valid = !masked && top != -inf;  // warp-uniform
+        if (a.empty_zero) valid = valid && __any_sync(0xffffffffu, id >= 0);
         float sel = 0.0f;
         if (valid) {
             float sum = 0.0f;

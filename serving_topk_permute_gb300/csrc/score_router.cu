@@ -1,0 +1,853 @@
+// score_router.cu -- routing by scores with a selection bias and expert groups
+// (moe_score_router_forward), the gradient of its weights (moe_score_router_backward) and the step of
+// the bias (moe_score_router_update_bias).
+//
+//   s = sigmoid(l) or softmax(l),  c = s + b,  a group's value: its largest c, or the sum of its two largest
+//   the top_groups groups (ties to the lower group), among their experts the k largest c (ties to the
+//   lower id),  w = scale s[ids] (/ their sum)
+//   dl_j = scale (1 - s_j) W_j (dw_j - sum_i W_i dw_i), W = s / sum s (sigmoid; softmax without the
+//   factor 1 - s_j: over the picked logits it is a softmax itself), or scale s_j (1 - s_j) dw_j where the
+//   weights are not divided by their sum; all other experts 0
+//
+// One warp per token row. A group lies in L = 32 / (number of groups, rounded up to a power of two)
+// neighbouring lanes, C consecutive experts in each, so that ids ascend with the lanes and a
+// group's two largest are joined in log2 L steps.
+//
+// Which experts. The order is that of the exact scores, which 32 bits do not always show. Values become
+// integer keys with the id below them; a pick is the warp's maximum of the lanes' largest. After the
+// picks, values next to each other in the order (the k-th and the next one, the last group taken and the
+// first one left among them) have to be further apart than the error of their computation; where two
+// are not, the warp decides again with scores of some 45 bits: 0.2% of the rows of 256 sigmoid scores with
+// a bias. Without a bias, or when all biases are equal, the order is that of the logits.
+//
+// Measured on GB300, 256 experts in 8 groups, a bias, fp32: 16,384 tokens 18.0 us (the bytes would take 2.6),
+// of which 2.5 are the counts' and 0.7 the rows decided again; 64 tokens 4.9 us. A row takes some 600
+// instructions, 290 of them on the half-rate integer pipe, which bounds it: 32 warps of an SM keep it 55%
+// busy. Three CTAs on an SM (42 registers) spill: 22 us.
+//
+// Counts are integers: a CTA counts in shared memory; up to 128 tokens run as one cluster that joins
+// through distributed shared memory, more leave a row of counts for each CTA to a second kernel.
+#include "block.h"
+#include "common.cuh"
+#include "kernels.h"
+#include "router.cuh"
+
+namespace moe {
+
+constexpr int SCORE_WARPS = 16;
+constexpr int SCORE_THREADS = 32 * SCORE_WARPS;
+constexpr int SCORE_CLUSTER_TOKENS = 128;  // 128 x 256: 5.7 us so, 513 x 256: 6.5 us the other way, 11.5 so
+constexpr uint32_t KEY_FINITE = 0x00800000u;  // ordered keys below: -inf
+constexpr int score_ctas(int C) { return C > 8 ? 1 : 2; }
+
+// this lane's experts: [first, first + count)
+struct LaneExperts {
+    int first, count, group;
+    __device__ __forceinline__ LaneExperts(const ScoreArgs& a, int lane) {
+        group = lane >> a.lane_bits;
+        const int at = (lane & ((1 << a.lane_bits) - 1)) * a.per;
+        first = group * a.group_size + at;
+        count = group < a.groups ? max(0, min(a.per, a.group_size - at)) : 0;
+    }
+};
+
+// The row's logits of this lane, -inf where it has none. VEC: every lane has C experts and rows start on
+// 16-byte boundaries.
+template <bool BF16, int C, bool VEC>
+__device__ __forceinline__ void load_row(const ScoreArgs& a, int64_t row, const LaneExperts& x, float (&l)[C]) {
+    if constexpr (VEC && BF16) {
+        const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(a.logits) + row + x.first;
+        uint32_t w[C / 2];
+        if constexpr (C >= 8) {
+#pragma unroll
+            for (int i = 0; i < C / 8; ++i) {
+                const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+            }
+        } else if constexpr (C == 4) {
+            const uint2 q = *reinterpret_cast<const uint2*>(p);
+            w[0] = q.x, w[1] = q.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        }
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) {
+            l[2 * i] = __uint_as_float(w[i] << 16);
+            l[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else if constexpr (VEC) {
+        const float* p = reinterpret_cast<const float*>(a.logits) + row + x.first;
+        if constexpr (C >= 4) {
+#pragma unroll
+            for (int i = 0; i < C / 4; ++i) {
+                const float4 q = reinterpret_cast<const float4*>(p)[i];
+                l[4 * i] = q.x, l[4 * i + 1] = q.y, l[4 * i + 2] = q.z, l[4 * i + 3] = q.w;
+            }
+        } else {
+            const float2 q = *reinterpret_cast<const float2*>(p);
+            l[0] = q.x, l[1] = q.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            l[i] = i < x.count ? logit_at<BF16>(a.logits, row + x.first + i) : -__int_as_float(0x7F800000);
+    }
+}
+
+__device__ __forceinline__ float fast_rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// within 2^-21.8 of the sigmoid: the argument's rounding 0.34 2^-24 (s (1 - s) |l| <= 0.224), 2 ulp of
+// the exponential times s (1 - s), the sum's rounding and 1 ulp of the reciprocal
+__device__ __forceinline__ float fast_sigmoid(float l) { return fast_rcp(1.0f + fast_exp2(-LOG2E * l)); }
+// ------------------------------------------------------------------ scores of some 45 bits
+// Sums of two floats, the second at most half an ulp of the first (Dekker, 1971). FP64 would do, at
+// 1/64 of the rate of fp32: one row decided so took 30 us, as long as thousands of others.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {  // exact (Knuth)
+    const float s = __fadd_rn(a, b), t = __fadd_rn(s, -a);
+    return {s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -t)), __fadd_rn(b, -t))};
+}
+__device__ __forceinline__ Two quick_two_sum(float a, float b) {  // exact for |a| >= |b|
+    const float s = __fadd_rn(a, b);
+    return {s, __fadd_rn(b, -__fadd_rn(s, -a))};
+}
+__device__ __forceinline__ Two operator+(const Two& a, const Two& b) {
+    const Two s = two_sum(a.hi, b.hi), t = two_sum(a.lo, b.lo);
+    const Two u = quick_two_sum(s.hi, __fadd_rn(s.lo, t.hi));
+    return quick_two_sum(u.hi, __fadd_rn(u.lo, t.lo));
+}
+__device__ __forceinline__ Two operator*(const Two& a, const Two& b) {
+    const float p = __fmul_rn(a.hi, b.hi);
+    const float e = __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -p)));
+    return quick_two_sum(p, e);
+}
+__device__ __forceinline__ Two inverse(const Two& d) {
+    const float q = __fdiv_rn(1.0f, d.hi);
+    const float r = __fmaf_rn(-d.lo, q, __fmaf_rn(-d.hi, q, 1.0f));
+    return quick_two_sum(q, __fmul_rn(r, q));
+}
+// e^x for x = hi + lo <= 0, to some 2^-44 of it; 0 below -87. x = n ln 2 + r, e^r = (e^(r/4))^4, the series up to
+// r^8 / 8! with its first terms in pairs. n ln 2 is taken off in parts of ln 2, the first two of 12 and
+// 17 bits, so that their products with n are exact.
+__device__ __forceinline__ Two exp_two(float x, float x_lo) {
+    if (!(x > -87.0f)) return {x != x ? x : 0.0f, 0.0f};
+    const float n = rintf(x * LOG2E);
+    constexpr float L1 = 2839 * 0x1p-12f, L2 = 68603 * 0x1p-31f;
+    constexpr float L3 = (float)(0.69314718055994530942 - (double)L1 - (double)L2);
+    const float a = __fmaf_rn(-n, L1, x);  // exact
+    const Two b = two_sum(a, __fmul_rn(-n, L2));
+    const Two r0 = two_sum(b.hi, __fmaf_rn(-n, L3, __fadd_rn(b.lo, x_lo)));
+    const Two r = {0.25f * r0.hi, 0.25f * r0.lo};
+    auto coef = [](double c) { return Two{(float)c, (float)(c - (double)(float)c)}; };
+    const float top = fmaf(r.hi, fmaf(r.hi, fmaf(r.hi, 1.0f / 40320, 1.0f / 5040), 1.0f / 720), 1.0f / 120);
+    Two q = coef(1.0 / 24) + r * Two{top, 0.0f};
+    q = coef(1.0 / 6) + r * q;
+    q = Two{0.5f, 0.0f} + r * q;
+    q = Two{1.0f, 0.0f} + r * q;
+    q = Two{1.0f, 0.0f} + r * q;
+    q = q * q;
+    q = q * q;
+    const float f = __int_as_float(((int)n + 127) << 23);  // n >= -126
+    return {q.hi * f, q.lo * f};
+}
+__device__ __forceinline__ Two sigmoid_two(float l) {
+    const Two e = exp_two(-fabsf(l), 0.0f), y = inverse(Two{1.0f, 0.0f} + e);
+    return l >= 0.0f ? y : e * y;  // NaN: e is one
+}
+// Keys in the order of the pairs, a NaN above all numbers. Two numbers that differ by less than their last
+// bits may have the same key.
+__device__ __forceinline__ uint64_t order_key(const Two& v) {
+    const float inf = __int_as_float(0x7F800000);
+    return (uint64_t)order_key(v.hi) << 32 | order_key(fabsf(v.hi) < inf ? v.lo : 0.0f);
+}
+__device__ __forceinline__ Two key_value(uint64_t k) { return {key_value((uint32_t)(k >> 32)), key_value((uint32_t)k)}; }
+__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t min_u64(uint64_t a, uint64_t b) { return a < b ? a : b; }
+
+// What lane j gets: the j-th expert (-1: none) and its logit.
+struct Pick {
+    int id;
+    float l;
+};
+
+// The row's experts, decided by such scores. Loops stay rolled: rows come here one in thousands, and a
+// long way through instructions that no cache holds takes longer than what they do.
+template <bool BF16>
+__device__ __noinline__ Pick select_exact_scores(const ScoreArgs& a, int64_t row, bool by_logit, float b0) {
+    const int lane = threadIdx.x % 32;
+    const LaneExperts x(a, lane);
+    const float inf = __int_as_float(0x7F800000);
+    float top = 0.0f;
+    Two inv = {1.0f, 0.0f};
+    if (!a.sigmoid) {
+        float m = -inf;
+        for (int i = 0; i < x.count; ++i) m = max_nan(m, logit_at<BF16>(a.logits, row + x.first + i));
+        top = key_value(__reduce_max_sync(0xffffffffu, order_key(m)));
+        Two sum = {0.0f, 0.0f};
+#pragma unroll 1
+        for (int i = 0; i < x.count; ++i) {
+            const Two d = two_sum(logit_at<BF16>(a.logits, row + x.first + i), -top);
+            sum = sum + exp_two(d.hi, d.hi > -inf ? d.lo : 0.0f);
+        }
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1)
+            sum = sum + Two{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)};
+        inv = inverse(sum);
+    }
+    uint64_t key[32];            // what the order goes by, 0: not to be taken
+    uint64_t g1 = 0, g2 = 0;     // the two largest scores with bias
+    const bool logits_alone = by_logit && !(a.top2 && a.top_groups < a.groups);
+#pragma unroll 2
+    for (int i = 0; i < x.count; ++i) {
+        const float v = logit_at<BF16>(a.logits, row + x.first + i), b = by_logit ? b0 : a.bias[x.first + i];
+        key[i] = 0;
+        if (v == -inf || b == -inf) continue;
+        if (logits_alone) {
+            key[i] = order_key(Two{v, 0.0f});
+            g1 = max_u64(g1, key[i]);
+            continue;
+        }
+        Two s;
+        if (a.sigmoid) {
+            s = sigmoid_two(v);
+        } else {
+            const Two d = two_sum(v, -top);
+            s = exp_two(d.hi, d.lo) * inv;
+        }
+        const uint64_t c = order_key(fabsf(b) < inf ? s + Two{b, 0.0f} : Two{s.hi + b, 0.0f});
+        key[i] = by_logit ? order_key(Two{v, 0.0f}) : c;
+        g2 = max_u64(g2, min_u64(g1, c));
+        g1 = max_u64(g1, c);
+    }
+    int count = x.count;
+    if (a.top_groups < a.groups) {
+#pragma unroll 1
+        for (int o = 1; o < 1 << a.lane_bits; o <<= 1) {
+            const uint64_t u1 = __shfl_xor_sync(0xffffffffu, g1, o), u2 = __shfl_xor_sync(0xffffffffu, g2, o);
+            g2 = max_u64(min_u64(g1, u1), max_u64(g2, u2));
+            g1 = max_u64(g1, u1);
+        }
+        if (a.top2 && g2 != 0) {
+            const Two p = key_value(g1), q = key_value(g2);
+            g1 = order_key(fabsf(p.hi) < inf && fabsf(q.hi) < inf ? p + q : Two{p.hi + q.hi, 0.0f});
+        }
+        int rank = 0;
+#pragma unroll 1
+        for (int g = 0; g < a.groups; ++g) {
+            const uint64_t u = __shfl_sync(0xffffffffu, g1, g << a.lane_bits);
+            rank += u > g1 || (g < x.group && u == g1);
+        }
+        if (rank >= a.top_groups) count = 0;
+    }
+    Pick mine = {-1, 0.0f};
+#pragma unroll 1
+    for (int j = 0; j < a.k; ++j) {
+        uint64_t m = 0;
+        int place = 0;
+#pragma unroll 1
+        for (int i = 0; i < count; ++i)
+            if (key[i] > m) m = key[i], place = i;
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(m >> 32));
+        if (hi == 0) break;  // warp-uniform
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(m >> 32) == hi ? (uint32_t)m : 0u);
+        const int holder = __ffs(__ballot_sync(0xffffffffu, m == ((uint64_t)hi << 32 | lo))) - 1;
+        if (lane == holder) key[place] = 0;
+        place = __shfl_sync(0xffffffffu, x.first + place, holder);
+        if (lane == j) mine.id = place;
+    }
+    if (mine.id >= 0) mine.l = logit_at<BF16>(a.logits, row + mine.id);
+    return mine;
+}
+
+// Puts the candidates of the lanes below n (the k best among them) in order by their scores to 2^-44,
+// ties to the lowest id. Not for softmax with a bias, whose sum is not known so well.
+__device__ __noinline__ Pick settle(const ScoreArgs& a, Pick p, int n, bool by_logit) {
+    const int lane = threadIdx.x % 32;
+    const float b = by_logit || p.id < 0 ? 0.0f : a.bias[p.id];
+    const uint64_t key = p.id < 0 ? 0 : order_key(by_logit ? Two{p.l, 0.0f} : sigmoid_two(p.l) + Two{b, 0.0f});
+    int rank = 0;  // candidates that come before mine; those without an expert stay behind in their order
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+        const uint64_t u = __shfl_sync(0xffffffffu, key, j);
+        const int id = __shfl_sync(0xffffffffu, p.id, j);
+        rank += u > key || (u == key && (id < p.id || (id == p.id && j < lane)));
+    }
+    int from = lane;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j)
+        if (__shfl_sync(0xffffffffu, rank, j) == lane) from = j;
+    const Pick q = {__shfl_sync(0xffffffffu, p.id, from), __shfl_sync(0xffffffffu, p.l, from)};
+    return lane < a.k ? q : Pick{-1, 0.0f};
+}
+
+// Whether this lane's group is taken, by sums of such scores. t1, t2: keys with the ids of the group's two
+// largest. Sigmoid scores, or largest logits.
+template <bool BF16>
+__device__ __noinline__ bool settle_groups(const ScoreArgs& a, int64_t row, bool by_logit, float b0, uint32_t t1,
+                                           uint32_t t2) {
+    const int group = (int)(threadIdx.x % 32) >> a.lane_bits;
+    const float inf = __int_as_float(0x7F800000);
+    Two c[2] = {{-inf, 0.0f}, {0.0f, 0.0f}};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t t = i ? t2 : t1;
+        if (t <= 511u || (i && !a.top2)) continue;  // none
+        const int id = (int)(511u - (t & 511u));
+        const float l = logit_at<BF16>(a.logits, row + id);
+        if (by_logit && !a.top2)
+            c[i] = {l, 0.0f};
+        else
+            c[i] = sigmoid_two(l) + Two{by_logit ? b0 : a.bias[id], 0.0f};
+    }
+    const uint64_t value = order_key(c[0].hi > -inf ? c[0] + c[1] : c[0]);
+    int rank = 0;
+#pragma unroll 1
+    for (int g = 0; g < a.groups; ++g) {
+        const uint64_t u = __shfl_sync(0xffffffffu, value, g << a.lane_bits);
+        rank += u > value || (g < group && u == value);
+    }
+    return rank < a.top_groups && group < a.groups;
+}
+
+// Keys: 23 bits of a value above 9 of 511 - id, so that all are different, the larger key is the larger
+// value, then the lower id, and a pick is one warp maximum. 0 .. 511: no expert that may be taken.
+// With a bias the value is the mantissa of 1 <= 1 + unit (c - lowest bias) < 2: steps of 2^-23 of the range
+// that c can have. Where the order is that of the logits, it is their ordered bits.
+constexpr uint32_t TAG = 511u;  // E <= 512
+constexpr uint32_t NO_EXPERT = TAG + 1;
+constexpr uint32_t LOGIT_KEY = KEY_FINITE - NO_EXPERT;  // taken off ordered logits: the lowest number is above NO_EXPERT
+
+// What a warp's rows share of the biases.
+template <int C>
+struct Biases {
+    float b[C];      // sigmoid: 1 + unit (b - lowest), and a little; softmax: b - lowest
+    float unit;      // sigmoid: 1 / range
+    float spread, lowest;
+    float b0;        // the bias, where all are equal
+    bool by_logit;   // all equal, or none
+    bool closed;     // this lane has an expert of bias -inf
+    bool odd;        // a bias is NaN or +inf
+    __device__ __forceinline__ Biases(const ScoreArgs& a, const LaneExperts& x) {
+        const float inf = __int_as_float(0x7F800000);
+        unit = 1.0f;
+        spread = lowest = b0 = 0.0f;
+        by_logit = true;
+        closed = odd = false;
+#pragma unroll
+        for (int i = 0; i < C; ++i) b[i] = 0.0f;
+        if (!a.bias) return;
+        uint32_t lo = KEY_NAN, hi = 0, least = KEY_NAN;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (i < x.count) {
+                b[i] = a.bias[x.first + i];
+                const uint32_t key = order_key(b[i]);
+                lo = min(lo, key);
+                hi = max(hi, key);
+                if (b[i] > -inf) least = min(least, key);
+                closed = closed || b[i] == -inf;
+            }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        least = __reduce_min_sync(0xffffffffu, least);
+        b0 = key_value(lo);
+        by_logit = lo == hi && fabsf(b0) < inf;
+        if (by_logit) return;
+        odd = !(key_value(hi) < inf);
+        if (odd || key_value(hi) == -inf) return;
+        lowest = key_value(least);
+        spread = key_value(hi) - lowest;
+        odd = !(spread < 0x1p100f);
+        unit = 0x1.ffffp-1f / (1.0f + spread);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            b[i] = b[i] - lowest;
+            if (a.sigmoid) b[i] = fmaf(b[i], unit, 1.0f + 0x1p-20f);
+        }
+    }
+};
+
+// The row's experts. sum: of the exponentials past the largest logit, top (softmax, where it is needed).
+template <bool BF16, int C, bool VEC>
+__device__ __forceinline__ Pick pick_row(const ScoreArgs& a, int64_t row, const LaneExperts& x, float (&v)[C],
+                                         const Biases<C>& B, int lane, float& top, float& sum) {
+    const float inf = __int_as_float(0x7F800000);
+    const bool limited = a.top_groups < a.groups, by_logit = B.by_logit;
+    top = 0.0f;
+    sum = 1.0f;
+    float inv = 1.0f;
+    uint32_t key[C];
+    const uint32_t tag = TAG - (uint32_t)x.first;
+    if (!a.sigmoid && (!by_logit || !a.renorm || (limited && a.top2))) {
+        float m = v[0];
+#pragma unroll
+        for (int i = 1; i < C; ++i) m = max_nan(m, v[i]);
+        top = key_value(__reduce_max_sync(0xffffffffu, order_key(m)));
+        sum = 0.0f;
+        float e[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            e[i] = fast_exp(v[i] - top);  // NaN only where the row holds a NaN or +inf, or nothing but -inf
+            if (!VEC && i >= x.count) e[i] = 0.0f;
+            sum += e[i];
+        }
+        sum = warp_sum(sum);
+        inv = fast_rcp(sum);  // also the largest score
+        if (!by_logit) {
+            const float unit = fast_div(0x1.fffp-1f, inv + B.spread), times = inv * unit;
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                key[i] = (__float_as_uint(fmaf(e[i], times, fmaf(B.b[i], unit, 1.0f + 0x1p-20f))) << 9) + (tag - i);
+        }
+    } else if (!by_logit) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            key[i] = (__float_as_uint(fmaf(fast_sigmoid(v[i]), B.unit, B.b[i])) << 9) + (tag - i);
+    }
+    if (by_logit) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) key[i] = ((order_key(v[i]) - LOGIT_KEY) & ~TAG) | (tag - i);
+    }
+    bool out = !VEC || B.closed;
+#pragma unroll
+    for (int i = 0; i < C; ++i) out = out || v[i] == -inf;
+    if (out) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (v[i] == -inf || B.b[i] == -inf || (!VEC && i >= x.count)) key[i] = 0;
+    }
+    // the lane's two largest
+    uint32_t h1 = max(key[0], key[1]), h2 = min(key[0], key[1]);
+#pragma unroll
+    for (int i = 2; i < C; i += 2) {
+        const uint32_t hi = max(key[i], key[i + 1]), lo = min(key[i], key[i + 1]);
+        h2 = __vimax3_u32(min(h1, hi), h2, lo);
+        h1 = max(h1, hi);
+    }
+    // How far two values may be apart and still be out of order. Sigmoid: twice 2^-21.8 of unit, and the
+    // roundings of unit, bias and sum, half a step each; softmax: twice 2^-18 of the largest. fp32 logits
+    // lose 9 bits, bf16 ones none.
+    const int near = by_logit ? (BF16 ? -1 : 0) : a.sigmoid ? 9 : 68;
+    bool exact = B.odd;  // the row is to be decided by select_exact_scores (warp-uniform)
+    if (limited) {
+        uint32_t t1 = h1, t2 = h2;
+        for (int o = 1; o < 1 << a.lane_bits; o <<= 1) {
+            const uint32_t u1 = __shfl_xor_sync(0xffffffffu, t1, o), u2 = __shfl_xor_sync(0xffffffffu, t2, o);
+            t2 = __vimax3_u32(min(t1, u1), t2, u2);
+            t1 = max(t1, u1);
+        }
+        // the groups' keys: a value above 5 bits of 31 - group
+        int value = (int)(t1 >> 9), slack = near;
+        if (a.top2) {
+            if (!by_logit) {
+                // a missing second counts as c = 0, up to where no sum of two reaches
+                const float unit = a.sigmoid ? B.unit : fast_div(0x1.fffp-1f, inv + B.spread);
+                const float zero = fminf(fmaxf(-B.lowest * unit, -2.0f), 2.0f);
+                value += (1 << 24) + (t2 >= NO_EXPERT ? (int)(t2 >> 9) : (int)(zero * 0x1p23f) + 8);
+                slack = 2 * near + 2;
+            } else {
+                // steps of 2^-20; logits that lost their lowest bits are off by 2^-14 of them
+                const float v1 = key_value((t1 & ~TAG) + LOGIT_KEY), cut = BF16 ? 0.0f : 0x1p6f;
+                const float s1 = a.sigmoid ? fast_sigmoid(v1) : fast_exp(v1 - top) * inv;
+                float s = s1 - B.b0, off = (a.sigmoid ? s1 * (1.0f - s1) : s1) * fabsf(v1) * cut;
+                if (t2 >= NO_EXPERT) {
+                    const float v2 = key_value((t2 & ~TAG) + LOGIT_KEY);
+                    const float s2 = a.sigmoid ? fast_sigmoid(v2) : fast_exp(v2 - top) * inv;
+                    s = s1 + s2;
+                    off = fmaf((a.sigmoid ? s2 * (1.0f - s2) : s2) * fabsf(v2), cut, off);
+                }
+                s = fminf(fmaxf(s, -4.0f), 4.0f) + 4.0f;  // NaN: a key of its own, decided below
+                value = t1 >= NO_EXPERT ? __float2int_rn(s * 0x1p20f) : 0;
+                slack = (int)fminf(off, 0x1p28f) + (a.sigmoid ? 8 : 24);
+                slack = (int)__reduce_max_sync(0xffffffffu, t1 >= NO_EXPERT ? (uint32_t)(2 * slack) : 0u);
+            }
+        }
+        const bool there = t1 >= NO_EXPERT;
+        const uint32_t gk = x.group < a.groups ? (there ? (uint32_t)value << 5 : 0u) + (31u - x.group) : 0u;
+        bool kept = false;
+        uint32_t rest = gk, last, next;
+        if (2 * a.top_groups <= a.groups) {
+            last = 0;
+            for (int g = 0; g < a.top_groups; ++g) {
+                last = __reduce_max_sync(0xffffffffu, rest);
+                if (rest == last) kept = true, rest = 0;
+            }
+            next = __reduce_max_sync(0xffffffffu, rest);
+        } else {
+            kept = true;
+            next = 0;
+            if (x.group >= a.groups) rest = ~0u;
+            for (int g = a.top_groups; g < a.groups; ++g) {
+                next = __reduce_min_sync(0xffffffffu, rest);
+                if (rest == next) kept = false, rest = ~0u;
+            }
+            last = __reduce_min_sync(0xffffffffu, rest);
+        }
+        // Groups too close are looked at again, unless more experts than the largest may be among those that
+        // count (or the two largest: the third may be larger than the second).
+        if (next >= 32u && (int)(last >> 5) - (int)(next >> 5) <= slack) {
+            const uint32_t t = a.top2 ? t2 : t1, least = t - min(t, (uint32_t)(near + 1) << 9);
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < C; ++i) n += t >= NO_EXPERT && key[i] >= NO_EXPERT && key[i] >= least;
+            for (int o = 1; o < 1 << a.lane_bits; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            exact = exact || (!a.sigmoid && (!by_logit || a.top2)) || __any_sync(0xffffffffu, n > (a.top2 ? 2 : 1));
+            if (!exact) kept = settle_groups<BF16>(a, row, by_logit, B.b0, t1, t2);
+        }
+        if (!kept) h1 = h2 = 0;
+    }
+    uint32_t m = __reduce_max_sync(0xffffffffu, h1);
+    // keys from here on: a NaN, or a logit of +inf
+    if (m >= (by_logit ? 0xFF800000u - LOGIT_KEY - TAG : 0xFFFFFE00u)) exact = true;
+    if (exact) return select_exact_scores<BF16>(a, row, by_logit, B.b0);
+    auto after = [&]() {  // the largest key below m
+        const bool held = h1 == m;
+        h1 = held ? h2 : h1;
+        h2 = held ? 0 : h2;
+        if constexpr (C > 2) {
+            if (__any_sync(0xffffffffu, held && h1 == 0)) {  // its second, or it has no more
+                uint32_t d = 0;
+#pragma unroll
+                for (int i = 0; i < C; ++i) d = __viaddmax_u32(key[i], 0u - m, d);
+                d = m + d < m ? m + d : 0;  // keys below m have wrapped, those above have not
+                h1 = held ? d : h1;
+            }
+        }
+        return __reduce_max_sync(0xffffffffu, h1);
+    };
+    // the picks; m ends as the one behind them
+    uint32_t mine = 0;
+    const bool short_keys = BF16 && by_logit;  // 16 bits and the id: nothing is lost
+    const int last = short_keys ? a.k - 1 : a.k;
+#pragma unroll 4
+    for (int j = 0;; ++j) {
+        mine = lane == j ? m : mine;
+        if (j == last) break;
+        m = after();
+    }
+    Pick p = {-1, 0.0f};
+    auto take = [&]() {
+        if (mine >= NO_EXPERT) p.id = (int)(TAG - (mine & TAG)), p.l = logit_at<BF16>(a.logits, row + p.id);
+    };
+    uint32_t behind = __shfl_down_sync(0xffffffffu, mine, 1);
+    if (lane >= a.k - 1) behind = lane == a.k - 1 ? m : 0;
+    if (lane >= a.k) mine = 0;
+    take();
+    if (short_keys) return p;
+    bool open = behind >= NO_EXPERT && (int)(mine >> 9) - (int)(behind >> 9) <= near;
+    if (__any_sync(0xffffffffu, open)) {
+        // equal logits with equal biases are equal, and in order, but for those behind the last pick
+        const float bias = by_logit || p.id < 0 ? 0.0f : a.bias[p.id];
+        const float ln = __shfl_down_sync(0xffffffffu, p.l, 1), bn = __shfl_down_sync(0xffffffffu, bias, 1);
+        if (lane < a.k - 1 && p.l == ln && bias == bn) open = false;
+        if (!__any_sync(0xffffffffu, open)) return p;
+        if (!a.sigmoid && !by_logit) return select_exact_scores<BF16>(a, row, by_logit, B.b0);
+        // every expert that may belong to the k best, a lane for each
+        const uint32_t kth = __shfl_sync(0xffffffffu, mine, a.k - 1) >> 9;
+        const uint32_t least = max(NO_EXPERT, (kth - min(kth, (uint32_t)near)) << 9);
+        int n = a.k;
+#pragma unroll 1
+        for (; n < 32 && m >= least; ++n) {
+            mine = lane == n ? m : mine;
+            m = after();
+        }
+        if (m >= least) return select_exact_scores<BF16>(a, row, by_logit, B.b0);
+        if (lane >= a.k) take();
+        p = settle(a, p, n, by_logit);
+    }
+    return p;
+}
+
+// Lane j's share of the row from its logit, before the scale: s_j, or s_j / sum of the picked ones. Where
+// all of these are far below 0 a sigmoid is e^l, and shares are a softmax's; so they are for softmax
+// scores. (Scores of their own would be lost below 2^-126.)
+__device__ __forceinline__ float share(const ScoreArgs& a, const Pick& p, float top, float sum) {
+    const bool got = p.id >= 0;
+    if (!a.renorm) return a.sigmoid ? fast_sigmoid(p.l) : fast_div(fast_exp(p.l - top), sum);
+    float s;
+    if (a.sigmoid && __any_sync(0xffffffffu, got && !(p.l < -20.0f)))
+        s = fast_sigmoid(p.l);
+    else
+        s = fast_exp(p.l - key_value(__reduce_max_sync(0xffffffffu, got ? order_key(p.l) : 0u)));
+    if (!got) s = 0.0f;
+    if (sum != sum) s = sum;  // a row of NaN scores, though its picked logits may be numbers
+    float total = s;
+    if (a.k <= 8) {
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    } else {
+        total = warp_sum(s);
+    }
+    return fast_div(s, total);
+}
+
+// This CTA's rows: ids and weights to memory, counts to s_counts, the number of valid rows of each warp.
+template <bool BF16, int C, bool VEC, int WARPS>
+__device__ __forceinline__ void score_rows(const ScoreArgs& a, int* s_counts, int* s_valid) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const LaneExperts x(a, lane);
+    const Biases<C> B(a, x);
+    int valid_rows = 0;
+    for (int64_t t = (int64_t)blockIdx.x * WARPS + warp; t < a.T; t += (int64_t)gridDim.x * WARPS) {
+        float v[C];
+        load_row<BF16, C, VEC>(a, t * a.ld, x, v);
+        const bool masked = a.mask && a.mask[t] == 0;
+        Pick p = {-1, 0.0f};
+        float w = 0.0f;
+        if (!masked) {  // warp-uniform
+            float top, sum;
+            p = pick_row<BF16, C, VEC>(a, t * a.ld, x, v, B, lane, top, sum);
+            w = share(a, p, top, sum) * a.scale;
+            if (__any_sync(0xffffffffu, p.id >= 0)) ++valid_rows;
+            if (p.id >= 0)
+                atomicAdd(&s_counts[p.id], 1);
+            else
+                w = 0.0f;
+        }
+        if (lane < a.k) {
+            a.ids[t * a.k + lane] = p.id;
+            a.w[t * a.k + lane] = w;
+        }
+    }
+    if (lane == 0) s_valid[warp] = valid_rows;
+}
+
+// More tokens: each CTA's counts to memory, joined by score_join_kernel.
+template <bool BF16, int C, bool VEC>
+__global__ void __launch_bounds__(SCORE_THREADS, score_ctas(C)) score_kernel(const __grid_constant__ ScoreArgs a) {
+    __shared__ int s_counts[SCORE_MAX_EXPERTS], s_valid[SCORE_WARPS];
+    for (int e = threadIdx.x; e < a.E; e += SCORE_THREADS) s_counts[e] = 0;
+    grid_dep_wait();
+    grid_dep_launch();
+    __syncthreads();
+    score_rows<BF16, C, VEC, SCORE_WARPS>(a, s_counts, s_valid);
+    if (!a.part_counts) return;
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += SCORE_THREADS)
+        a.part_counts[(int64_t)blockIdx.x * a.E + e] = s_counts[e];
+    if (threadIdx.x == 0) {
+        int n = 0;
+        for (int w = 0; w < SCORE_WARPS; ++w) n += s_valid[w];
+        a.part_valid[blockIdx.x] = n;
+    }
+}
+
+constexpr int SCORE_JOIN_THREADS = 1024;
+// CTA c: the experts 32 c .. 32 c + 31, one in each lane; warp w adds the parts w, w + 32, ...
+__global__ void __launch_bounds__(SCORE_JOIN_THREADS) score_join_kernel(const ScoreArgs a, int parts) {
+    constexpr int WARPS = SCORE_JOIN_THREADS / 32;
+    __shared__ int s_c[WARPS][32], s_n[WARPS];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, e = 32 * (int)blockIdx.x + lane;
+    grid_dep_wait();
+    grid_dep_launch();
+    int c = 0, n = 0;
+    if (e < a.E) {
+#pragma unroll 8
+        for (int i = warp; i < parts; i += WARPS) c += __ldcg(a.part_counts + (int64_t)i * a.E + e);
+    }
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < parts; i += SCORE_JOIN_THREADS) n += __ldcg(a.part_valid + i);
+    n = __reduce_add_sync(0xffffffffu, n);
+    s_c[warp][lane] = c;
+    if (lane == 0) s_n[warp] = n;
+    __syncthreads();
+    if (warp != 0) return;
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) c += s_c[w][lane];
+    if (a.counts && e < a.E) a.counts[e] = c;
+    n = __reduce_add_sync(0xffffffffu, s_n[lane]);
+    if (a.num_valid && blockIdx.x == 0 && lane == 0) *a.num_valid = n;
+}
+
+__device__ __forceinline__ int peer_int(const int* p, uint32_t rank) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+    return v;
+}
+
+// Few tokens: one cluster; CTA c joins the experts c, c + ctas, ...
+template <bool BF16, int C, bool VEC>
+__global__ void __launch_bounds__(SCORE_THREADS) score_cluster_kernel(const __grid_constant__ ScoreArgs a) {
+    __shared__ int s_counts[SCORE_MAX_EXPERTS], s_valid[SCORE_WARPS], s_n;
+    const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;
+    for (int e = threadIdx.x; e < a.E; e += SCORE_THREADS) s_counts[e] = 0;
+    grid_dep_wait();
+    grid_dep_launch();
+    __syncthreads();
+    score_rows<BF16, C, VEC, SCORE_WARPS>(a, s_counts, s_valid);
+    if (!a.counts && !a.num_valid) return;  // the same for every CTA
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int n = 0;
+        for (int w = 0; w < SCORE_WARPS; ++w) n += s_valid[w];
+        s_n = n;
+    }
+    if (ctas > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    const int e = (int)(threadIdx.x * ctas + rank);  // E <= 512 = the CTA's threads
+    if (a.counts && e < a.E) {
+        int c = 0;
+        for (uint32_t r = 0; r < ctas; ++r) c += ctas > 1 ? peer_int(s_counts + e, r) : s_counts[e];
+        a.counts[e] = c;
+    }
+    if (a.num_valid && rank == 0 && threadIdx.x == 0) {
+        int n = 0;
+        for (uint32_t r = 0; r < ctas; ++r) n += ctas > 1 ? peer_int(&s_n, r) : s_n;
+        *a.num_valid = n;
+    }
+    if (ctas > 1) cluster_sync();  // no CTA leaves while its shared memory is read
+}
+
+// ------------------------------------------------------------------ gradient
+constexpr int SCORE_GRAD_WARPS = 8;
+constexpr int SCORE_GRAD_THREADS = 32 * SCORE_GRAD_WARPS;
+
+// Only picked experts have a gradient: a warp takes 32 / KP rows at a time, KP (>= k, a power of two)
+// lanes for the slots of each, stores the rows' zeros while the picked logits are on their way, and then
+// their gradients over them. zero_vec: rows may be zeroed in pieces of 16 bytes.
+template <bool BF16>
+__global__ void __launch_bounds__(SCORE_GRAD_THREADS)
+    score_grad_kernel(const ScoreGradArgs a, int kp_bits, bool zero_vec) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int slot = lane & ((1 << kp_bits) - 1), sub = lane >> kp_bits, rows = 32 >> kp_bits;
+    using E = typename std::conditional<BF16, __nv_bfloat16, float>::type;
+    E* out = reinterpret_cast<E*>(a.dlogits);
+    grid_dep_wait();
+    grid_dep_launch();
+    auto total = [&](float v) {  // over a row's lanes
+        for (int o = 1; o < 1 << kp_bits; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    };
+    for (int64_t t0 = ((int64_t)blockIdx.x * SCORE_GRAD_WARPS + warp) * rows; t0 < a.T;
+         t0 += (int64_t)gridDim.x * SCORE_GRAD_WARPS * rows) {
+        const int64_t t = t0 + sub;
+        int id = -1;
+        float dw = 0.0f, l = -__int_as_float(0x7F800000);
+        if (t < a.T && slot < a.k) {
+            id = a.ids[t * a.k + slot];
+            dw = a.dw[t * a.k + slot];
+            if ((unsigned)id >= (unsigned)a.E) id = -1;
+            if (id >= 0) l = logit_at<BF16>(a.logits, t * a.ld + id);
+        }
+        const int live = (int)min((int64_t)rows, a.T - t0);
+        for (int r = 0; r < live; ++r) {
+            E* row = out + (t0 + r) * a.ldd;
+            if (zero_vec) {
+                for (int i = lane; i < a.E * (int)sizeof(E) / 16; i += 32)
+                    reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int i = lane; i < a.E; i += 32) row[i] = E(0.0f);
+            }
+        }
+        const bool got = id >= 0;
+        float d;
+        if (a.renorm) {
+            uint32_t most = got ? order_key(l) : 0u;
+            for (int o = 1; o < 1 << kp_bits; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+            const float top = key_value(most);
+            float s = 0.0f;
+            if (got) s = a.sigmoid && !(top < -20.0f) ? fast_sigmoid(l) : fast_exp(l - top);
+            const float w = fast_div(s, total(s));
+            d = w * (dw - total(got ? w * dw : 0.0f));
+            if (a.sigmoid) d *= fast_sigmoid(-l);  // 1 - s
+        } else {
+            d = fast_sigmoid(l) * fast_sigmoid(-l) * dw;
+        }
+        __syncwarp();  // the zeros come first
+        if (got) out[t * a.ldd + id] = E(a.scale * d);
+    }
+}
+
+// b_e += rate sign(mean of the counts - counts_e), decided in whole numbers
+__global__ void __launch_bounds__(SCORE_THREADS) score_bias_kernel(const int32_t* counts, float* bias, int E, float rate) {
+    __shared__ long long s_part[SCORE_THREADS / 32];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int e = threadIdx.x;  // E <= 512
+    const long long c = e < E ? counts[e] : 0;
+    long long sum = c;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (e % 32 == 0) s_part[e / 32] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int w = 0; w < SCORE_THREADS / 32; ++w) sum += s_part[w];
+    if (e < E && sum != c * E) bias[e] += sum > c * E ? rate : -rate;
+}
+
+// ------------------------------------------------------------------ host side
+int score_grid(int T, int E) {
+    if (T <= SCORE_CLUSTER_TOKENS) return 0;
+    const int64_t g = ceil_div(T, SCORE_WARPS), most = SMS * score_ctas(E > 256 ? 16 : 8);
+    return (int)(g < most ? g : most);
+}
+
+template <bool BF16, int C, bool VEC>
+static cudaError_t score_t(const ScoreArgs& a, cudaStream_t st) {
+    const int grid = score_grid(a.T, a.E);
+    if (grid == 0) {
+        const int64_t want = ceil_div(a.T, SCORE_WARPS);
+        const int ctas = want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
+        LaunchAttrs at(true, ctas);
+        cudaLaunchConfig_t cfg = at.config(dim3(ctas), dim3(SCORE_THREADS), 0, st);
+        return cudaLaunchKernelEx(&cfg, score_cluster_kernel<BF16, C, VEC>, a);
+    }
+    {
+        LaunchAttrs at(true);
+        cudaLaunchConfig_t cfg = at.config(dim3(grid), dim3(SCORE_THREADS), 0, st);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, score_kernel<BF16, C, VEC>, a);
+        if (e != cudaSuccess || (!a.counts && !a.num_valid)) return e;
+    }
+    LaunchAttrs at(true);
+    cudaLaunchConfig_t cfg = at.config(dim3((unsigned)ceil_div(a.E, 32)), dim3(SCORE_JOIN_THREADS), 0, st);
+    return cudaLaunchKernelEx(&cfg, score_join_kernel, a, grid);
+}
+
+template <int C>
+static cudaError_t score_c(const ScoreArgs& a, cudaStream_t st) {
+    // whole vectors of C experts in every lane
+    const int el = a.bf16 ? 2 : 4, vec = C * el < 16 ? C * el : 16;
+    const bool v = a.E == 32 * C && a.per == C && (uintptr_t)a.logits % vec == 0 && (a.ld * el) % vec == 0;
+    if (v) return a.bf16 ? score_t<true, C, true>(a, st) : score_t<false, C, true>(a, st);
+    return a.bf16 ? score_t<true, C, false>(a, st) : score_t<false, C, false>(a, st);
+}
+
+cudaError_t launch_score_router(const ScoreArgs& args, cudaStream_t st) {
+    ScoreArgs a = args;
+    int lanes = 32;
+    for (a.lane_bits = 5; 32 / lanes < a.groups; lanes /= 2) --a.lane_bits;
+    a.group_size = a.E / a.groups;
+    a.per = (int)ceil_div(a.group_size, lanes);
+    if (a.per <= 2) return score_c<2>(a, st);
+    if (a.per <= 4) return score_c<4>(a, st);
+    if (a.per <= 8) return score_c<8>(a, st);
+    if (a.per <= 16) return score_c<16>(a, st);
+    return score_c<32>(a, st);  // 17 groups of 30, say
+}
+
+cudaError_t launch_score_grad(const ScoreGradArgs& a, cudaStream_t st) {
+    int bits = 0;
+    while (1 << bits < a.k) ++bits;
+    const int el = a.bf16 ? 2 : 4;
+    const bool vec = (uintptr_t)a.dlogits % 16 == 0 && a.ldd * el % 16 == 0 && a.E * el % 16 == 0;
+    const int64_t per_cta = SCORE_GRAD_WARPS * (32 >> bits), g = ceil_div(a.T, per_cta), most = SMS * 8;
+    LaunchAttrs at(true);
+    cudaLaunchConfig_t cfg = at.config(dim3((unsigned)(g < most ? g : most)), dim3(SCORE_GRAD_THREADS), 0, st);
+    return a.bf16 ? cudaLaunchKernelEx(&cfg, score_grad_kernel<true>, a, bits, vec)
+                  : cudaLaunchKernelEx(&cfg, score_grad_kernel<false>, a, bits, vec);
+}
+
+cudaError_t launch_score_bias(const int32_t* counts, float* bias, int E, float rate, cudaStream_t st) {
+    LaunchAttrs at(true);
+    cudaLaunchConfig_t cfg = at.config(dim3(1), dim3(SCORE_THREADS), 0, st);
+    return cudaLaunchKernelEx(&cfg, score_bias_kernel, counts, bias, E, rate);
+}
+
+}  // namespace moe

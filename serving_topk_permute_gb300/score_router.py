@@ -1,0 +1,160 @@
+"""Binding of the score router (include/moe.h): sigmoid or softmax scores with a selection bias and
+expert groups, the gradient of its weights, and the step of the bias. Argument checks and marshalling
+only, as in block.py.
+"""
+from __future__ import annotations
+
+import ctypes
+from ctypes import byref
+from dataclasses import dataclass
+
+import torch
+
+from . import block
+from .block import (F32, I32, I64, LOGITS, P, SZ, RouterOutput, _at_device, _current_device, _device_of, _fail, _flat,
+                    _matrix, _on, _row_stride, _stream)
+from .moe import MOE_OK
+
+SCORES = {"sigmoid": 0, "softmax": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
+
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+
+
+class ScoreRouterConfigC(ctypes.Structure):
+    _fields_ = [("num_experts", I32), ("top_k", I32), ("score", I32), ("num_groups", I32), ("top_groups", I32),
+                ("group_score", I32), ("renormalize", I32), ("logits_type", I32), ("scale", F32)]
+
+
+_lib = block.declare({
+    "moe_score_router_workspace_size": [P, I32, P],
+    "moe_score_router_forward": [P, I32, P, I64, P, P, P, P, P, P, P, SZ, P],
+    "moe_score_router_backward": [P, I32, P, I64, P, P, P, I64, P],
+    "moe_score_router_update_bias": [I32, P, F32, P, P],
+})
+
+
+@dataclass(frozen=True)
+class ScoreRouterConfig:
+    """What a ScoreRouter is built for. It cannot be changed. score: "sigmoid" or "softmax"; group_score: "max"
+    or "top2" (the sum of a group's two largest)."""
+    num_experts: int
+    top_k: int
+    score: str = "sigmoid"
+    num_groups: int = 1
+    top_groups: int = 1
+    group_score: str = "top2"
+    renormalize: bool = True
+    scale: float = 1.0
+
+
+class ScoreRouter:
+    """Router by scores: the top-k experts by score plus bias among the best groups, their weights and per-expert
+    counts (moe_score_router_forward, moe_score_router_backward)."""
+
+    def __init__(self, cfg: ScoreRouterConfig):
+        # buffers are checked by what the library was told, whatever becomes of cfg
+        self._cfg, self._E, self._k = cfg, cfg.num_experts, cfg.top_k
+        if cfg.score not in SCORES or cfg.group_score not in GROUP_SCORES:
+            raise ValueError(f"score must be one of {list(SCORES)}, group_score one of {list(GROUP_SCORES)}, got "
+                             f"{cfg.score!r} and {cfg.group_score!r}")
+        self._c = {d: ScoreRouterConfigC(cfg.num_experts, cfg.top_k, SCORES[cfg.score], cfg.num_groups, cfg.top_groups,
+                                         GROUP_SCORES[cfg.group_score], 1 if cfg.renormalize else 0, code, cfg.scale)
+                   for d, code in LOGITS.items()}
+        self._ref = {d: byref(c) for d, c in self._c.items()}
+        self.workspace_size(0)
+        self._forward, self._backward = _lib().moe_score_router_forward, _lib().moe_score_router_backward
+
+    @property
+    def cfg(self) -> ScoreRouterConfig:
+        return self._cfg
+
+    def workspace_size(self, num_tokens: int) -> int:
+        n = SZ()
+        st = _lib().moe_score_router_workspace_size(byref(self._c[_F32]), num_tokens, byref(n))
+        if st != MOE_OK:
+            _fail("moe_score_router_workspace_size", st)
+        return n.value
+
+    def alloc(self, num_tokens: int, device=None) -> RouterOutput:
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        E, k, T = self._E, self._k, num_tokens
+        empty = torch.empty
+        return RouterOutput(empty((T, k), dtype=_I32, device=device), empty((T, k), dtype=_F32, device=device),
+                            empty(E, dtype=_I32, device=device), empty(1, dtype=_I32, device=device), None, None,
+                            empty(self.workspace_size(T), dtype=_U8, device=device))
+
+    def _logits(self, logits: torch.Tensor):
+        """Number of tokens, the logits' device and row stride."""
+        shape = _matrix("logits", logits)
+        dtype = logits.dtype
+        if dtype not in LOGITS:
+            raise ValueError(f"logits must be float32 or bfloat16, got {dtype}")
+        dev = _device_of("logits", logits)
+        ld = _row_stride("logits", logits, dtype, shape, dev)
+        if shape[1] != self._E:
+            raise ValueError(f"logits must be [T, {self._E}], got {tuple(shape)}")
+        return shape[0], dev, ld
+
+    def forward(self, logits: torch.Tensor, bias: torch.Tensor | None = None, token_mask: torch.Tensor | None = None,
+                out: RouterOutput | None = None, stream=None) -> RouterOutput:
+        """logits fp32 or bf16 [T, E]; bias fp32 [E]; token_mask bool [T] (False: padding). With out, its buffers
+        are written (counts and num_valid when it has them); else they are allocated. There is no balance loss:
+        prob_mean and loss are None."""
+        T, dev, ld = self._logits(logits)
+        E, k = self._E, self._k
+        pb = pm = None
+        if bias is not None:
+            _flat("bias", bias, _F32, E, dev)
+            pb = bias.data_ptr()
+        if token_mask is not None:
+            if token_mask.dtype not in (torch.bool, _U8):
+                raise ValueError("token_mask must be bool or uint8")
+            _flat("token_mask", token_mask, token_mask.dtype, T, dev)
+            pm = token_mask.data_ptr()
+        if out is None:
+            with _on(stream):
+                out = self.alloc(T, logits.device)
+        args = out._args
+        if args is None or args[0] != (T, E, k, dev) or [f() for f in args[2]] != args[3]:
+            if out.prob_mean is not None or out.loss is not None:
+                raise ValueError("a ScoreRouter has no balance loss: prob_mean and loss must be None")
+            out._check(T, E, k, dev)
+            args = out._args
+        ids, w, counts, valid, _, _, ws, n = args[1]
+        call = self._forward if dev == _current_device() else _at_device(self._forward, dev)
+        st = call(self._ref[logits.dtype], T, logits.data_ptr(), ld, pb, pm, ids, w, counts, valid, ws, n,
+                  _stream(stream, dev))
+        if st:
+            _fail("moe_score_router_forward", st)
+        return out
+
+    def backward(self, logits: torch.Tensor, topk_ids: torch.Tensor, d_weights: torch.Tensor,
+                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """The gradient of sum(d_weights * topk_weights) with respect to logits, in the logits' type (the choice
+        of experts held constant)."""
+        T, dev, ld = self._logits(logits)
+        if out is None:
+            with _on(stream):
+                out = torch.empty((T, self._E), dtype=logits.dtype, device=logits.device)
+        ldo = _row_stride("out", out, logits.dtype, logits.shape, dev)
+        _flat("topk_ids", topk_ids, _I32, T * self._k, dev)
+        _flat("d_weights", d_weights, _F32, T * self._k, dev)
+        call = self._backward if dev == _current_device() else _at_device(self._backward, dev)
+        st = call(self._ref[logits.dtype], T, logits.data_ptr(), ld, topk_ids.data_ptr(), d_weights.data_ptr(),
+                  out.data_ptr(), ldo, _stream(stream, dev))
+        if st:
+            _fail("moe_score_router_backward", st)
+        return out
+
+    def update_bias(self, bias: torch.Tensor, counts: torch.Tensor, rate: float, stream=None) -> torch.Tensor:
+        """bias += rate * sign(mean(counts) - counts), in place: one step towards even loads."""
+        dev = _device_of("bias", bias)
+        _flat("bias", bias, _F32, self._E, dev)
+        _flat("counts", counts, _I32, self._E, dev)
+        fn = _lib().moe_score_router_update_bias
+        call = fn if dev == _current_device() else _at_device(fn, dev)
+        st = call(self._E, counts.data_ptr(), rate, bias.data_ptr(), _stream(stream, dev))
+        if st:
+            _fail("moe_score_router_update_bias", st)
+        return bias
