@@ -408,6 +408,56 @@ int moe_add_rmsnorm(int32_t rows, int32_t hidden, const void* x, int64_t x_strid
                     void* out, int64_t out_stride, const moe_quant_t* q, void* stream);
 
 /*
+ * Sandwich norm: the norm after a block, its gate, the scaled residual and the norm before the next block:
+ *   u = gamma_post * f / sqrt(mean(f^2) + eps),  z = residual_scale * residual + gate * u,
+ *   h = gamma_pre * z / sqrt(mean(z^2) + eps);  sum_out = bf16(z), out = bf16(h), q = quantised h (from the fp32 h)
+ *   gate   by gate_kind: NULL (1), fp32 [rows] (one for each token) or fp32 [H] (one for each channel)
+ */
+#define MOE_GATE_NONE    0
+#define MOE_GATE_TOKEN   1
+#define MOE_GATE_CHANNEL 2
+typedef struct moe_sandwich {
+    const float* gamma_post;   /* fp32 [H] */
+    const float* gamma_pre;    /* fp32 [H] */
+    const float* gate;
+    int32_t gate_kind;         /* MOE_GATE_* */
+    float   residual_scale;    /* finite */
+    float   eps;               /* finite, >= 0 */
+} moe_sandwich_t;
+
+/*
+ *   f, residual, sum_out, out   bf16 [rows, H] with their own row strides; sum_out, out and q may be NULL, but one
+ *                               of out and q is given; sum_out may be residual or f, and out may be f or residual,
+ *                               at the same stride (each row is read before it is written); no other overlap
+ *   stats                       fp32 [rows, 2] or NULL: 1 / sqrt(mean + eps) of f and of z, for the backward pass
+ *   H                           1 .. 16384; a multiple of 32 with q
+ * Sums are fp32, in an order that depends on H, the alignment and the number of rows (152 or fewer, or more).
+ * Deterministic for the same call. rows == 0 launches nothing.
+ */
+int moe_sandwich_norm(int32_t rows, int32_t hidden, const moe_sandwich_t* p, const void* f, int64_t f_stride,
+                      const void* residual, int64_t residual_stride, void* sum_out, int64_t sum_stride, void* out,
+                      int64_t out_stride, const moe_quant_t* q, float* stats, void* stream);
+
+/* Bytes of the workspace of moe_sandwich_norm_backward (never 0). Host-only. */
+int moe_sandwich_norm_workspace_size(int32_t rows, int32_t hidden, size_t* bytes);
+
+/*
+ * The gradients of sum(d_sum * z) + sum(d_out * h) (rounding held constant).
+ *   f, residual, stats       as moe_sandwich_norm had and wrote them
+ *   d_sum, d_out             bf16 [rows, H] with their own row strides; one of them may be NULL (zeros)
+ *   d_f, d_residual          bf16 [rows, H]: written; each may be d_sum or d_out at the same stride, no other overlap
+ *   d_gate                   fp32 [rows] or [H] by gate_kind, d_gamma_post, d_gamma_pre fp32 [H]: each may be NULL
+ * Deterministic: every sum has a fixed order. With rows == 0 the gradients of gammas and gate are zeros. The
+ * workspace's contents do not matter.
+ */
+int moe_sandwich_norm_backward(int32_t rows, int32_t hidden, const moe_sandwich_t* p, const void* f, int64_t f_stride,
+                               const void* residual, int64_t residual_stride, const float* stats, const void* d_sum,
+                               int64_t d_sum_stride, const void* d_out, int64_t d_out_stride, void* d_f,
+                               int64_t d_f_stride, void* d_residual, int64_t d_residual_stride, float* d_gate,
+                               float* d_gamma_post, float* d_gamma_pre, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
  * Router: probabilities p = softmax(logits), the top_k experts of each token by descending
  * logit (ties to the lowest expert id), their weights p (renormalize: divided by their sum),
  * tokens per expert, and the balance loss

@@ -5,3 +5,5 @@ from .block import (LinearConfig, LinearPlan, LinearWeight, Quantized, Router, R
 from .moe import (FORMATS, LayerConfig, MoeError, Plan, config_workspace_size, error_string,  # noqa: F401
                   lib, library_path, permute_noalloc, validate)
 from .score_router import ScoreRouter, ScoreRouterConfig  # noqa: F401
+from .sandwich import (SandwichGrads, sandwich_norm, sandwich_norm_backward,  # noqa: F401
+                       sandwich_norm_workspace_size)

@@ -31,6 +31,30 @@ struct NormArgs {
 };
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
 
+// ------------------------------------------------------------------ sandwich norm
+struct SandwichArgs {
+    NormArgs n;              // x: the block's output f, res: the residual, gamma: the second norm's
+    const float* post;       // the first norm's gamma
+    const float* gate;       // by gate_kind: null, [T] or [H]
+    int gate_kind;
+    float alpha;             // of the residual
+    float* stats;            // [T][2]: 1 / rms(f), 1 / rms(z); or null
+};
+struct SandwichGradArgs {
+    const __nv_bfloat16 *f, *res, *d_sum, *d_out;  // d_sum or d_out may be null
+    __nv_bfloat16 *d_f, *d_res;
+    int64_t ldf, ldr, lds, ldo, ldd, ldg;
+    const float *post, *pre, *gate, *stats;
+    int gate_kind, T, H;
+    float alpha;
+    float inv_h;             // 1 / H (set by launch_sandwich_grad)
+    float *d_gate, *d_post, *d_pre;  // each may be null
+    float* part;             // sandwich_grad_floats
+};
+cudaError_t launch_sandwich(const SandwichArgs& a, cudaStream_t st);
+int64_t sandwich_grad_floats(int T, int H);
+cudaError_t launch_sandwich_grad(const SandwichGradArgs& a, cudaStream_t st);
+
 // ------------------------------------------------------------------ router
 struct RouterArgs {
     const void* logits;

@@ -104,6 +104,18 @@ int check_linear(const moe_linear_config_t* c) {
     return MOE_OK;
 }
 
+int check_sandwich(const moe_sandwich_t* p, int rows, int hidden) {
+    if (!p || rows < 0 || hidden < 1 || hidden > MAX_ROW) return MOE_ERR_INVALID_ARG;
+    if (p->gate_kind < MOE_GATE_NONE || p->gate_kind > MOE_GATE_CHANNEL) return MOE_ERR_UNSUPPORTED;
+    if (!(p->eps >= 0.0f) || !isfinite(p->eps) || !isfinite(p->residual_scale)) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!p->gamma_post || !p->gamma_pre || (p->gate_kind != MOE_GATE_NONE) != (p->gate != nullptr))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(p->gamma_post, 4) || !aligned_to(p->gamma_pre, 4) || !aligned_to(p->gate, 4))
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
 int check_router(const moe_router_config_t* c) {
     if (!c) return MOE_ERR_INVALID_ARG;
     if (c->num_experts < 1 || c->num_experts > MAX_EXPERTS) return MOE_ERR_INVALID_ARG;
@@ -282,6 +294,118 @@ int moe_add_rmsnorm(int32_t rows, int32_t hidden, const void* x, int64_t x_strid
         a.row_scale = q->row_scale;
     }
     CUDA_TRY(launch_norm(a, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+// ------------------------------------------------------------------ sandwich norm
+int moe_sandwich_norm(int32_t rows, int32_t hidden, const moe_sandwich_t* p, const void* f, int64_t f_stride,
+                      const void* residual, int64_t residual_stride, void* sum_out, int64_t sum_stride, void* out,
+                      int64_t out_stride, const moe_quant_t* q, float* stats, void* stream) {
+    int v = check_sandwich(p, rows, hidden);
+    if (v != MOE_OK) return v;
+    if (q && hidden % 32) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!out && !q) return MOE_ERR_INVALID_ARG;
+    if (q && (v = check_quant(q)) != MOE_OK) return v;
+    if (!f || !residual || !rows_ok(f, f_stride, rows, hidden) || !rows_ok(residual, residual_stride, rows, hidden) ||
+        (sum_out && !rows_ok(sum_out, sum_stride, rows, hidden)) || (out && !rows_ok(out, out_stride, rows, hidden)) ||
+        !aligned_to(stats, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (sum_out && sum_out == out) return MOE_ERR_INVALID_ARG;
+    SandwichArgs a{};
+    NormArgs& n = a.n;
+    n.x = (const __nv_bfloat16*)f;
+    n.ldx = f_stride;
+    n.res = (const __nv_bfloat16*)residual;
+    n.ldr = residual_stride;
+    n.gamma = p->gamma_pre;
+    n.eps = p->eps;
+    n.sum = (__nv_bfloat16*)sum_out;
+    n.lds = sum_stride;
+    n.out = (__nv_bfloat16*)out;
+    n.ldo = out_stride;
+    n.T = rows;
+    n.H = hidden;
+    n.fmt = -1;
+    if (q) {
+        n.fmt = q->format;
+        n.atoms = q->sf_layout == MOE_SF_ATOMS;
+        n.nks = stages_of(q->format, hidden);
+        n.codes = (uint8_t*)q->codes;
+        n.sf = (uint8_t*)q->sf;
+        n.row_scale = q->row_scale;
+    }
+    a.post = p->gamma_post;
+    a.gate = p->gate;
+    a.gate_kind = p->gate_kind;
+    a.alpha = p->residual_scale;
+    a.stats = stats;
+    CUDA_TRY(launch_sandwich(a, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+int moe_sandwich_norm_workspace_size(int32_t rows, int32_t hidden, size_t* bytes) {
+    if (!bytes || rows < 0 || hidden < 1 || hidden > MAX_ROW) return MOE_ERR_INVALID_ARG;
+    const int64_t need = 4 * sandwich_grad_floats(rows, hidden);
+    *bytes = (size_t)(need > 256 ? need : 256);
+    return MOE_OK;
+}
+
+int moe_sandwich_norm_backward(int32_t rows, int32_t hidden, const moe_sandwich_t* p, const void* f, int64_t f_stride,
+                               const void* residual, int64_t residual_stride, const float* stats, const void* d_sum,
+                               int64_t d_sum_stride, const void* d_out, int64_t d_out_stride, void* d_f,
+                               int64_t d_f_stride, void* d_residual, int64_t d_residual_stride, float* d_gate,
+                               float* d_gamma_post, float* d_gamma_pre, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    const int v = check_sandwich(p, rows, hidden);
+    if (v != MOE_OK) return v;
+    for (const void* q : {(const void*)stats, (const void*)d_gate, (const void*)d_gamma_post, (const void*)d_gamma_pre})
+        if (!aligned_to(q, 4)) return MOE_ERR_INVALID_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (rows == 0) {
+        for (float* g : {p->gate_kind == MOE_GATE_CHANNEL ? d_gate : nullptr, d_gamma_post, d_gamma_pre})
+            if (g) CUDA_TRY(cudaMemsetAsync(g, 0, 4 * (size_t)hidden, st));
+        return MOE_OK;
+    }
+    if (!f || !residual || !stats || (!d_sum && !d_out) || !d_f || !d_residual || d_f == d_residual ||
+        (d_gate && p->gate_kind == MOE_GATE_NONE))
+        return MOE_ERR_INVALID_ARG;
+    if (!rows_ok(f, f_stride, rows, hidden) || !rows_ok(residual, residual_stride, rows, hidden) ||
+        (d_sum && !rows_ok(d_sum, d_sum_stride, rows, hidden)) || (d_out && !rows_ok(d_out, d_out_stride, rows, hidden)) ||
+        !rows_ok(d_f, d_f_stride, rows, hidden) || !rows_ok(d_residual, d_residual_stride, rows, hidden))
+        return MOE_ERR_INVALID_ARG;
+    if (d_gamma_post || d_gamma_pre || (d_gate && p->gate_kind == MOE_GATE_CHANNEL)) {
+        size_t need = 0;
+        moe_sandwich_norm_workspace_size(rows, hidden, &need);
+        if (workspace && workspace_bytes < need) return MOE_ERR_WORKSPACE;
+        if (!workspace || !aligned_to(workspace, 256)) return MOE_ERR_INVALID_ARG;
+    }
+    SandwichGradArgs a{};
+    a.f = (const __nv_bfloat16*)f;
+    a.ldf = f_stride;
+    a.res = (const __nv_bfloat16*)residual;
+    a.ldr = residual_stride;
+    a.d_sum = (const __nv_bfloat16*)d_sum;
+    a.lds = d_sum_stride;
+    a.d_out = (const __nv_bfloat16*)d_out;
+    a.ldo = d_out_stride;
+    a.d_f = (__nv_bfloat16*)d_f;
+    a.ldd = d_f_stride;
+    a.d_res = (__nv_bfloat16*)d_residual;
+    a.ldg = d_residual_stride;
+    a.post = p->gamma_post;
+    a.pre = p->gamma_pre;
+    a.gate = p->gate;
+    a.stats = stats;
+    a.gate_kind = p->gate_kind;
+    a.T = rows;
+    a.H = hidden;
+    a.alpha = p->residual_scale;
+    a.d_gate = d_gate;
+    a.d_post = d_gamma_post;
+    a.d_pre = d_gamma_pre;
+    a.part = (float*)workspace;
+    CUDA_TRY(launch_sandwich_grad(a, st));
     return MOE_OK;
 }
 
