@@ -14,7 +14,8 @@
 //
 // Forward: a row lives in the registers of its threads between its one read and its writes, as in the
 // norm. Gradient: a thread keeps the same columns for every row of its CTA and sums C and dpre for them in
-// registers; each CTA leaves one row of sums to a second kernel, which adds them in a fixed order.
+// registers; each CTA leaves one row of sums to a second kernel, which adds them in a fixed order. Rows come
+// through a ring in shared memory, two ahead.
 #include "block.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -166,136 +167,387 @@ cudaError_t launch_sandwich(const SandwichArgs& args, cudaStream_t st) {
 // workspace's size, which a caller may ask for without a GPU.
 constexpr int SANDWICH_SMS = 152;
 
-// The sums of four values over a row's threads, in every thread. s: four values for each warp of the CTA.
-__device__ __forceinline__ float4 four_sums(float4 v, float4* s) {
-    const int lane = threadIdx.x % 32;
-    auto warp4 = [&](float4 u) {  // lanes 0, 8, 16, 24 end with the sums of x, z, y, w
-        const bool up = lane & 16, odd = lane & 8;
-        float a = (up ? u.y : u.x) + __shfl_xor_sync(0xffffffffu, up ? u.x : u.y, 16);
-        float b = (up ? u.w : u.z) + __shfl_xor_sync(0xffffffffu, up ? u.z : u.w, 16);
+// The sums of three values over a row's threads, in every thread. mine, all: this warp's and the row's first
+// place in shared memory, 16 bytes for each warp.
+__device__ __forceinline__ float3 three_sums(float x, float y, float z, uint32_t mine, uint32_t all, int warps, int lane) {
+    const bool up = lane & 16, odd = lane & 8;
+    auto add_up = [&](float x, float y, float z) {  // lanes 0.., 8.., 16.. end with the sums of x, z, y
+        float a = (up ? y : x) + __shfl_xor_sync(0xffffffffu, up ? x : y, 16);
+        const float b = z + __shfl_xor_sync(0xffffffffu, z, 16);
         a = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
         return a;
     };
-    float a = warp4(v);
-    const int warps = blockDim.x / 32;
+    float a = add_up(x, y, z);
     if (warps > 1) {
-        float* mine = reinterpret_cast<float*>(s + threadIdx.y * warps + threadIdx.x / 32);
-        if (lane % 8 == 0) mine[(lane & 16 ? 1 : 0) + (lane & 8 ? 2 : 0)] = a;
+        if (lane % 8 == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + lane / 2), "f"(a) : "memory");
         __syncthreads();
-        a = warp4(lane < warps ? s[threadIdx.y * warps + lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // x, z, y, (z)
+        if (lane < warps)
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                         : "r"(all + 16 * lane)
+                         : "memory");
+        a = add_up(v.x, v.z, v.y);
     }
-    return make_float4(__shfl_sync(0xffffffffu, a, 0), __shfl_sync(0xffffffffu, a, 16),
-                       __shfl_sync(0xffffffffu, a, 8), __shfl_sync(0xffffffffu, a, 24));
+    return make_float3(__shfl_sync(0xffffffffu, a, 0), __shfl_sync(0xffffffffu, a, 16), __shfl_sync(0xffffffffu, a, 8));
 }
 
-template <int MAXC, int MAXT, int MIN_CTAS, bool RAGGED>
-__global__ void __launch_bounds__(MAXT, MIN_CTAS)
-    sandwich_grad_kernel(const SandwichGradArgs a, const bool vectors_aligned) {
-    const int tid = threadIdx.x, NT = blockDim.x, H = a.H, chunks = (H + 7) / 8;
-    __shared__ float4 s_sums[2][NORM_MAX_WARPS];
-    extern __shared__ uint4 s_rows[];  // RAGGED: [rows][chunks]
-    uint4* s_row = s_rows + threadIdx.y * chunks;
-    grid_dep_wait();
-    grid_dep_launch();
-    const bool columns = a.part != nullptr;
-    float w[MAXC][8], pre[MAXC][8], c_sum[MAXC][8], p_sum[MAXC][8];
+// 16 bytes from global to shared memory, both aligned, behind the threads' backs; groups of copies
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 shared16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Pairs of floats in the packed instructions, which halve the count that would bound the gradient.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ f2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ f2 bf16_pair(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+__device__ __forceinline__ void halves(f2 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ float half_sum(f2 v) {
+    float lo, hi;
+    halves(v, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ uint32_t to_bf16(f2 v) {
+    float lo, hi;
+    halves(v, lo, hi);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ void put_shared16(uint32_t addr, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// How a thread's chunk of one matrix's rows comes into shared memory: of aligned rows as it is; RAGGED: as
+// the aligned 16-byte pieces that hold the row, chunk c in the pieces c and c + 1, of which a warp has 33. Nothing
+// outside the matrix is read: of pieces that reach over its ends only what belongs to the row.
+template <bool RAGGED>
+struct RowRing {
+    static constexpr int SLOTS = RAGGED ? 33 : 32;  // of a warp
+    // `row` is the row's first element, `at` this lane's slot for chunk c. ends: this is one of the first or
+    // last rows, whose pieces may reach over the matrix's ends.
+    static __device__ __forceinline__ void issue(uint32_t at, const uint8_t* row, int H, int c, int lane, bool ends,
+                                                 int64_t before, int64_t behind) {
+        if constexpr (!RAGGED) {
+            if (8 * c < H) copy16(at, row + 16 * c);
+        } else {
+            const int m = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+            auto piece = [&](uint32_t to, int b) {  // the piece whose first byte is b in the row
+                if (b >= 2 * H) return;
+                if (!ends || (b >= -(int)min((int64_t)16, before) && b + 16 <= 2 * H + (int)min((int64_t)16, behind))) {
+                    copy16(to, row + b);
+                } else {
+                    put_shared16(to, RowLoad<1, true>::edge(reinterpret_cast<const __nv_bfloat16*>(row), b / 2, H));
+                }
+            };
+            piece(at, 16 * c - m);
+            if (lane == 31) piece(at + 16, 16 * c + 16 - m);
+        }
+    }
+    // The chunk with `left` elements of the row from its first on, zeros past the row (slots that no copy
+    // writes hold zeros); m: the row's bytes past a 16-byte boundary.
+    static __device__ __forceinline__ uint4 chunk(uint32_t at, int m, int left) {
+        if constexpr (!RAGGED) {
+            return shared16(at);
+        } else {
+            uint4 v = cut(shared16(at), shared16(at + 16), m);
+            if (left < 8) {
+                v.x = left <= 0 ? 0u : left == 1 ? v.x & 0xFFFFu : v.x;
+                v.y = left <= 2 ? 0u : left == 3 ? v.y & 0xFFFFu : v.y;
+                v.z = left <= 4 ? 0u : left == 5 ? v.z & 0xFFFFu : v.z;
+                v.w = left <= 6 ? 0u : left == 7 ? v.w & 0xFFFFu : v.w;
+            }
+            return v;
+        }
+    }
+    // Chunk c of a row of the output. RAGGED: the destination's aligned pieces, each cut out of two
+    // neighbouring lanes' chunks; where a warp's chunks begin and end, and at the row's ends, 2 bytes at a time.
+    static __device__ __forceinline__ void store(uint8_t* row, const uint4& v, int H, int c, int lane, bool live) {
+        if constexpr (!RAGGED) {
+            if (live && 8 * c < H) *reinterpret_cast<uint4*>(row + 16 * c) = v;
+        } else {
+            uint4 before;
+            before.x = __shfl_up_sync(0xffffffffu, v.x, 1);
+            before.y = __shfl_up_sync(0xffffffffu, v.y, 1);
+            before.z = __shfl_up_sync(0xffffffffu, v.z, 1);
+            before.w = __shfl_up_sync(0xffffffffu, v.w, 1);
+            const int m = (int)(reinterpret_cast<uintptr_t>(row) & 15), b = 16 * c - m;
+            if (!live || 8 * c >= H) return;
+            const bool whole = b >= 0 && b + 16 <= 2 * H && (lane > 0 || m == 0);
+            if (whole) *reinterpret_cast<uint4*>(row + b) = m == 0 ? v : cut(before, v, 16 - m);
+            // whether the next piece, with the last m bytes of this chunk, is not one of this warp's whole ones
+            const bool tail = lane == 31 || b + 32 > 2 * H;
+            if (!whole || tail) {
+                uint16_t* o = reinterpret_cast<uint16_t*>(row) + 8 * c;
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < MAXC; ++i) {
-        const int c = tid + i * NT;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[i][j] = pre[i][j] = c_sum[i][j] = p_sum[i][j] = 0.0f;
-        if (c < chunks) {
-            load_gamma(w[i], a.post, c, H, vectors_aligned);
-            load_gamma(pre[i], a.pre, c, H, vectors_aligned);
-            if (a.gate_kind == MOE_GATE_CHANNEL) {
-                float g[8];
-                load_gamma(g, a.gate, c, H, vectors_aligned);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[i][j] *= g[j];
+                for (int j = 0; j < 8; ++j)
+                    if ((2 * j >= 16 - m ? tail : !whole) && 8 * c + j < H) o[j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
             }
         }
     }
-    int round = 0;
-    for (int64_t t0 = (int64_t)blockIdx.x * blockDim.y; t0 < a.T; t0 += (int64_t)gridDim.x * blockDim.y, round ^= 1) {
-        const int64_t t = t0 + threadIdx.y;
-        const bool live = t < a.T;
-        const int nchunks = live ? chunks : 0;
-        RowLoad<MAXC, RAGGED> fv, rv, sv, ov;
-        fv.issue(a.f, a.ldf, t, a.T, H, nchunks, tid, NT);
-        rv.issue(a.res, a.ldr, t, a.T, H, nchunks, tid, NT);
-        if (a.d_sum) sv.issue(a.d_sum, a.lds, t, a.T, H, nchunks, tid, NT);
-        if (a.d_out) ov.issue(a.d_out, a.ldo, t, a.T, H, nchunks, tid, NT);
-        const float rf = live ? a.stats[2 * t] : 0.0f, rz = live ? a.stats[2 * t + 1] : 0.0f;
-        const float gt = live && a.gate_kind == MOE_GATE_TOKEN ? a.gate[t] : 1.0f;
-        float fh[MAXC][8], zh[MAXC][8], e[MAXC][8], ds[MAXC][8];
-        float4 sums = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // e zh, w fh ds, w fh e, w fh zh
+};
+
+// One row of a CTA's row group at a time, STAGES - 1 rows ahead on their way into shared memory: a thread
+// copies what it reads itself (RAGGED: its warp does), so that no barrier belongs to that. Chunks are
+// read twice, before and after the sums over the row, rather than held in registers: these hold the
+// columns' sums and, for one chunk a thread, the columns' factors w and pre.
+template <int MAXC, int MAXT, int MIN_CTAS, int STAGES, bool RAGGED, bool MANY>
+__global__ void __launch_bounds__(MAXT, MIN_CTAS)
+    sandwich_grad_kernel(const __grid_constant__ SandwichGradArgs a, const bool vectors_aligned) {
+    using Ring = RowRing<RAGGED>;
+    constexpr uint32_t MATRIX = 16 * Ring::SLOTS * (MAXT / 32), STAGE = 4 * MAXC * MATRIX;
+    // MANY: the CTA has several rows at a time. Otherwise a row's addresses are the same for all of its threads
+    // and stay in uniform registers.
+    const int y = MANY ? threadIdx.y : 0, rows_at_once = MANY ? blockDim.y : 1;
+    const int tid = threadIdx.x, lane = tid % 32, NT = blockDim.x, H = a.H, chunks = (H + 7) / 8;
+    __shared__ float4 s_sums[2][NORM_MAX_WARPS];
+    extern __shared__ uint4 s_ring[];  // [stage][matrix][chunk of a thread][warp of the CTA][SLOTS]
+    const int row_warps = NT / 32, warp = y * row_warps + tid / 32;
+    // this thread's slot for the matrix and the chunk 0 of stage 0; the others are at constant distances
+    const uint32_t slot = smem_u32(s_ring) + 16 * Ring::SLOTS * warp + 16 * lane;
+    const uint32_t row_place = smem_u32(s_sums) + 16 * y * row_warps, warp_place = row_place + 16 * (tid / 32);
+    grid_dep_wait();
+    grid_dep_launch();
+    const int T = a.T, step = gridDim.x * rows_at_once;
+    int t = blockIdx.x * rows_at_once + y;
+    auto issue = [&](int next, uint32_t stage_at) {  // the copies of row `next`
+        if (next < T) {
+            const bool ends = RAGGED && (next < 16 || T - next <= 16);  // a stride may be one element
+            auto matrix = [&](int n, const __nv_bfloat16* p, int64_t ld) {
+                const uint8_t* row = reinterpret_cast<const uint8_t*>(p + next * ld);
+#pragma unroll
+                for (int i = 0; i < MAXC; ++i)
+                    Ring::issue(stage_at + (n * MAXC + i) * MATRIX, row, H, tid + i * NT, lane, ends, 2 * next * ld,
+                                2 * (T - 1 - next) * ld);
+            };
+            matrix(0, a.f, a.ldf);
+            matrix(1, a.res, a.ldr);
+            if (a.d_sum) matrix(2, a.d_sum, a.lds);
+            if (a.d_out) matrix(3, a.d_out, a.ldo);
+        }
+        copies_end_group();
+    };
+    // slots that no copy ever writes (past the row, of a matrix that is not there) are zeros
+#pragma unroll
+    for (int n = 0; n < STAGES * 4 * MAXC; ++n) {
+        put_shared16(slot + n * MATRIX, make_uint4(0, 0, 0, 0));
+        if (RAGGED && lane == 31) put_shared16(slot + n * MATRIX + 16, make_uint4(0, 0, 0, 0));
+    }
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) issue(t + s * step, slot + s * STAGE);
+    const bool columns = a.part != nullptr, token = a.gate_kind == MOE_GATE_TOKEN;
+    // the columns' factors of half a chunk (n: which half)
+    auto load_factors = [&](int c, int n, float4& w, float4& e) {
+        float p[4] = {0.0f, 0.0f, 0.0f, 0.0f}, q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const int h = 8 * c + 4 * n;
+        if (vectors_aligned && h + 4 <= H) {
+            const float4 u = *reinterpret_cast<const float4*>(a.post + h), v = *reinterpret_cast<const float4*>(a.pre + h);
+            p[0] = u.x, p[1] = u.y, p[2] = u.z, p[3] = u.w;
+            q[0] = v.x, q[1] = v.y, q[2] = v.z, q[3] = v.w;
+            if (a.gate_kind == MOE_GATE_CHANNEL) {
+                const float4 g = *reinterpret_cast<const float4*>(a.gate + h);
+                p[0] *= g.x, p[1] *= g.y, p[2] *= g.z, p[3] *= g.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (h + j < H) {
+                    p[j] = a.gate_kind == MOE_GATE_CHANNEL ? a.post[h + j] * a.gate[h + j] : a.post[h + j];
+                    q[j] = a.pre[h + j];
+                }
+        }
+        w = make_float4(p[0], p[1], p[2], p[3]);
+        e = make_float4(q[0], q[1], q[2], q[3]);
+    };
+    constexpr bool KEPT = MAXC * MAXT <= 1024;  // in registers
+    f2 kept_w[MAXC][4], kept_pre[MAXC][4];
+    auto as_pairs = [](const float4& v, f2* to) { to[0] = pair(v.x, v.y), to[1] = pair(v.z, v.w); };
+    if constexpr (KEPT) {
+#pragma unroll
+        for (int n = 0; n < 2 * MAXC; ++n) {
+            float4 w, e;
+            load_factors(tid + n / 2 * NT, n % 2, w, e);
+            as_pairs(w, kept_w[n / 2] + n % 2 * 2);
+            as_pairs(e, kept_pre[n / 2] + n % 2 * 2);
+        }
+    }
+    auto factors = [&](int i, int n, f2 (&w)[2], f2 (&pre)[2]) {
+        if constexpr (KEPT) {
+            w[0] = kept_w[i][2 * n], w[1] = kept_w[i][2 * n + 1];
+            pre[0] = kept_pre[i][2 * n], pre[1] = kept_pre[i][2 * n + 1];
+        } else {
+            float4 p, q;
+            load_factors(tid + i * NT, n, p, q);
+            as_pairs(p, w);
+            as_pairs(q, pre);
+        }
+    };
+    f2 c_sum[MAXC][4], p_sum[MAXC][4];
+#pragma unroll
+    for (int i = 0; i < MAXC; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c_sum[i][k] = p_sum[i][k] = 0ull;
+    // a row's own factors, fetched one row ahead: 1 / rms(f), 1 / rms(z), the token's gate
+    float own_f = 0.0f, own_z = 0.0f, own_g = 1.0f;
+    auto fetch = [&](int row) {
+        if (row < T) {
+            own_f = a.stats[2 * (int64_t)row];
+            own_z = a.stats[2 * (int64_t)row + 1];
+            if (token) own_g = a.gate[row];
+        }
+    };
+    fetch(t);
+    const f2 alpha = both(a.alpha);
+    uint32_t at = slot, ahead = slot + (STAGES - 1) * STAGE, other = 0;
+    for (int t0 = blockIdx.x * rows_at_once; t0 < T; t0 += step, t += step) {
+        const bool live = !MANY || t < T;
+        // where the rows' chunks begin in their pieces
+        int m[4] = {0, 0, 0, 0};
+        if constexpr (RAGGED) {
+            auto past = [&](const __nv_bfloat16* p, int64_t ld) { return (int)(reinterpret_cast<uintptr_t>(p + t * ld) & 15); };
+            m[0] = past(a.f, a.ldf), m[1] = past(a.res, a.ldr), m[2] = past(a.d_sum, a.lds), m[3] = past(a.d_out, a.ldo);
+            __syncwarp();  // the last row in that stage has been read by the whole warp
+        }
+        issue(t + (STAGES - 1) * step, ahead);
+        const float rf = live ? own_f : 0.0f, rz = live ? own_z : 0.0f, gt = own_g;
+        fetch(t + step);
+        copies_wait<STAGES - 1>();
+        if constexpr (RAGGED) __syncwarp();  // the neighbours' copies have landed too
+        // a chunk of the four matrices as it lies in shared memory
+        auto read = [&](int i, uint4 (&v)[4]) {
+            const int left = H - 8 * (tid + i * NT);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) v[n] = Ring::chunk(at + (n * MAXC + i) * MATRIX, m[n], left);
+        };
+        auto word = [](uint4& v, int k) -> uint32_t& { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; };
+        // The rows' factors 1 / rms(f) and 1 / rms(z) go into the sums and results, not into every element:
+        // with u = w f, z = alpha r + gt rf u, ds + e / rms(z) the first part of dz
+        const f2 to_z = both(gt * rf), zs = both(rz);
+        float ez_all = 0.0f, ud_all = 0.0f, uz_all = 0.0f;
+#pragma unroll
+        for (int i = 0; i < MAXC; ++i) {
+            uint4 v[4];
+            read(i, v);
+            if constexpr (RAGGED) {  // as chunks from here on: cut once
+                __syncwarp();
+#pragma unroll
+                for (int n = 0; n < 4; ++n) put_shared16(at + (n * MAXC + i) * MATRIX, v[n]);
+            }
+            f2 w[2], pre[2];
+            f2 ez = 0ull, ud = 0ull, uz = 0ull;  // by chunks, as in the norm
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k % 2 == 0) factors(i, k / 2, w, pre);
+                const f2 u = mul2(w[k % 2], bf16_pair(word(v[0], k))), e = mul2(pre[k % 2], bf16_pair(word(v[3], k)));
+                const f2 z = fma2(to_z, u, mul2(alpha, bf16_pair(word(v[1], k))));
+                ez = fma2(e, z, ez);
+                ud = fma2(u, fma2(zs, e, bf16_pair(word(v[2], k))), ud);
+                uz = fma2(u, z, uz);
+            }
+            ez_all += half_sum(ez), ud_all += half_sum(ud), uz_all += half_sum(uz);
+        }
+        // two places: the last row's may still be read
+        const float3 s = three_sums(ez_all, ud_all, uz_all, warp_place + other, row_place + other, row_warps, lane);
+        other ^= 16 * NORM_MAX_WARPS;
+        // mean(e zh), sum(w fh dz), and the second mean
+        const float m1 = rz * s.x * a.inv_h, total = rf * fmaf(-m1 * rz * rz, s.z, s.y), m2 = gt * total * a.inv_h;
+        if (token && a.d_gate && live && tid == 0) a.d_gate[t] = total;
+        const f2 less_z = both(-m1 * rz * rz), less_f = both(-m2 * rf * rf);
 #pragma unroll
         for (int i = 0; i < MAXC; ++i) {
             const int c = tid + i * NT;
-            unpack_bf16x8(fv.chunk(i, a.f + t * a.ldf, c, H), fh[i]);
-            unpack_bf16x8(rv.chunk(i, a.res + t * a.ldr, c, H), zh[i]);
+            uint4 v[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ds[i][j] = e[i][j] = 0.0f;
-            if (a.d_sum) unpack_bf16x8(sv.chunk(i, a.d_sum + t * a.lds, c, H), ds[i]);
-            if (a.d_out) unpack_bf16x8(ov.chunk(i, a.d_out + t * a.ldo, c, H), e[i]);
-            float4 part = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // by chunks, as in the norm
+            for (int n = 0; n < 4; ++n) v[n] = shared16(at + (n * MAXC + i) * MATRIX);
+            f2 w[2], pre[2];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                fh[i][j] *= rf;
-                const float u = w[i][j] * fh[i][j];
-                zh[i][j] = fmaf(gt, u, a.alpha * zh[i][j]) * rz;
-                if (columns) p_sum[i][j] = fmaf(e[i][j], zh[i][j], p_sum[i][j]);
-                e[i][j] *= pre[i][j];
-                part.x = fmaf(e[i][j], zh[i][j], part.x);
-                part.y = fmaf(u, ds[i][j], part.y);
-                part.z = fmaf(u, e[i][j], part.z);
-                part.w = fmaf(u, zh[i][j], part.w);
+            for (int k = 0; k < 4; ++k) {
+                if (k % 2 == 0) factors(i, k / 2, w, pre);
+                const f2 f = bf16_pair(word(v[0], k)), dh = mul2(zs, bf16_pair(word(v[3], k)));
+                const f2 z = fma2(to_z, mul2(w[k % 2], f), mul2(alpha, bf16_pair(word(v[1], k))));
+                const f2 dz = fma2(less_z, z, fma2(pre[k % 2], dh, bf16_pair(word(v[2], k))));
+                const f2 gz = mul2(to_z, dz);
+                p_sum[i][k] = fma2(dh, z, p_sum[i][k]);
+                c_sum[i][k] = fma2(f, gz, c_sum[i][k]);
+                word(v[0], k) = to_bf16(fma2(less_f, f, mul2(w[k % 2], gz)));
+                word(v[1], k) = to_bf16(mul2(alpha, dz));
             }
-            sums.x += part.x, sums.y += part.y, sums.z += part.z, sums.w += part.w;
+            Ring::store(reinterpret_cast<uint8_t*>(a.d_f + t * a.ldd), v[0], H, c, lane, live);
+            Ring::store(reinterpret_cast<uint8_t*>(a.d_res + t * a.ldg), v[1], H, c, lane, live);
         }
-        const float4 s = four_sums(sums, s_sums[round]);  // two places: the last row's may still be read
-        const float m1 = s.x * a.inv_h, total = fmaf(rz, fmaf(-m1, s.w, s.z), s.y), m2 = gt * total * a.inv_h;
-        if (a.gate_kind == MOE_GATE_TOKEN && a.d_gate && live && tid == 0) a.d_gate[t] = total;
-#pragma unroll
-        for (int i = 0; i < MAXC; ++i) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float dz = fmaf(rz, fmaf(-m1, zh[i][j], e[i][j]), ds[i][j]);
-                if (columns) c_sum[i][j] = fmaf(gt * fh[i][j], dz, c_sum[i][j]);
-                fh[i][j] = rf * fmaf(-m2, fh[i][j], gt * w[i][j] * dz);  // df
-                ds[i][j] = a.alpha * dz;                                 // dr
-            }
-        }
-        auto store = [&](const float (&v)[MAXC][8], __nv_bfloat16* dst) {
-#pragma unroll
-            for (int i = 0; i < MAXC; ++i) {
-                const int c = tid + i * NT;
-                if (c < nchunks) (RAGGED ? s_row : reinterpret_cast<uint4*>(dst))[c] = pack_bf16x8_rn(v[i]);
-            }
-            if constexpr (RAGGED) {
-                row_barrier();
-                if (live) store_ragged(s_row, dst, H, tid, NT);
-                row_barrier();  // shared memory is written again
-            }
-        };
-        store(fh, a.d_f + t * a.ldd);
-        store(ds, a.d_res + t * a.ldg);
+        at = at == slot + (STAGES - 1) * STAGE ? slot : at + STAGE;
+        ahead = ahead == slot + (STAGES - 1) * STAGE ? slot : ahead + STAGE;
     }
     if (columns) {
-        const int64_t rows = (int64_t)gridDim.x * blockDim.y, at = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-        const int64_t ld = 8 * (int64_t)chunks;
+        if constexpr (MANY) {  // the CTA's rows in order, through shared memory (the copies' last reader has left)
+            f2* s_all = reinterpret_cast<f2*>(s_ring);  // [y][tid][8 MAXC]
+            copies_wait<0>();
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < MAXC; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    s_all[(8 * i + k) * blockDim.y * NT + y * NT + tid] = p_sum[i][k];
+                    s_all[(8 * i + 4 + k) * blockDim.y * NT + y * NT + tid] = c_sum[i][k];
+                }
+            __syncthreads();
+            if (y > 0) return;
+            for (int r = 1; r < rows_at_once; ++r)
+#pragma unroll
+                for (int i = 0; i < MAXC; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        p_sum[i][k] = add2(p_sum[i][k], s_all[(8 * i + k) * blockDim.y * NT + r * NT + tid]);
+                        c_sum[i][k] = add2(c_sum[i][k], s_all[(8 * i + 4 + k) * blockDim.y * NT + r * NT + tid]);
+                    }
+        }
+        const int64_t width = 8 * (int64_t)chunks;
 #pragma unroll
         for (int i = 0; i < MAXC; ++i) {
             const int c = tid + i * NT;
             if (c < chunks) {
-                float4* p = reinterpret_cast<float4*>(a.part + at * ld) + 2 * c;
-                float4* q = reinterpret_cast<float4*>(a.part + (rows + at) * ld) + 2 * c;
-                p[0] = make_float4(p_sum[i][0], p_sum[i][1], p_sum[i][2], p_sum[i][3]);
-                p[1] = make_float4(p_sum[i][4], p_sum[i][5], p_sum[i][6], p_sum[i][7]);
-                q[0] = make_float4(c_sum[i][0], c_sum[i][1], c_sum[i][2], c_sum[i][3]);
-                q[1] = make_float4(c_sum[i][4], c_sum[i][5], c_sum[i][6], c_sum[i][7]);
+                ulonglong2* p = reinterpret_cast<ulonglong2*>(a.part + blockIdx.x * width) + 2 * c;
+                ulonglong2* q = reinterpret_cast<ulonglong2*>(a.part + (gridDim.x + blockIdx.x) * width) + 2 * c;
+                p[0] = make_ulonglong2(p_sum[i][0], p_sum[i][1]);
+                p[1] = make_ulonglong2(p_sum[i][2], p_sum[i][3]);
+                q[0] = make_ulonglong2(c_sum[i][0], c_sum[i][1]);
+                q[1] = make_ulonglong2(c_sum[i][2], c_sum[i][3]);
             }
         }
     }
@@ -339,35 +591,46 @@ struct GradShape {
 GradShape grad_shape(int T, int H) {
     const int64_t chunks = ceil_div(H, 8);
     GradShape s;
-    s.maxc = chunks <= 1024 ? 1 : 2;
+    s.maxc = chunks <= 32 ? 1 : chunks <= 1024 ? 2 : 4;
     s.threads = (int)align_up(ceil_div(chunks, s.maxc), 32);
     s.rows = s.threads >= SANDWICH_CTA ? 1 : SANDWICH_CTA / s.threads;
-    const int resident = s.threads <= 256 ? 3 : s.threads <= 512 ? 2 : 1;
+    const int resident = s.threads <= 128 ? 4 : s.threads <= 192 ? 3 : s.threads <= 320 ? 2 : 1;
     const int64_t want = ceil_div(T, s.rows), most = (int64_t)SANDWICH_SMS * resident;
     s.grid = (int)(want < most ? want : most);
     return s;
 }
 
-template <int MAXC, int MAXT, int MIN_CTAS, bool RAGGED>
+template <int MAXC, int MAXT, int MIN_CTAS, int STAGES, bool RAGGED, bool MANY = false>
 cudaError_t grad_t(const SandwichGradArgs& a, const GradShape& s, cudaStream_t st) {
+    const auto kernel = sandwich_grad_kernel<MAXC, MAXT, MIN_CTAS, STAGES, RAGGED, MANY>;
+    constexpr size_t SMEM = (size_t)STAGES * 4 * MAXC * (MAXT / 32) * 16 * RowRing<RAGGED>::SLOTS;
+    static_assert(MIN_CTAS * (SMEM + 2048) <= 233472 && SMEM <= 232448 - 1024, "shared memory budget");
+    if (SMEM > 40 * 1024) {  // 48 KB with the static arrays need no leave
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+        if (e != cudaSuccess) return e;
+    }
     LaunchAttrs at(true);
-    cudaLaunchConfig_t cfg = at.config(dim3((unsigned)s.grid), dim3((unsigned)s.threads, (unsigned)s.rows),
-                                       RAGGED ? (size_t)s.rows * ceil_div(a.H, 8) * 16 : 0, st);
+    cudaLaunchConfig_t cfg = at.config(dim3((unsigned)s.grid), dim3((unsigned)s.threads, (unsigned)s.rows), SMEM, st);
     const uintptr_t v = (uintptr_t)a.post | (uintptr_t)a.pre | (a.gate_kind == MOE_GATE_CHANNEL ? (uintptr_t)a.gate : 0);
-    return cudaLaunchKernelEx(&cfg, sandwich_grad_kernel<MAXC, MAXT, MIN_CTAS, RAGGED>, a, v % 16 == 0);
+    return cudaLaunchKernelEx(&cfg, kernel, a, v % 16 == 0);
 }
 template <bool RAGGED>
 cudaError_t grad_r(const SandwichGradArgs& a, const GradShape& s, cudaStream_t st) {
-    if (s.maxc == 2) return grad_t<2, 1024, 1, RAGGED>(a, s, st);
-    if (s.threads * s.rows <= 256) return grad_t<1, 256, 3, RAGGED>(a, s, st);
-    if (s.threads <= 512) return grad_t<1, 512, 2, RAGGED>(a, s, st);
-    return grad_t<1, 1024, 1, RAGGED>(a, s, st);
+    if (s.maxc == 4) return grad_t<4, 512, 1, 1, RAGGED>(a, s, st);
+    if (s.maxc == 1) return grad_t<1, 128, 4, 3, RAGGED, true>(a, s, st);
+    if (s.rows > 1) return grad_t<2, 128, 4, 3, RAGGED, true>(a, s, st);
+    if (s.threads <= 128) return grad_t<2, 128, 4, 3, RAGGED>(a, s, st);
+    if (s.threads <= 192) return grad_t<2, 192, 3, RAGGED ? 2 : 3, RAGGED>(a, s, st);
+    if (s.threads <= 256) return grad_t<2, 256, 2, 3, RAGGED>(a, s, st);
+    if (s.threads <= 320) return grad_t<2, 320, 2, 2, RAGGED>(a, s, st);
+    if (s.threads <= 448) return grad_t<2, 448, 1, 3, RAGGED>(a, s, st);
+    return grad_t<2, 512, 1, 3, RAGGED>(a, s, st);
 }
 }  // namespace
 
 int64_t sandwich_grad_floats(int T, int H) {
     const GradShape s = grad_shape(T, H);
-    return 2 * (int64_t)s.grid * s.rows * align_up(H, 8);
+    return 2 * (int64_t)s.grid * align_up(H, 8);
 }
 
 cudaError_t launch_sandwich_grad(const SandwichGradArgs& args, cudaStream_t st) {
@@ -387,7 +650,7 @@ cudaError_t launch_sandwich_grad(const SandwichGradArgs& args, cudaStream_t st) 
     if (e != cudaSuccess || !a.part) return e;
     LaunchAttrs at(true);
     cudaLaunchConfig_t cfg = at.config(dim3((unsigned)ceil_div(a.H, 32)), dim3(COLUMN_THREADS), 0, st);
-    return cudaLaunchKernelEx(&cfg, sandwich_columns_kernel, a, s.grid * s.rows);
+    return cudaLaunchKernelEx(&cfg, sandwich_columns_kernel, a, s.grid);
 }
 
 }  // namespace moe
