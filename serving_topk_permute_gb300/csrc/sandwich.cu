@@ -114,86 +114,7 @@ __global__ void __launch_bounds__(MAXT, MIN_CTAS) sandwich_kernel(const Sandwich
     if constexpr (FMT >= 0) quantize_row<FMT, MAXC>(n, z, t, live, nchunks, s_red3);
 }
 
-constexpr int SANDWICH_CTA = 128;  // rows of fewer threads share a CTA of about this many
-
-template <int FMT, int MAXC, int MAXT, int MIN_CTAS, bool RAGGED>
-static cudaError_t sandwich_t(const SandwichArgs& a, cudaStream_t st) {
-    const int64_t chunks = ceil_div(a.n.H, 8), threads = align_up(ceil_div(chunks, MAXC), 32);
-    const int64_t rows = threads >= SANDWICH_CTA ? 1 : SANDWICH_CTA / threads;
-    LaunchAttrs at(true);
-    cudaLaunchConfig_t cfg =
-        at.config(dim3((unsigned)ceil_div(a.n.T, rows)), dim3((unsigned)threads, (unsigned)rows),
-                  RAGGED && (a.n.sum || a.n.out) ? (size_t)(rows * chunks * 16) : 0, st);
-    const uintptr_t v = (uintptr_t)a.post | (uintptr_t)a.n.gamma |
-                        (a.gate_kind == MOE_GATE_CHANNEL ? (uintptr_t)a.gate : 0);
-    return cudaLaunchKernelEx(&cfg, sandwich_kernel<FMT, MAXC, MAXT, MIN_CTAS, RAGGED>, a, v % 16 == 0);
-}
-
-template <int FMT, bool RAGGED>
-static cudaError_t sandwich_f(const SandwichArgs& a, cudaStream_t st) {
-    if (a.n.T <= 152 && a.n.H <= 8192) return sandwich_t<FMT, 1, 1024, 1, RAGGED>(a, st);
-    if (a.n.H <= 4096) return sandwich_t<FMT, 2, 256, RAGGED ? 4 : 5, RAGGED>(a, st);
-    if constexpr (RAGGED) {
-        return sandwich_t<FMT, 2, 1024, 1, true>(a, st);
-    } else {
-        if (a.n.H <= 7168) return sandwich_t<FMT, 4, 224, 5, false>(a, st);
-        return sandwich_t<FMT, 4, 512, 2, false>(a, st);
-    }
-}
-
-cudaError_t launch_sandwich(const SandwichArgs& args, cudaStream_t st) {
-    SandwichArgs a = args;
-    NormArgs& n = a.n;
-    n.inv_h = 1.0f / (float)n.H;
-    // whether the sizes, strides and addresses give every row whole, aligned 16-byte pieces
-    uintptr_t bits = (uintptr_t)n.x | (uintptr_t)(2 * n.ldx) | (uintptr_t)(2 * n.H) | (uintptr_t)n.res |
-                     (uintptr_t)(2 * n.ldr);
-    if (n.sum) bits |= (uintptr_t)n.sum | (uintptr_t)(2 * n.lds);
-    if (n.out) bits |= (uintptr_t)n.out | (uintptr_t)(2 * n.ldo);
-    const bool ragged = bits % 16 != 0;
-    switch (n.fmt) {
-        case MOE_FMT_MXFP8:
-            return ragged ? sandwich_f<MOE_FMT_MXFP8, true>(a, st) : sandwich_f<MOE_FMT_MXFP8, false>(a, st);
-        case MOE_FMT_NVFP4:
-            return ragged ? sandwich_f<MOE_FMT_NVFP4, true>(a, st) : sandwich_f<MOE_FMT_NVFP4, false>(a, st);
-        case MOE_FMT_MXFP4:
-            return ragged ? sandwich_f<MOE_FMT_MXFP4, true>(a, st) : sandwich_f<MOE_FMT_MXFP4, false>(a, st);
-        default: return ragged ? sandwich_f<-1, true>(a, st) : sandwich_f<-1, false>(a, st);
-    }
-}
-
-// ------------------------------------------------------------------ gradient
-// SMs of the GPU this is built for: how many CTAs share the column sums is part of their order and of the
-// workspace's size, which a caller may ask for without a GPU.
-constexpr int SANDWICH_SMS = 152;
-
-// The sums of three values over a row's threads, in every thread. mine, all: this warp's and the row's first
-// place in shared memory, 16 bytes for each warp.
-__device__ __forceinline__ float3 three_sums(float x, float y, float z, uint32_t mine, uint32_t all, int warps, int lane) {
-    const bool up = lane & 16, odd = lane & 8;
-    auto add_up = [&](float x, float y, float z) {  // lanes 0.., 8.., 16.. end with the sums of x, z, y
-        float a = (up ? y : x) + __shfl_xor_sync(0xffffffffu, up ? x : y, 16);
-        const float b = z + __shfl_xor_sync(0xffffffffu, z, 16);
-        a = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-        return a;
-    };
-    float a = add_up(x, y, z);
-    if (warps > 1) {
-        if (lane % 8 == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + lane / 2), "f"(a) : "memory");
-        __syncthreads();
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // x, z, y, (z)
-        if (lane < warps)
-            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                         : "r"(all + 16 * lane)
-                         : "memory");
-        a = add_up(v.x, v.z, v.y);
-    }
-    return make_float3(__shfl_sync(0xffffffffu, a, 0), __shfl_sync(0xffffffffu, a, 16), __shfl_sync(0xffffffffu, a, 8));
-}
-
+// ------------------------------------------------------------------ rows through shared memory
 // 16 bytes from global to shared memory, both aligned, behind the threads' backs; groups of copies
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -322,6 +243,240 @@ struct RowRing {
         }
     }
 };
+
+// Many aligned rows of more than 2048 columns: CTAs that stay, the columns' factors in their threads' registers, rows
+// STAGES - 1 ahead on their way into shared memory. One CTA a row (sandwich_kernel) waits for memory, two sums
+// and its factors one after the other.
+template <int FMT, int MAXC, int MAXT, int MIN_CTAS, int STAGES>
+__global__ void __launch_bounds__(MAXT, MIN_CTAS)
+    sandwich_ring_kernel(const __grid_constant__ SandwichArgs a, const bool vectors_aligned) {
+    using Ring = RowRing<false>;
+    constexpr uint32_t MATRIX = 16 * Ring::SLOTS * (MAXT / 32), STAGE = 2 * MAXC * MATRIX;
+    const NormArgs& n = a.n;
+    const int tid = threadIdx.x, lane = tid % 32, NT = blockDim.x, H = n.H, T = n.T, step = gridDim.x;
+    const int chunks = (H + 7) / 8;
+    __shared__ float s_red[NORM_MAX_WARPS], s_red2[NORM_MAX_WARPS], s_red3[NORM_MAX_WARPS];
+    extern __shared__ uint4 s_ring[];  // [stage][matrix][chunk of a thread][warp][SLOTS]
+    const uint32_t slot = smem_u32(s_ring) + 16 * Ring::SLOTS * (tid / 32) + 16 * lane;
+    grid_dep_wait();
+    grid_dep_launch();
+    auto issue = [&](int next, uint32_t stage_at) {  // the copies of row `next`
+        if (next < T) {
+            auto matrix = [&](int k, const __nv_bfloat16* p, int64_t ld) {
+                const uint8_t* row = reinterpret_cast<const uint8_t*>(p + next * ld);
+#pragma unroll
+                for (int i = 0; i < MAXC; ++i)
+                    Ring::issue(stage_at + (k * MAXC + i) * MATRIX, row, H, tid + i * NT, lane, false, 0, 0);
+            };
+            matrix(0, n.x, n.ldx);
+            matrix(1, n.res, n.ldr);
+        }
+        copies_end_group();
+    };
+    // slots past the row, which no copy ever writes, are zeros
+#pragma unroll
+    for (int k = 0; k < STAGES * 2 * MAXC; ++k) put_shared16(slot + k * MATRIX, make_uint4(0, 0, 0, 0));
+    int t = blockIdx.x;
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) issue(t + s * step, slot + s * STAGE);
+    f2 w[MAXC][4], pre[MAXC][4];
+#pragma unroll
+    for (int i = 0; i < MAXC; ++i) {
+        const int c = tid + i * NT;
+        float p[8], e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = e[j] = 0.0f;
+        if (c < chunks) {
+            load_gamma(p, a.post, c, H, vectors_aligned);
+            load_gamma(e, n.gamma, c, H, vectors_aligned);
+            if (a.gate_kind == MOE_GATE_CHANNEL) {
+                float g[8];
+                load_gamma(g, a.gate, c, H, vectors_aligned);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) p[j] *= g[j];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[i][k] = pair(p[2 * k], p[2 * k + 1]), pre[i][k] = pair(e[2 * k], e[2 * k + 1]);
+    }
+    const bool token = a.gate_kind == MOE_GATE_TOKEN;
+    float own = token && t < T ? a.gate[t] : 1.0f;  // the token's gate, fetched one row ahead
+    const f2 alpha = both(a.alpha);
+    uint32_t at = slot, ahead = slot + (STAGES - 1) * STAGE;
+    for (; t < T; t += step) {
+        issue(t + (STAGES - 1) * step, ahead);
+        const float gate = own;
+        if (token && t + step < T) own = a.gate[t + step];
+        copies_wait<STAGES - 1>();
+        auto word = [](const uint4& v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; };
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < MAXC; ++i) {
+            const uint4 v = shared16(at + i * MATRIX);
+            f2 sq = 0ull;  // by chunks: the rounding errors of many short sums average out
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const f2 f = bf16_pair(word(v, k));
+                sq = fma2(f, f, sq);
+            }
+            ss += half_sum(sq);
+        }
+        const Scale first(row_join<false>(ss, s_red), (float)H, n.inv_h, n.eps);
+        const f2 to_z = both(first.hi * gate);
+        f2 z[MAXC][4];
+        ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < MAXC; ++i) {
+            const uint4 f = shared16(at + i * MATRIX), r = shared16(at + (MAXC + i) * MATRIX);
+            f2 sq = 0ull;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                z[i][k] = fma2(mul2(to_z, bf16_pair(word(f, k))), w[i][k], mul2(alpha, bf16_pair(word(r, k))));
+                sq = fma2(z[i][k], z[i][k], sq);
+            }
+            ss += half_sum(sq);
+        }
+        auto store = [&](__nv_bfloat16* row) {
+#pragma unroll
+            for (int i = 0; i < MAXC; ++i)
+                Ring::store(reinterpret_cast<uint8_t*>(row),
+                            make_uint4(to_bf16(z[i][0]), to_bf16(z[i][1]), to_bf16(z[i][2]), to_bf16(z[i][3])), H,
+                            tid + i * NT, lane, true);
+        };
+        if (n.sum) store(n.sum + t * n.lds);
+        const Scale second(row_join<false>(ss, s_red2), (float)H, n.inv_h, n.eps);
+        if (a.stats && tid == 0) {
+            a.stats[2 * (int64_t)t] = first.hi;
+            a.stats[2 * (int64_t)t + 1] = second.hi;
+        }
+        if constexpr (FMT < 0) {
+            const f2 rz = both(second.hi);
+#pragma unroll
+            for (int i = 0; i < MAXC; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) z[i][k] = mul2(mul2(z[i][k], rz), pre[i][k]);
+            store(n.out + t * n.ldo);
+        } else {
+            float h[MAXC][8];
+#pragma unroll
+            for (int i = 0; i < MAXC; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float z0, z1, g0, g1;
+                    halves(z[i][k], z0, z1);
+                    halves(pre[i][k], g0, g1);
+                    h[i][2 * k] = second.apply(z0, g0);
+                    h[i][2 * k + 1] = second.apply(z1, g1);
+                    z[i][k] = pair(h[i][2 * k], h[i][2 * k + 1]);
+                }
+            if (n.out) store(n.out + t * n.ldo);
+            quantize_row<FMT, MAXC>(n, h, t, true, chunks, s_red3);
+        }
+        at = at == slot + (STAGES - 1) * STAGE ? slot : at + STAGE;
+        ahead = ahead == slot + (STAGES - 1) * STAGE ? slot : ahead + STAGE;
+    }
+}
+
+// SMs of the GPU this is built for: how many CTAs share the column sums is part of their order and of the
+// workspace's size, which a caller may ask for without a GPU.
+constexpr int SANDWICH_SMS = 152;
+
+constexpr int SANDWICH_CTA = 128;  // rows of fewer threads share a CTA of about this many
+
+template <int FMT, int MAXC, int MAXT, int MIN_CTAS, bool RAGGED>
+static cudaError_t sandwich_t(const SandwichArgs& a, cudaStream_t st) {
+    const int64_t chunks = ceil_div(a.n.H, 8), threads = align_up(ceil_div(chunks, MAXC), 32);
+    const int64_t rows = threads >= SANDWICH_CTA ? 1 : SANDWICH_CTA / threads;
+    LaunchAttrs at(true);
+    cudaLaunchConfig_t cfg =
+        at.config(dim3((unsigned)ceil_div(a.n.T, rows)), dim3((unsigned)threads, (unsigned)rows),
+                  RAGGED && (a.n.sum || a.n.out) ? (size_t)(rows * chunks * 16) : 0, st);
+    const uintptr_t v = (uintptr_t)a.post | (uintptr_t)a.n.gamma |
+                        (a.gate_kind == MOE_GATE_CHANNEL ? (uintptr_t)a.gate : 0);
+    return cudaLaunchKernelEx(&cfg, sandwich_kernel<FMT, MAXC, MAXT, MIN_CTAS, RAGGED>, a, v % 16 == 0);
+}
+
+template <int FMT, int MAXC, int MAXT, int MIN_CTAS, int STAGES>
+static cudaError_t sandwich_ring(const SandwichArgs& a, cudaStream_t st) {
+    const auto kernel = sandwich_ring_kernel<FMT, MAXC, MAXT, MIN_CTAS, STAGES>;
+    constexpr size_t SMEM = (size_t)STAGES * 2 * MAXC * MAXT * 16;
+    static_assert(MIN_CTAS * (SMEM + 2048) <= 233472, "shared memory budget");
+    if (SMEM > 40 * 1024) {  // 48 KB with the static arrays need no leave
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t threads = align_up(ceil_div(ceil_div(a.n.H, 8), MAXC), 32), most = (int64_t)SANDWICH_SMS * MIN_CTAS;
+    LaunchAttrs at(true);
+    cudaLaunchConfig_t cfg = at.config(dim3((unsigned)(a.n.T < most ? a.n.T : most)), dim3((unsigned)threads), SMEM, st);
+    const uintptr_t v = (uintptr_t)a.post | (uintptr_t)a.n.gamma |
+                        (a.gate_kind == MOE_GATE_CHANNEL ? (uintptr_t)a.gate : 0);
+    return cudaLaunchKernelEx(&cfg, kernel, a, v % 16 == 0);
+}
+
+template <int FMT, bool RAGGED>
+static cudaError_t sandwich_f(const SandwichArgs& a, cudaStream_t st) {
+    if (a.n.T <= 152 && a.n.H <= 8192) return sandwich_t<FMT, 1, 1024, 1, RAGGED>(a, st);
+    if constexpr (RAGGED) {
+        return a.n.H <= 4096 ? sandwich_t<FMT, 2, 256, 4, true>(a, st) : sandwich_t<FMT, 2, 1024, 1, true>(a, st);
+    } else {
+        if (a.n.H <= 2048) return sandwich_t<FMT, 2, 256, 5, false>(a, st);
+        // 8192 x 4096 42.8 us (three CTAs 44.1, four chunks a thread 46.8, one CTA a row 46.2); 8192 x 7168 82.6 us,
+        // MXFP8 78.9 (two chunks a thread 84.4 and 82.7, three CTAs 87.0 and 103, one CTA a row 90.9 and 81.5)
+        if (a.n.H <= 4096) return sandwich_ring<FMT, 2, 256, 4, 2>(a, st);
+        if (a.n.H <= 7168) return sandwich_ring<FMT, 4, 224, 2, 3>(a, st);
+        if (a.n.H <= 8192) return sandwich_ring<FMT, 4, 256, 2, 3>(a, st);
+        return sandwich_t<FMT, 4, 512, 2, false>(a, st);
+    }
+}
+
+cudaError_t launch_sandwich(const SandwichArgs& args, cudaStream_t st) {
+    SandwichArgs a = args;
+    NormArgs& n = a.n;
+    n.inv_h = 1.0f / (float)n.H;
+    // whether the sizes, strides and addresses give every row whole, aligned 16-byte pieces
+    uintptr_t bits = (uintptr_t)n.x | (uintptr_t)(2 * n.ldx) | (uintptr_t)(2 * n.H) | (uintptr_t)n.res |
+                     (uintptr_t)(2 * n.ldr);
+    if (n.sum) bits |= (uintptr_t)n.sum | (uintptr_t)(2 * n.lds);
+    if (n.out) bits |= (uintptr_t)n.out | (uintptr_t)(2 * n.ldo);
+    const bool ragged = bits % 16 != 0;
+    switch (n.fmt) {
+        case MOE_FMT_MXFP8:
+            return ragged ? sandwich_f<MOE_FMT_MXFP8, true>(a, st) : sandwich_f<MOE_FMT_MXFP8, false>(a, st);
+        case MOE_FMT_NVFP4:
+            return ragged ? sandwich_f<MOE_FMT_NVFP4, true>(a, st) : sandwich_f<MOE_FMT_NVFP4, false>(a, st);
+        case MOE_FMT_MXFP4:
+            return ragged ? sandwich_f<MOE_FMT_MXFP4, true>(a, st) : sandwich_f<MOE_FMT_MXFP4, false>(a, st);
+        default: return ragged ? sandwich_f<-1, true>(a, st) : sandwich_f<-1, false>(a, st);
+    }
+}
+
+// ------------------------------------------------------------------ gradient
+// The sums of three values over a row's threads, in every thread. mine, all: this warp's and the row's first
+// place in shared memory, 16 bytes for each warp.
+__device__ __forceinline__ float3 three_sums(float x, float y, float z, uint32_t mine, uint32_t all, int warps, int lane) {
+    const bool up = lane & 16, odd = lane & 8;
+    auto add_up = [&](float x, float y, float z) {  // lanes 0.., 8.., 16.. end with the sums of x, z, y
+        float a = (up ? y : x) + __shfl_xor_sync(0xffffffffu, up ? x : y, 16);
+        const float b = z + __shfl_xor_sync(0xffffffffu, z, 16);
+        a = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        return a;
+    };
+    float a = add_up(x, y, z);
+    if (warps > 1) {
+        if (lane % 8 == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + lane / 2), "f"(a) : "memory");
+        __syncthreads();
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // x, z, y, (z)
+        if (lane < warps)
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                         : "r"(all + 16 * lane)
+                         : "memory");
+        a = add_up(v.x, v.z, v.y);
+    }
+    return make_float3(__shfl_sync(0xffffffffu, a, 0), __shfl_sync(0xffffffffu, a, 16), __shfl_sync(0xffffffffu, a, 8));
+}
 
 // One row of a CTA's row group at a time, STAGES - 1 rows ahead on their way into shared memory: a thread
 // copies what it reads itself (RAGGED: its warp does), so that no barrier belongs to that. Chunks are
