@@ -709,27 +709,36 @@ __global__ void __launch_bounds__(MAXT, MIN_CTAS)
 }
 
 constexpr int COLUMN_THREADS = 1024;
-// The column sums: CTA c the columns 32 c .. 32 c + 31, one in each lane; warp w adds the parts w, w + 32, ...,
-// then the warps in order.
+// The column sums: CTA c the columns from c COLUMNS on; thread (s, h) adds every SLICES-th part of one from the
+// s-th on, lanes of the same column join, then the warps in order. 16 columns where 32 would leave too few CTAs
+// (500 x 2050 15.0 us, 15.8 with 32), 32 where 16 would make too many (8192 x 7168 117 us, 119 with 16).
+template <int COLUMNS>
 __global__ void __launch_bounds__(COLUMN_THREADS) sandwich_columns_kernel(const SandwichGradArgs a, int parts) {
-    constexpr int WARPS = COLUMN_THREADS / 32;
-    __shared__ float s_p[WARPS][32], s_c[WARPS][32];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, h = 32 * (int)blockIdx.x + lane;
+    constexpr int SLICES = COLUMN_THREADS / COLUMNS, WARPS = COLUMN_THREADS / 32;
+    __shared__ float s_p[WARPS][COLUMNS], s_c[WARPS][COLUMNS];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int h = COLUMNS * (int)blockIdx.x + lane % COLUMNS, slice = threadIdx.x / COLUMNS;
     const int64_t ld = (int64_t)((a.H + 7) / 8) * 8;
     grid_dep_wait();
     grid_dep_launch();
     float p = 0.0f, c = 0.0f;
     if (h < a.H) {
-#pragma unroll 5
-        for (int i = warp; i < parts; i += WARPS) {
+#pragma unroll 4
+        for (int i = slice; i < parts; i += SLICES) {
             p += __ldcg(a.part + i * ld + h);
             c += __ldcg(a.part + (parts + i) * ld + h);
         }
     }
-    s_p[warp][lane] = p;
-    s_c[warp][lane] = c;
+    if constexpr (COLUMNS < 32) {
+        p += __shfl_xor_sync(0xffffffffu, p, COLUMNS);
+        c += __shfl_xor_sync(0xffffffffu, c, COLUMNS);
+    }
+    if (lane < COLUMNS) {
+        s_p[warp][lane] = p;
+        s_c[warp][lane] = c;
+    }
     __syncthreads();
-    if (warp != 0 || h >= a.H) return;
+    if (threadIdx.x >= COLUMNS || h >= a.H) return;
     p = c = 0.0f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) p += s_p[w][lane], c += s_c[w][lane];
@@ -804,8 +813,10 @@ cudaError_t launch_sandwich_grad(const SandwichGradArgs& args, cudaStream_t st) 
     const cudaError_t e = bits % 16 ? grad_r<true>(a, s, st) : grad_r<false>(a, s, st);
     if (e != cudaSuccess || !a.part) return e;
     LaunchAttrs at(true);
-    cudaLaunchConfig_t cfg = at.config(dim3((unsigned)ceil_div(a.H, 32)), dim3(COLUMN_THREADS), 0, st);
-    return cudaLaunchKernelEx(&cfg, sandwich_columns_kernel, a, s.grid);
+    const int columns = a.H <= 4096 ? 16 : 32;
+    cudaLaunchConfig_t cfg = at.config(dim3((unsigned)ceil_div(a.H, columns)), dim3(COLUMN_THREADS), 0, st);
+    return columns == 16 ? cudaLaunchKernelEx(&cfg, sandwich_columns_kernel<16>, a, s.grid)
+                         : cudaLaunchKernelEx(&cfg, sandwich_columns_kernel<32>, a, s.grid);
 }
 
 }  // namespace moe
