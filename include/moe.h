@@ -626,6 +626,59 @@ int moe_linear_forward_quantized(moe_linear_plan_t plan, int32_t num_tokens, con
 /* As moe_last_status, for a workspace of the two forwards above. */
 int moe_linear_last_status(moe_linear_plan_t plan, void* workspace, void* stream, int32_t* status);
 
+/*
+ * Product with 4-bit integer weights: out[t, n] = bf16(sum_k x[t, k] (q[n, k] - z[n, k / g]) s[n, k / g]) with bf16
+ * activations as they are, a scale and optionally a zero point for each group of g neighbouring k. out_features
+ * 1 .. 2^20, in_features a multiple of 32 up to 32768 (the last group may be shorter), max_tokens >= 1.
+ */
+#define MOE_SCALE_BF16 0
+#define MOE_SCALE_F16  1
+typedef struct moe_int4_config {
+    int32_t out_features;    /* N */
+    int32_t in_features;     /* K */
+    int32_t max_tokens;
+    int32_t group_size;      /* 32, 64 or 128 */
+    int32_t zero_points;     /* 0 (z = 8) or 1 */
+    int32_t scale_type;      /* MOE_SCALE_* */
+} moe_int4_config_t;
+
+typedef struct moe_int4_plan_s* moe_int4_plan_t;
+
+int moe_int4_config_validate(const moe_int4_config_t* cfg);
+int moe_int4_plan(const moe_int4_config_t* cfg, moe_int4_plan_t* out);
+int moe_int4_plan_destroy(moe_int4_plan_t plan);
+/* Limit of each bounded wait inside the product's kernels (0: the default, 2 s). */
+int moe_int4_set_wait_timeout(moe_int4_plan_t plan, uint64_t timeout_ns);
+
+/*
+ * A weight. Checkpoint layout (src): codes u8 [N, K/2], element 2i in the low nibble; scales [N, ceil(K/g)] of
+ * scale_type; zeros u8 [N, ceil(K/g)], one zero point 0 .. 15 in a byte (NULL without zero points). Kernel layout
+ * (dst): other orders of them, each 256-byte aligned, of moe_int4_weight_size bytes; src and dst do not overlap.
+ */
+typedef struct moe_int4_weight {
+    void* codes;
+    void* scales;
+    void* zeros;
+} moe_int4_weight_t;
+/* Bytes of each tensor of the kernel layout (zeros: 0 without zero points). Host-only. */
+int moe_int4_weight_size(moe_int4_plan_t plan, size_t* codes, size_t* scales, size_t* zeros);
+int moe_int4_transform_weight(moe_int4_plan_t plan, const moe_int4_weight_t* src, moe_int4_weight_t* dst, void* stream);
+
+/* Bytes of the workspace of moe_int4_forward for num_tokens tokens. */
+int moe_int4_workspace_size(moe_int4_plan_t plan, int32_t num_tokens, size_t* bytes);
+
+/*
+ * x bf16 [T, K], row stride x_stride; out bf16 [T, N], row stride out_stride; out overlaps neither x, the weight nor
+ * the workspace. Sums are fp32: q - z and x are multiplied exactly and each group's sum is
+ * scaled. Deterministic; a row may round otherwise in a batch of
+ * another size. T == 0 launches nothing. The workspace's contents do not matter.
+ */
+int moe_int4_forward(moe_int4_plan_t plan, int32_t num_tokens, const void* x, int64_t x_stride,
+                     const moe_int4_weight_t* weight, void* out, int64_t out_stride, void* workspace,
+                     size_t workspace_bytes, void* stream);
+/* As moe_linear_last_status, for a workspace of moe_int4_forward. */
+int moe_int4_last_status(moe_int4_plan_t plan, void* workspace, void* stream, int32_t* status);
+
 /* Static string for a status code. */
 const char* moe_error_string(int32_t status);
 

@@ -7,3 +7,4 @@ from .moe import (FORMATS, LayerConfig, MoeError, Plan, config_workspace_size, e
 from .score_router import ScoreRouter, ScoreRouterConfig  # noqa: F401
 from .sandwich import (SandwichGrads, sandwich_norm, sandwich_norm_backward,  # noqa: F401
                        sandwich_norm_workspace_size)
+from .int4 import Int4LinearConfig, Int4LinearPlan, Int4LinearWeight, int4_validate  # noqa: F401

@@ -167,4 +167,40 @@ struct LinearMaps {
 cudaError_t launch_linear(int fmt, const LinearMaps& m, const LinearArgs& p, const LinearShape& s, int num_sms,
                           cudaStream_t st);
 
+// ------------------------------------------------------------------ 4-bit integer weights
+// units of 64 k, 16-feature tiles (whole 128-feature blocks), groups with a place of their own (whole units)
+__host__ __device__ constexpr int int4_units(int K) { return (K + 63) / 64; }
+__host__ __device__ constexpr int64_t int4_tiles(int64_t N) { return (N + 127) / 128 * 8; }
+__host__ __device__ constexpr int int4_slots(int K, int group) {
+    return group == 32 ? 2 * int4_units(K) : group == 64 ? int4_units(K) : (int4_units(K) + 1) / 2;
+}
+struct Int4Layout {
+    const uint8_t* src_codes;    // [N][K / 2]
+    const uint16_t* src_scales;  // [N][groups]
+    const uint8_t* src_zeros;    // [N][groups] or null
+    uint32_t* codes;             // [tiles][units][32 lanes][4]
+    uint32_t* scales;            // [tiles][slots][8]
+    uint8_t* zeros;              // [tiles][slots][8] or null
+    int N, K, group;
+};
+struct Int4Args {
+    const __nv_bfloat16* x;      // rows at 16-byte boundaries
+    int64_t ldx;
+    const uint4* codes;
+    const uint32_t* scales;
+    const uint8_t* zeros;        // or null: the zero point is 8
+    int half;                    // scales are fp16 (else bf16)
+    int group, M, N, K;
+    int slots, unit_shift;       // set by launch_int4
+    __nv_bfloat16* out;
+    int64_t ldo;
+    int* status;                 // number of CTAs that report, then a word of each
+    unsigned long long timeout_ns;
+};
+cudaError_t launch_int4_layout(const Int4Layout& a, cudaStream_t st);
+cudaError_t launch_int4_rows(const void* x, int64_t ldx, void* dst, int M, int K, cudaStream_t st);
+cudaError_t launch_int4(const Int4Args& a, int num_sms, cudaStream_t st);
+int int4_max_ctas(int N, int num_sms);
+cudaError_t int4_prepare();
+
 }  // namespace moe

@@ -15,6 +15,7 @@ using namespace moe;
 namespace {
 
 constexpr int MAX_ROW = 16384;          // widest row of the norm, the quantiser and the product's K
+constexpr int MAX_INT4_ROW = 32768;     // K of the product with 4-bit integer weights
 constexpr int MAX_EXPERTS = 512;
 constexpr int MAX_TOP_K = 32;
 constexpr int MAX_OUT = 1 << 20;
@@ -86,6 +87,12 @@ bool map_atoms(CUtensorMap* m, const void* base, uint64_t atoms, uint32_t box_at
 }
 
 }  // namespace
+
+struct moe_int4_plan_s {
+    moe_int4_config_t cfg;
+    int num_sms;
+    unsigned long long timeout_ns;
+};
 
 struct moe_linear_plan_s {
     moe_linear_config_t cfg;
@@ -215,6 +222,43 @@ int check_forward(moe_linear_plan_t plan, int T, const moe_linear_weight_t* w, c
         return MOE_ERR_INVALID_ARG;
     if (!rows_ok(out, out_stride, T, c.out_features)) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < (size_t)lin_layout(plan, T).total) return MOE_ERR_WORKSPACE;
+    return MOE_OK;
+}
+
+int check_int4(const moe_int4_config_t* c) {
+    if (!c) return MOE_ERR_INVALID_ARG;
+    if (c->out_features < 1 || c->out_features > MAX_OUT) return MOE_ERR_INVALID_ARG;
+    if (c->in_features < 32 || c->in_features % 32 || c->in_features > MAX_INT4_ROW) return MOE_ERR_INVALID_ARG;
+    if (c->max_tokens < 1 || c->max_tokens > (1 << 28)) return MOE_ERR_INVALID_ARG;
+    if (c->group_size != 32 && c->group_size != 64 && c->group_size != 128) return MOE_ERR_UNSUPPORTED;
+    if (c->zero_points != 0 && c->zero_points != 1) return MOE_ERR_INVALID_ARG;
+    if (c->scale_type != MOE_SCALE_BF16 && c->scale_type != MOE_SCALE_F16) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// workspace of the product with 4-bit weights: its status words, then rows of x that are copied
+int64_t int4_status_bytes(const moe_int4_plan_s* plan) {
+    return align_up(4 * (1 + (int64_t)int4_max_ctas(plan->cfg.out_features, plan->num_sms)), REGION_ALIGN);
+}
+
+// The status words of a product, most of them at most: waits for the stream, and clears them.
+int read_status(void* workspace, int most, cudaStream_t st, int32_t* status) {
+    // words[0]: how many CTAs the last product had (bounded: before the first one it may be anything)
+    const int* words = (const int*)workspace;
+    int ctas = 0, v = MOE_OK;
+    CUDA_TRY(cudaMemcpyAsync(&ctas, words, sizeof(int), cudaMemcpyDeviceToHost, st));
+    CUDA_TRY(cudaStreamSynchronize(st));
+    ctas = ctas < 0 || ctas > most ? most : ctas;
+    int part[512];
+    for (int i = 0; i < ctas && v == MOE_OK; i += 512) {
+        const int n = ctas - i < 512 ? ctas - i : 512;
+        CUDA_TRY(cudaMemcpyAsync(part, words + 1 + i, n * sizeof(int), cudaMemcpyDeviceToHost, st));
+        CUDA_TRY(cudaStreamSynchronize(st));
+        for (int j = 0; j < n && v == MOE_OK; ++j) v = part[j];
+    }
+    CUDA_TRY(cudaMemsetAsync(workspace, 0, sizeof(int), st));
+    CUDA_TRY(cudaStreamSynchronize(st));
+    *status = v;
     return MOE_OK;
 }
 
@@ -729,25 +773,128 @@ int moe_linear_forward_quantized(moe_linear_plan_t plan, int32_t num_tokens, con
 
 int moe_linear_last_status(moe_linear_plan_t plan, void* workspace, void* stream, int32_t* status) {
     if (!plan || !workspace || !status) return MOE_ERR_INVALID_ARG;
-    cudaStream_t st = (cudaStream_t)stream;
-    // words[0]: how many CTAs the last product had (bounded: before the first one it may be anything)
-    const int most = linear_max_ctas(plan->cfg.out_features, plan->num_sms);
-    const int* words = (const int*)workspace;
-    int ctas = 0, v = MOE_OK;
-    CUDA_TRY(cudaMemcpyAsync(&ctas, words, sizeof(int), cudaMemcpyDeviceToHost, st));
-    CUDA_TRY(cudaStreamSynchronize(st));
-    ctas = ctas < 0 || ctas > most ? most : ctas;
-    int part[512];
-    for (int i = 0; i < ctas && v == MOE_OK; i += 512) {
-        const int n = ctas - i < 512 ? ctas - i : 512;
-        CUDA_TRY(cudaMemcpyAsync(part, words + 1 + i, n * sizeof(int), cudaMemcpyDeviceToHost, st));
-        CUDA_TRY(cudaStreamSynchronize(st));
-        for (int j = 0; j < n && v == MOE_OK; ++j) v = part[j];
-    }
-    CUDA_TRY(cudaMemsetAsync(workspace, 0, sizeof(int), st));
-    CUDA_TRY(cudaStreamSynchronize(st));
-    *status = v;
+    return read_status(workspace, linear_max_ctas(plan->cfg.out_features, plan->num_sms), (cudaStream_t)stream, status);
+}
+
+// ------------------------------------------------------------------ 4-bit integer weights
+int moe_int4_config_validate(const moe_int4_config_t* cfg) { return check_int4(cfg); }
+
+int moe_int4_plan(const moe_int4_config_t* cfg, moe_int4_plan_t* out) {
+    if (!out) return MOE_ERR_INVALID_ARG;
+    *out = nullptr;
+    const int v = check_int4(cfg);
+    if (v != MOE_OK) return v;
+    int dev = 0, major = 0, sms = 0;
+    CUDA_TRY(cudaGetDevice(&dev));
+    CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
+    CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    if (major != 10) return MOE_ERR_UNSUPPORTED;
+    if (!get_encode()) return MOE_ERR_CUDA;
+    CUDA_TRY(int4_prepare());
+    moe_int4_plan_s* p = new (std::nothrow) moe_int4_plan_s{*cfg, sms, DEFAULT_TIMEOUT_NS};
+    if (!p) return MOE_ERR_CUDA;
+    *out = p;
     return MOE_OK;
+}
+
+int moe_int4_plan_destroy(moe_int4_plan_t plan) {
+    delete plan;
+    return MOE_OK;
+}
+
+int moe_int4_set_wait_timeout(moe_int4_plan_t plan, uint64_t timeout_ns) {
+    if (!plan) return MOE_ERR_INVALID_ARG;
+    plan->timeout_ns = timeout_ns ? timeout_ns : DEFAULT_TIMEOUT_NS;
+    return MOE_OK;
+}
+
+int moe_int4_weight_size(moe_int4_plan_t plan, size_t* codes, size_t* scales, size_t* zeros) {
+    if (!plan || !codes || !scales || !zeros) return MOE_ERR_INVALID_ARG;
+    const moe_int4_config_t& c = plan->cfg;
+    const int64_t tiles = int4_tiles(c.out_features), slots = int4_slots(c.in_features, c.group_size);
+    *codes = (size_t)(tiles * int4_units(c.in_features) * 512);
+    *scales = (size_t)(tiles * slots * 32);
+    *zeros = c.zero_points ? (size_t)(tiles * slots * 8) : 0;
+    return MOE_OK;
+}
+
+int moe_int4_transform_weight(moe_int4_plan_t plan, const moe_int4_weight_t* src, moe_int4_weight_t* dst, void* stream) {
+    if (!plan || !src || !dst || !src->codes || !src->scales || !dst->codes || !dst->scales) return MOE_ERR_INVALID_ARG;
+    const moe_int4_config_t& c = plan->cfg;
+    if ((c.zero_points != 0) != (src->zeros != nullptr) || (c.zero_points != 0) != (dst->zeros != nullptr))
+        return MOE_ERR_INVALID_ARG;
+    if (src->codes == dst->codes || src->scales == dst->scales || (src->zeros && src->zeros == dst->zeros) ||
+        !aligned_to(src->scales, 2) || !aligned_to(dst->codes, 256) || !aligned_to(dst->scales, 256) ||
+        !aligned_to(dst->zeros, 256))
+        return MOE_ERR_INVALID_ARG;
+    Int4Layout a{};
+    a.src_codes = (const uint8_t*)src->codes;
+    a.src_scales = (const uint16_t*)src->scales;
+    a.src_zeros = (const uint8_t*)src->zeros;
+    a.codes = (uint32_t*)dst->codes;
+    a.scales = (uint32_t*)dst->scales;
+    a.zeros = (uint8_t*)dst->zeros;
+    a.N = c.out_features;
+    a.K = c.in_features;
+    a.group = c.group_size;
+    CUDA_TRY(launch_int4_layout(a, (cudaStream_t)stream));
+    return MOE_OK;
+}
+
+int moe_int4_workspace_size(moe_int4_plan_t plan, int32_t num_tokens, size_t* bytes) {
+    if (!plan || !bytes || num_tokens < 0) return MOE_ERR_INVALID_ARG;
+    if (num_tokens > plan->cfg.max_tokens) return MOE_ERR_CAPACITY;
+    *bytes = (size_t)(int4_status_bytes(plan) + align_up(2 * (int64_t)num_tokens * plan->cfg.in_features, REGION_ALIGN));
+    return MOE_OK;
+}
+
+int moe_int4_forward(moe_int4_plan_t plan, int32_t num_tokens, const void* x, int64_t x_stride,
+                     const moe_int4_weight_t* w, void* out, int64_t out_stride, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    if (!plan || num_tokens < 0) return MOE_ERR_INVALID_ARG;
+    const moe_int4_config_t& c = plan->cfg;
+    const int T = num_tokens;
+    if (T > c.max_tokens) return MOE_ERR_CAPACITY;
+    if (T == 0) return MOE_OK;
+    if (!w || !w->codes || !w->scales || !x || !out || !workspace || x == out) return MOE_ERR_INVALID_ARG;
+    if ((c.zero_points != 0) != (w->zeros != nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(w->codes, 256) || !aligned_to(w->scales, 256) || !aligned_to(w->zeros, 256) ||
+        !aligned_to(workspace, 256))
+        return MOE_ERR_INVALID_ARG;
+    if (!rows_ok(x, x_stride, T, c.in_features) || !rows_ok(out, out_stride, T, c.out_features))
+        return MOE_ERR_INVALID_ARG;
+    size_t need = 0;
+    moe_int4_workspace_size(plan, T, &need);
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    cudaStream_t st = (cudaStream_t)stream;
+    Int4Args a{};
+    a.x = (const __nv_bfloat16*)x;
+    a.ldx = T > 1 ? x_stride : c.in_features;
+    if (!aligned_to(x, 16) || a.ldx % 8) {
+        void* rows = (uint8_t*)workspace + int4_status_bytes(plan);
+        CUDA_TRY(launch_int4_rows(x, a.ldx, rows, T, c.in_features, st));
+        a.x = (const __nv_bfloat16*)rows;
+        a.ldx = c.in_features;
+    }
+    a.codes = (const uint4*)w->codes;
+    a.scales = (const uint32_t*)w->scales;
+    a.zeros = (const uint8_t*)w->zeros;
+    a.half = c.scale_type == MOE_SCALE_F16;
+    a.group = c.group_size;
+    a.M = T;
+    a.N = c.out_features;
+    a.K = c.in_features;
+    a.out = (__nv_bfloat16*)out;
+    a.ldo = out_stride;
+    a.status = (int*)workspace;
+    a.timeout_ns = plan->timeout_ns;
+    CUDA_TRY(launch_int4(a, plan->num_sms, st));
+    return MOE_OK;
+}
+
+int moe_int4_last_status(moe_int4_plan_t plan, void* workspace, void* stream, int32_t* status) {
+    if (!plan || !workspace || !status) return MOE_ERR_INVALID_ARG;
+    return read_status(workspace, int4_max_ctas(plan->cfg.out_features, plan->num_sms), (cudaStream_t)stream, status);
 }
 
 }  // extern "C"

@@ -33,52 +33,18 @@
 #include "block.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "pipeline.cuh"
 #include "quant.cuh"
 
 namespace moe {
 
 // ------------------------------------------------------------------ shared pieces
-// The bounded waits. Short limits are counted in polls of some 16 ns each, so that a limit of a
-// nanosecond is one poll.
-__device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, const volatile int* abort) {
-    if (timeout_ns >= SHORT_WAIT_NS) return mbar_wait(bar, parity, timeout_ns, abort);
-    for (uint64_t i = 0; i <= timeout_ns / 16; ++i)
-        if (mbar_test_wait(bar, parity)) return true;
-    return false;
-}
-__device__ __forceinline__ bool lin_wait_cl(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
-                                            const volatile int* abort) {
-    if (timeout_ns >= SHORT_WAIT_NS) return mbar_wait_cl(bar, parity, timeout_ns, abort);
-    for (uint64_t i = 0; i <= timeout_ns / 16; ++i)
-        if (mbar_test_wait_cl(bar, parity)) return true;
-    return false;
-}
-
-// One lane of the warp, always the same. The producer and MMA warps run their loops with all
-// lanes and predicate only the copies and MMAs with this: the loop's addresses and descriptors
-// then stay in uniform registers. (A loop that one thread runs alone moves every operand there
-// for each instruction: measured, 4 MMAs and 12 scale copies took 1085 cycles to issue that way
-// and 408 this way, against 512 that the MMAs need.)
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
 // One thread of each CTA, after every warp's last wait: status[0] is the number of CTAs, the words
 // after it are theirs.
 __device__ __forceinline__ void write_status(const LinearArgs& p, uint32_t cta, uint32_t ctas, bool gave_up) {
     if (cta == 0) p.status[0] = (int)ctas;
     p.status[1 + cta] = gave_up ? MOE_ERR_TIMEOUT : MOE_OK;
 }
-// a wait of the whole warp: every lane returns the same
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, const volatile int* abort) {
-    return __all_sync(0xffffffffu, lin_wait(bar, parity, timeout_ns, abort));
-}
-__device__ __forceinline__ bool warp_wait_cl(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
-                                             const volatile int* abort) {
-    return __all_sync(0xffffffffu, lin_wait_cl(bar, parity, timeout_ns, abort));
-}
-
 // What an NVFP4 token's sums are multiplied by, one factor after the other: its scale times the weight's
 // and 1. Where that product leaves the normal range though an output need not (rows or weights around
 // 2^-100), the significands' product with an exponent that keeps every sum (2^-20 .. 2^40, or zero) in
@@ -91,20 +57,6 @@ __device__ __forceinline__ float2 token_scale(float xs, float ws) {
     const float m = frexpf(xs, &ex) * frexpf(ws, &ew);
     const int e = ex + ew, first = min(max(e, -100), 80);
     return make_float2(ldexpf(m, first), ldexpf(1.0f, min(e - first, 127)));
-}
-
-// Shared-memory descriptors differ only in their low word: the address / 16 (and, for operand rows,
-// a leading offset of 1 in bits 16 ..). The high words are those of kmajor_sw128_desc and
-// sf_atom_desc.
-__device__ __forceinline__ uint64_t row_desc(uint32_t addr16) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(addr16 | 0x10000u), "n"(0x40004040));
-    return d;
-}
-__device__ __forceinline__ uint64_t atom_desc(uint32_t addr16) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(addr16), "n"(0x4008));
-    return d;
 }
 
 // The 4 K steps of a stage: rows at a and b (addresses / 16), N columns, scale factors in tensor

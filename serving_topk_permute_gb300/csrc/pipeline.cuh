@@ -1,0 +1,58 @@
+// pipeline.cuh -- what the products' pipelines share: bounded waits of a thread or a warp, the elected lane,
+// shared-memory descriptors.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// The bounded waits. Short limits are counted in polls of some 16 ns each, so that a limit of a
+// nanosecond is one poll.
+__device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, const volatile int* abort) {
+    if (timeout_ns >= SHORT_WAIT_NS) return mbar_wait(bar, parity, timeout_ns, abort);
+    for (uint64_t i = 0; i <= timeout_ns / 16; ++i)
+        if (mbar_test_wait(bar, parity)) return true;
+    return false;
+}
+__device__ __forceinline__ bool lin_wait_cl(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                            const volatile int* abort) {
+    if (timeout_ns >= SHORT_WAIT_NS) return mbar_wait_cl(bar, parity, timeout_ns, abort);
+    for (uint64_t i = 0; i <= timeout_ns / 16; ++i)
+        if (mbar_test_wait_cl(bar, parity)) return true;
+    return false;
+}
+
+// One lane of the warp, always the same. The producer and MMA warps run their loops with all
+// lanes and predicate only the copies and MMAs with this: the loop's addresses and descriptors
+// then stay in uniform registers. (A loop that one thread runs alone moves every operand there
+// for each instruction: measured, 4 MMAs and 12 scale copies took 1085 cycles to issue that way
+// and 408 this way, against 512 that the MMAs need.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// a wait of the whole warp: every lane returns the same
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, const volatile int* abort) {
+    return __all_sync(0xffffffffu, lin_wait(bar, parity, timeout_ns, abort));
+}
+__device__ __forceinline__ bool warp_wait_cl(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                             const volatile int* abort) {
+    return __all_sync(0xffffffffu, lin_wait_cl(bar, parity, timeout_ns, abort));
+}
+
+// Shared-memory descriptors differ only in their low word: the address / 16 (and, for operand rows,
+// a leading offset of 1 in bits 16 ..). The high words are those of kmajor_sw128_desc and
+// sf_atom_desc.
+__device__ __forceinline__ uint64_t row_desc(uint32_t addr16) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(addr16 | 0x10000u), "n"(0x40004040));
+    return d;
+}
+__device__ __forceinline__ uint64_t atom_desc(uint32_t addr16) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(addr16), "n"(0x4008));
+    return d;
+}
+
+}  // namespace moe

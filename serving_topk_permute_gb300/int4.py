@@ -1,0 +1,201 @@
+"""Binding of the product with 4-bit integer weights (include/moe.h): bf16 activations, a scale and
+optionally a zero point for each group of K. Argument checks and marshalling only, as in block.py.
+"""
+from __future__ import annotations
+
+import ctypes
+from ctypes import byref
+from dataclasses import dataclass
+
+import torch
+
+from . import block
+from .block import (I32, I64, P, SZ, _at_device, _current_device, _device_of, _fail, _flat, _matrix, _on, _places,
+                    _row_stride, _set_once, _stream)
+from .moe import MOE_OK
+
+SCALE_TYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+_BF16, _U8 = torch.bfloat16, torch.uint8
+
+
+class Int4ConfigC(ctypes.Structure):
+    _fields_ = [("out_features", I32), ("in_features", I32), ("max_tokens", I32), ("group_size", I32),
+                ("zero_points", I32), ("scale_type", I32)]
+
+
+class Int4WeightC(ctypes.Structure):
+    _fields_ = [("codes", P), ("scales", P), ("zeros", P)]
+
+
+_lib = block.declare({
+    "moe_int4_config_validate": [P],
+    "moe_int4_plan": [P, P],
+    "moe_int4_plan_destroy": [P],
+    "moe_int4_set_wait_timeout": [P, ctypes.c_uint64],
+    "moe_int4_weight_size": [P, P, P, P],
+    "moe_int4_transform_weight": [P, P, P, P],
+    "moe_int4_workspace_size": [P, I32, P],
+    "moe_int4_forward": [P, I32, P, I64, P, P, I64, P, SZ, P],
+    "moe_int4_last_status": [P, P, P, P],
+})
+
+
+@dataclass(frozen=True)
+class Int4LinearConfig:
+    """What an Int4LinearPlan is built for. It cannot be changed. group_size: 32, 64 or 128; zero_points: the
+    weight has one for each group (else codes stand for code - 8); scale_dtype: bfloat16 or float16."""
+    out_features: int
+    in_features: int
+    max_tokens: int
+    group_size: int = 128
+    zero_points: bool = False
+    scale_dtype: torch.dtype = torch.bfloat16
+
+    def to_c(self) -> Int4ConfigC:
+        if self.scale_dtype not in SCALE_TYPES:
+            raise ValueError(f"scale_dtype must be bfloat16 or float16, got {self.scale_dtype}")
+        return Int4ConfigC(self.out_features, self.in_features, self.max_tokens, self.group_size,
+                           1 if self.zero_points else 0, SCALE_TYPES[self.scale_dtype])
+
+
+def int4_validate(cfg: Int4LinearConfig) -> int:
+    return _lib().moe_int4_config_validate(byref(cfg.to_c()))
+
+
+class Int4LinearWeight:
+    """A weight in the kernel layout (Int4LinearPlan.transform_weight). Its tensors can be neither replaced nor
+    resized."""
+
+    __setattr__ = _set_once
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None, what: tuple):
+        there = [t for t in (codes, scales, zeros) if t is not None]
+        self._dev = _device_of("codes", codes)
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self._what = what  # of the plan that laid it out
+        self._ask, self._at = _places(there)
+        self._c = Int4WeightC(codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr())
+        self._ref = byref(self._c)
+
+    def _arg(self, dev: int, what: tuple):
+        """The library's argument."""
+        if self._what != what:
+            raise ValueError(f"the weight was laid out for (N, K, group, zero points, scale type) {self._what}, "
+                             f"this plan takes {what}")
+        if self._dev != dev:
+            raise ValueError(f"the weight is on cuda:{self._dev}, the plan is for cuda:{dev}")
+        if [f() for f in self._ask] != self._at:
+            raise ValueError("a tensor of the Int4LinearWeight was resized or given other memory: make a new one")
+        return self._ref
+
+
+class Int4LinearPlan:
+    """out[t, n] = sum_k x[t, k] (q[n, k] - z[n, k / g]) s[n, k / g] (moe_int4_*), on the device that is current when
+    the plan is made."""
+
+    def __init__(self, cfg: Int4LinearConfig):
+        # tensors are checked by what the library was told, whatever becomes of cfg
+        self._cfg, self._N, self._K = cfg, cfg.out_features, cfg.in_features
+        h = ctypes.c_void_p()
+        st = _lib().moe_int4_plan(byref(cfg.to_c()), byref(h))
+        if st != MOE_OK:
+            _fail("moe_int4_plan", st)
+        self._h, self._dev = h, _current_device()
+        self._what = (cfg.out_features, cfg.in_features, cfg.group_size, bool(cfg.zero_points), cfg.scale_dtype)
+        self._groups = -(-cfg.in_features // cfg.group_size)
+        self._forward = _lib().moe_int4_forward
+        self._destroy = _lib().moe_int4_plan_destroy
+
+    def __del__(self):
+        if getattr(self, "_h", None) and getattr(self, "_destroy", None):
+            self._destroy(self._h)
+            self._h = None
+
+    @property
+    def cfg(self) -> Int4LinearConfig:
+        return self._cfg
+
+    def workspace_size(self, num_tokens: int) -> int:
+        n = SZ()
+        st = _lib().moe_int4_workspace_size(self._h, num_tokens, byref(n))
+        if st != MOE_OK:
+            _fail("moe_int4_workspace_size", st)
+        return n.value
+
+    def alloc_workspace(self, num_tokens: int, device=None) -> torch.Tensor:
+        return torch.zeros(self.workspace_size(num_tokens), dtype=_U8, device=device or torch.device("cuda", self._dev))
+
+    def transform_weight(self, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None,
+                         stream=None) -> Int4LinearWeight:
+        """Checkpoint codes [N, K / 2] (bytes, element 2i in the low nibble), scales [N, groups] in the plan's scale
+        type and zero points [N, groups] (bytes), in the kernel layout."""
+        N, K, cfg, dev = self._N, self._K, self._cfg, self._dev
+        _flat("codes", codes, _U8, N * K // 2, dev)
+        _flat("scales", scales, cfg.scale_dtype, N * self._groups, dev)
+        if (zeros is not None) != bool(cfg.zero_points):
+            raise ValueError("zeros must be given when, and only when, the plan has zero points")
+        if zeros is not None:
+            _flat("zeros", zeros, _U8, N * self._groups, dev)
+        sizes = [SZ(), SZ(), SZ()]
+        st = _lib().moe_int4_weight_size(self._h, *(byref(n) for n in sizes))
+        if st != MOE_OK:
+            _fail("moe_int4_weight_size", st)
+        with _on(stream):
+            new = [torch.empty(n.value, dtype=_U8, device=codes.device) if n.value else None for n in sizes]
+        w = Int4LinearWeight(*new, self._what)
+        src = Int4WeightC(codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr())
+        fn = _lib().moe_int4_transform_weight
+        call = fn if dev == _current_device() else _at_device(fn, dev)
+        st = call(self._h, byref(src), w._ref, _stream(stream, dev))
+        if st != MOE_OK:
+            _fail("moe_int4_transform_weight", st)
+        return w
+
+    def forward(self, x: torch.Tensor, weight: Int4LinearWeight, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """x bf16 [T, K]; out bf16 [T, N]."""
+        N, dev = self._N, self._dev
+        shape = _matrix("x", x)
+        T = shape[0]
+        if shape[1] != self._K:
+            raise ValueError(f"x must be [T, {self._K}], got {tuple(shape)}")
+        ldx = _row_stride("x", x, _BF16, shape, dev)
+        ref = weight._arg(dev, self._what)
+        if out is None:
+            with _on(stream):
+                out = torch.empty((T, N), dtype=_BF16, device=x.device)
+        ldo = _row_stride("out", out, _BF16, (T, N), dev)
+        if workspace is None:
+            with _on(stream):
+                workspace = self.alloc_workspace(T, out.device)
+        elif workspace.get_device() != dev or workspace.dtype is not _U8 or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{dev}")
+        fn = self._forward
+        call = fn if dev == _current_device() else _at_device(fn, dev)
+        st = call(self._h, T, x.data_ptr(), ldx, ref, out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel(),
+                  _stream(stream, dev))
+        if st:
+            _fail("moe_int4_forward", st)
+        return out
+
+    def set_wait_timeout(self, ns: int):
+        """Limit of each bounded wait in the product's kernels (0: the default, 2 s)."""
+        st = _lib().moe_int4_set_wait_timeout(self._h, ns)
+        if st != MOE_OK:
+            _fail("moe_int4_set_wait_timeout", st)
+
+    def last_status(self, workspace: torch.Tensor, stream=None) -> int:
+        """The status of the last forward in this workspace, which is waited for (moe_int4_last_status)."""
+        v = I32()
+        least = self.workspace_size(0)  # the status words lie at its start, as many for every number of tokens
+        if workspace.get_device() != self._dev or workspace.dtype is not _U8 or not workspace.is_contiguous() or \
+                workspace.numel() < least:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor of {least} bytes or more on "
+                             f"cuda:{self._dev}, got {workspace.numel()} {workspace.dtype} on {workspace.device}")
+        fn = _lib().moe_int4_last_status
+        call = fn if self._dev == _current_device() else _at_device(fn, self._dev)
+        st = call(self._h, workspace.data_ptr(), _stream(stream, self._dev), byref(v))
+        if st != MOE_OK:
+            _fail("moe_int4_last_status", st)
+        return v.value
