@@ -669,9 +669,9 @@ int moe_int4_workspace_size(moe_int4_plan_t plan, int32_t num_tokens, size_t* by
 
 /*
  * x bf16 [T, K], row stride x_stride; out bf16 [T, N], row stride out_stride; out overlaps neither x, the weight nor
- * the workspace. Sums are fp32: q - z and x are multiplied exactly and each group's sum is
- * scaled. Deterministic; a row may round otherwise in a batch of
- * another size. T == 0 launches nothing. The workspace's contents do not matter.
+ * the workspace. Sums are fp32. Up to 16 tokens, q - z and x are multiplied exactly and each group's sum is scaled;
+ * with more, the weights (q - z) s are rounded to the nearest bf16 first. Deterministic; a row may round otherwise in a
+ * batch of another size. T == 0 launches nothing. The workspace's contents do not matter.
  */
 int moe_int4_forward(moe_int4_plan_t plan, int32_t num_tokens, const void* x, int64_t x_stride,
                      const moe_int4_weight_t* weight, void* out, int64_t out_stride, void* workspace,

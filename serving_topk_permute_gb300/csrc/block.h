@@ -168,17 +168,15 @@ cudaError_t launch_linear(int fmt, const LinearMaps& m, const LinearArgs& p, con
                           cudaStream_t st);
 
 // ------------------------------------------------------------------ 4-bit integer weights
-// units of 64 k, 16-feature tiles (whole 128-feature blocks), groups with a place of their own (whole units)
-__host__ __device__ constexpr int int4_units(int K) { return (K + 63) / 64; }
+// blocks of 128 k, 16-feature tiles (whole 128-feature blocks), groups with a place of their own (whole blocks)
+__host__ __device__ constexpr int int4_blocks(int K) { return (K + 127) / 128; }
 __host__ __device__ constexpr int64_t int4_tiles(int64_t N) { return (N + 127) / 128 * 8; }
-__host__ __device__ constexpr int int4_slots(int K, int group) {
-    return group == 32 ? 2 * int4_units(K) : group == 64 ? int4_units(K) : (int4_units(K) + 1) / 2;
-}
+__host__ __device__ constexpr int int4_slots(int K, int group) { return int4_blocks(K) * (128 / group); }
 struct Int4Layout {
     const uint8_t* src_codes;    // [N][K / 2]
     const uint16_t* src_scales;  // [N][groups]
     const uint8_t* src_zeros;    // [N][groups] or null
-    uint32_t* codes;             // [tiles][units][32 lanes][4]
+    uint32_t* codes;             // [tiles][blocks][2][32 lanes][4]
     uint32_t* scales;            // [tiles][slots][8]
     uint8_t* zeros;              // [tiles][slots][8] or null
     int N, K, group;
@@ -191,7 +189,8 @@ struct Int4Args {
     const uint8_t* zeros;        // or null: the zero point is 8
     int half;                    // scales are fp16 (else bf16)
     int group, M, N, K;
-    int slots, unit_shift;       // set by launch_int4
+    int slots;                   // set by launch_int4
+    uint32_t by4, by8, by12;     // 2^(32 - 4) and so on, set by launch_int4
     __nv_bfloat16* out;
     int64_t ldo;
     int* status;                 // number of CTAs that report, then a word of each
@@ -199,8 +198,10 @@ struct Int4Args {
 };
 cudaError_t launch_int4_layout(const Int4Layout& a, cudaStream_t st);
 cudaError_t launch_int4_rows(const void* x, int64_t ldx, void* dst, int M, int K, cudaStream_t st);
-cudaError_t launch_int4(const Int4Args& a, int num_sms, cudaStream_t st);
-int int4_max_ctas(int N, int num_sms);
-cudaError_t int4_prepare();
+// x: a map of the rows of x with boxes of 64 k x int4_box(M) tokens, 128-byte swizzle (unused by int4_few(M))
+cudaError_t launch_int4(const CUtensorMap& x, const Int4Args& a, int num_sms, cudaStream_t st);
+bool int4_few(int M);
+int int4_box(int M);
+int int4_max_ctas(int num_sms);
 
 }  // namespace moe

@@ -74,6 +74,18 @@ bool map_rows(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t row
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// rows of K bf16, row_bytes apart, loaded as 64 k x box_rows tiles with 128-byte swizzle; elements past the row
+// and rows past the last one are filled with zeros
+bool map_bf16_rows(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
+    cuuint64_t dims[2] = {K, rows};
+    cuuint64_t strides[1] = {row_bytes};
+    cuuint32_t box[2] = {64, box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // an array of 512-byte scale atoms as a 2-D uint32 tensor [atoms][128], loaded box_atoms at a time;
 // atoms past the last one are filled with zeros
 bool map_atoms(CUtensorMap* m, const void* base, uint64_t atoms, uint32_t box_atoms) {
@@ -238,7 +250,7 @@ int check_int4(const moe_int4_config_t* c) {
 
 // workspace of the product with 4-bit weights: its status words, then rows of x that are copied
 int64_t int4_status_bytes(const moe_int4_plan_s* plan) {
-    return align_up(4 * (1 + (int64_t)int4_max_ctas(plan->cfg.out_features, plan->num_sms)), REGION_ALIGN);
+    return align_up(4 * (1 + (int64_t)int4_max_ctas(plan->num_sms)), REGION_ALIGN);
 }
 
 // The status words of a product, most of them at most: waits for the stream, and clears them.
@@ -790,7 +802,6 @@ int moe_int4_plan(const moe_int4_config_t* cfg, moe_int4_plan_t* out) {
     CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     if (major != 10) return MOE_ERR_UNSUPPORTED;
     if (!get_encode()) return MOE_ERR_CUDA;
-    CUDA_TRY(int4_prepare());
     moe_int4_plan_s* p = new (std::nothrow) moe_int4_plan_s{*cfg, sms, DEFAULT_TIMEOUT_NS};
     if (!p) return MOE_ERR_CUDA;
     *out = p;
@@ -812,7 +823,7 @@ int moe_int4_weight_size(moe_int4_plan_t plan, size_t* codes, size_t* scales, si
     if (!plan || !codes || !scales || !zeros) return MOE_ERR_INVALID_ARG;
     const moe_int4_config_t& c = plan->cfg;
     const int64_t tiles = int4_tiles(c.out_features), slots = int4_slots(c.in_features, c.group_size);
-    *codes = (size_t)(tiles * int4_units(c.in_features) * 512);
+    *codes = (size_t)(tiles * int4_blocks(c.in_features) * 1024);
     *scales = (size_t)(tiles * slots * 32);
     *zeros = c.zero_points ? (size_t)(tiles * slots * 8) : 0;
     return MOE_OK;
@@ -888,13 +899,17 @@ int moe_int4_forward(moe_int4_plan_t plan, int32_t num_tokens, const void* x, in
     a.ldo = out_stride;
     a.status = (int*)workspace;
     a.timeout_ns = plan->timeout_ns;
-    CUDA_TRY(launch_int4(a, plan->num_sms, st));
+    CUtensorMap map{};
+    if (!int4_few(T) && !map_bf16_rows(&map, a.x, (uint64_t)c.in_features, (uint64_t)T, (uint64_t)(2 * a.ldx),
+                                       (uint32_t)int4_box(T)))
+        return MOE_ERR_CUDA;
+    CUDA_TRY(launch_int4(map, a, plan->num_sms, st));
     return MOE_OK;
 }
 
 int moe_int4_last_status(moe_int4_plan_t plan, void* workspace, void* stream, int32_t* status) {
     if (!plan || !workspace || !status) return MOE_ERR_INVALID_ARG;
-    return read_status(workspace, int4_max_ctas(plan->cfg.out_features, plan->num_sms), (cudaStream_t)stream, status);
+    return read_status(workspace, int4_max_ctas(plan->num_sms), (cudaStream_t)stream, status);
 }
 
 }  // extern "C"
