@@ -176,9 +176,9 @@ struct Int4Layout {
     const uint8_t* src_codes;    // [N][K / 2]
     const uint16_t* src_scales;  // [N][groups]
     const uint8_t* src_zeros;    // [N][groups] or null
-    uint32_t* codes;             // [tiles][blocks][2][32 lanes][4]
-    uint32_t* scales;            // [tiles][slots][8]
-    uint8_t* zeros;              // [tiles][slots][8] or null
+    uint32_t* codes;             // [tiles / 8][blocks][8][2][32 lanes][4]
+    uint32_t* scales;            // [tiles / 8][slots][64]
+    uint8_t* zeros;              // [tiles / 8][slots][64] or null
     int N, K, group;
 };
 struct Int4Args {
@@ -198,10 +198,15 @@ struct Int4Args {
 };
 cudaError_t launch_int4_layout(const Int4Layout& a, cudaStream_t st);
 cudaError_t launch_int4_rows(const void* x, int64_t ldx, void* dst, int M, int K, cudaStream_t st);
-// x: a map of the rows of x with boxes of 64 k x int4_box(M) tokens, 128-byte swizzle (unused by int4_few(M))
-cudaError_t launch_int4(const CUtensorMap& x, const Int4Args& a, int num_sms, cudaStream_t st);
-bool int4_few(int M);
-int int4_box(int M);
+// maps of the rows of x with boxes of 64 k x that many tokens (0: not needed), 128-byte swizzle
+struct Int4Boxes {
+    int x, cut;
+};
+struct Int4Maps {
+    CUtensorMap x, cut;
+};
+Int4Boxes int4_boxes(int M, int N, int num_sms);
+cudaError_t launch_int4(const Int4Maps& m, const Int4Args& a, int num_sms, cudaStream_t st);
 int int4_max_ctas(int num_sms);
 
 }  // namespace moe

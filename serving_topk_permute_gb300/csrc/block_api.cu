@@ -899,11 +899,13 @@ int moe_int4_forward(moe_int4_plan_t plan, int32_t num_tokens, const void* x, in
     a.ldo = out_stride;
     a.status = (int*)workspace;
     a.timeout_ns = plan->timeout_ns;
-    CUtensorMap map{};
-    if (!int4_few(T) && !map_bf16_rows(&map, a.x, (uint64_t)c.in_features, (uint64_t)T, (uint64_t)(2 * a.ldx),
-                                       (uint32_t)int4_box(T)))
-        return MOE_ERR_CUDA;
-    CUDA_TRY(launch_int4(map, a, plan->num_sms, st));
+    Int4Maps maps{};
+    const Int4Boxes boxes = int4_boxes(T, c.out_features, plan->num_sms);
+    auto map = [&](CUtensorMap* m, int tokens) {
+        return tokens == 0 || map_bf16_rows(m, a.x, (uint64_t)c.in_features, (uint64_t)T, (uint64_t)(2 * a.ldx), (uint32_t)tokens);
+    };
+    if (!map(&maps.x, boxes.x) || !map(&maps.cut, boxes.cut)) return MOE_ERR_CUDA;
+    CUDA_TRY(launch_int4(maps, a, plan->num_sms, st));
     return MOE_OK;
 }
 

@@ -37,8 +37,8 @@ __global__ void __launch_bounds__(256) int4_codes_kernel(const uint8_t* src, uin
     if (at >= words) return;
     const int units = 2 * int4_blocks(K);
     const int s = (int)(at % 4), lane = (int)(at / 4 % 32);
-    const int64_t unit = at / 128;
-    const int u = (int)(unit % units), tile = (int)(unit / units);
+    const int64_t unit = at / 128;  // [128 features][block][16 features][half of the block]
+    const int u = 2 * (int)(unit / 16 % (units / 2)) + (int)(unit % 2), tile = 8 * (int)(unit / 8 / units) + (int)(unit / 2 % 8);
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -47,16 +47,16 @@ __global__ void __launch_bounds__(256) int4_codes_kernel(const uint8_t* src, uin
     }
     dst[at] = w;
 }
-// Scales: for each 16 features and group, 8 words of the scales of the features i and i + 8; zero points
-// behind them: 8 bytes of the two nibbles. One thread for each word. Features past N have the scale 0.
+// Scales: for each 128 features and group, 64 words, 8 of each 16 features: the scales of the features i and i + 8.
+// Zero points alike: bytes of the two nibbles. One thread for each word. Features past N have the scale 0.
 __global__ void __launch_bounds__(256)
     int4_scales_kernel(const uint16_t* scales, const uint8_t* zeros, uint32_t* dst, uint8_t* dst_zeros, int N, int groups,
                        int slots, int64_t words) {
     const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
     grid_dep_wait();
     if (at >= words) return;
-    const int i = (int)(at % 8), g = (int)(at / 8 % slots);
-    const int64_t n = 16 * (at / 8 / slots) + i;
+    const int i = (int)(at % 8), g = (int)(at / 64 % slots);
+    const int64_t n = 128 * (at / 64 / slots) + 16 * (at / 8 % 8) + i;
     auto scale = [&](int64_t row) { return row < N && g < groups ? (uint32_t)scales[row * groups + g] : 0u; };
     dst[at] = scale(n) | scale(n + 8) << 16;
     if (zeros) {
@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) int4_few_kernel(const __grid
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         const int tile = min(tile0 + r, last_tile);
-        codes[r] = p.codes + ((int64_t)tile * blocks + first) * 64 + lane;
-        const int64_t at = ((int64_t)tile * p.slots + SPAN * first) * 8 + lane / 4;
+        codes[r] = p.codes + (((int64_t)(tile / 8) * blocks + first) * 8 + tile % 8) * 64 + lane;
+        const int64_t at = ((int64_t)(tile / 8) * p.slots + SPAN * first) * 64 + tile % 8 * 8 + lane / 4;
         scales[r] = p.scales + at;
         zeros[r] = p.zeros + at;
     }
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) int4_few_kernel(const __grid
         for (int r = 0; r < RT; ++r) {
             a.codes[r][0] = codes[r][0];
             a.codes[r][1] = codes[r][32];
-            codes[r] += 64 * WARPS;
+            codes[r] += 512 * WARPS;
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -199,11 +199,11 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) int4_few_kernel(const __grid
         for (int r = 0; r < RT; ++r) {
 #pragma unroll
             for (int g = 0; g < SPAN; ++g) {
-                a.scale[r][g] = scales[r][8 * g];
-                if (ZEROS) a.zero[r][g] = zeros[r][8 * g];
+                a.scale[r][g] = scales[r][64 * g];
+                if (ZEROS) a.zero[r][g] = zeros[r][64 * g];
             }
-            scales[r] += 8 * SPAN * WARPS;
-            if (ZEROS) zeros[r] += 8 * SPAN * WARPS;
+            scales[r] += 64 * SPAN * WARPS;
+            if (ZEROS) zeros[r] += 64 * SPAN * WARPS;
         }
     };
     auto multiply = [&](const Block& h) {
@@ -347,48 +347,104 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t b, 
         : "memory");
 }
 
-constexpr int MANY_WARPS = 8;                        // that make bf16 weights of the codes, and store the tile
-constexpr int MANY_THREADS = 64 + 32 * MANY_WARPS;   // warp 0: copies, warp 1: MMAs
 constexpr int MANY_MAX_SPLITS = 8;
 
-template <int BT>
+// a wait that is over as a rule: one test before the bounded wait
+__device__ __forceinline__ bool soon_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, const volatile int* abort) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    return warp_wait(bar, parity, timeout_ns, abort);
+}
+
+// A stage of 128 k of 128 features' codes with their scales and zero points
+template <int SPAN, bool ZEROS, bool HALF>
+struct Stage {
+    static constexpr int SCALES = 8192, ZERO_POINTS = SCALES + 256 * SPAN, BYTES = ZERO_POINTS + 64 * SPAN;
+    static constexpr int COPIED = ZEROS ? BYTES : ZERO_POINTS;
+    static constexpr int OWN = SPAN == 4 ? 2 : 1;  // groups of a unit of 64 k
+    // block ks of the features from 128 nt on, into shared memory (one thread)
+    static __device__ __forceinline__ void copy(const Int4Args& p, int nt, int ks, int blocks, uint32_t to, uint32_t full) {
+        mbar_arrive_expect_tx(full, COPIED);
+        bulk_load(to, p.codes + ((int64_t)nt * blocks + ks) * 512, 8192, full);
+        const int64_t slot = ((int64_t)nt * p.slots + SPAN * ks) * 64;
+        bulk_load(to + SCALES, p.scales + slot, 256 * SPAN, full);
+        if (ZEROS) bulk_load(to + ZERO_POINTS, p.zeros + slot, 64 * SPAN, full);
+    }
+    // a lane's part of a unit (half) of tile t of 16 features
+    uint4 codes;
+    uint32_t scale[OWN], zero[OWN];
+    __device__ __forceinline__ void load(const uint8_t* from, int t, int half, int lane) {
+        codes = *reinterpret_cast<const uint4*>(from + t * 1024 + half * 512 + lane * 16);
+#pragma unroll
+        for (int g = 0; g < OWN; ++g) {
+            const int at = (SPAN == 1 ? 0 : OWN * half + g) * 64 + t * 8 + lane / 4;
+            scale[g] = *reinterpret_cast<const uint32_t*>(from + SCALES + 4 * at);
+            zero[g] = ZEROS ? from[ZERO_POINTS + at] : 0;
+        }
+    }
+    // its weights, as 16 lanes x 32 columns of tensor memory hold them
+    __device__ __forceinline__ void weights(const Int4Args& p, uint32_t (&r)[16]) const {
+        const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+        for (int g = 0; g < OWN; ++g) {
+            uint32_t low = 0x43084308u, high = low;  // 136: the zero point is 8
+            if (ZEROS) zero_points(zero[g], low, high);
+            const Scaled<HALF> scaled(scale[g]);
+#pragma unroll
+            for (int s = 4 / OWN * g; s < 4 / OWN * (g + 1); ++s) {
+                uint32_t a[4];
+                whole_numbers(p, w[s], low, high, a);
+                r[4 * s] = scaled.times(a[0], 0);
+                r[4 * s + 1] = scaled.times(a[2], 0);
+                r[4 * s + 2] = scaled.times(a[1], 1);
+                r[4 * s + 3] = scaled.times(a[3], 1);
+            }
+        }
+    }
+};
+
+template <int BT, int SPAN>
 struct ManyCfg {
-    static constexpr int X_BYTES = BT * 256, CODE_BYTES = 8192;  // a stage of 128 k: tokens in two swizzled halves, codes
-    static constexpr int STAGE = X_BYTES + CODE_BYTES;
-    static constexpr int BAR_BYTES = 256;
-    static constexpr int CTAS = BT <= 128 ? 2 : 1;
-    static constexpr int BUDGET = (CTAS == 2 ? 233472 / 2 - 1024 : 232448) - BAR_BYTES - 1024;
-    static constexpr int STAGES = BUDGET / STAGE < 6 ? BUDGET / STAGE : 6;
-    static constexpr int SMEM = STAGES * STAGE + BAR_BYTES + 1024;
-    static constexpr int BUFS = BT == 256 ? 4 : 2;   // weights of a stage in tensor memory: 64 columns each
-    static constexpr int TMEM = BT == 256 ? 512 : 256;
+    static constexpr int X_BYTES = BT * 256, CODE_BYTES = Stage<SPAN, true, true>::BYTES;  // a stage's tokens; codes
+    // stages: of the codes, and of the tokens and of the weights in tensor memory (64 columns each), freed together
+    static constexpr int CS = BT == 128 ? 4 : BT == 64 ? 6 : 8, BUFS = BT == 128 ? 2 : 3;
+    static constexpr int AHEAD = CS - BUFS;  // codes are asked for so many stages before the tokens
+    static constexpr int BAR_BYTES = 512;
+    static constexpr int CTAS = 2;
+    static constexpr int WARPS = 8;                  // that make bf16 weights of the codes, and store the tile
+    static constexpr int THREADS = 64 + 32 * WARPS;  // warp 0: copies, warp 1: MMAs
+    static constexpr int RINGS = BUFS * X_BYTES + CS * CODE_BYTES;
+    static constexpr int SMEM = RINGS + BAR_BYTES + 1024;
+    static constexpr int TMEM = 256;
     static constexpr int SUM_BYTES = (BT + MANY_MAX_SPLITS) * 128 * 4;
-    static_assert(BT + 64 * BUFS <= TMEM && (2 * STAGES + 2 * BUFS + 2) * 8 + 16 <= BAR_BYTES, "budgets");
-    static_assert(BT == 256 || STAGES * STAGE >= SUM_BYTES, "the ring holds the sums");
-    static_assert(STAGES >= 2, "stages");
+    static_assert(SMEM <= 233472 / 2 - 1024, "shared memory");
+    static_assert(BT + 64 * BUFS <= TMEM && (2 * CS + 3 * BUFS + 2) * 8 + 16 <= BAR_BYTES, "budgets");
+    static_assert(RINGS >= SUM_BYTES, "the rings hold the sums");
+    // codes n wait for the weights of stage n - CS, those for the MMAs of stage n - CS - BUFS, which need its tokens
+    static_assert(AHEAD >= 0 && AHEAD < CS + BUFS, "no ring waits for itself");
 };
 
 // 128 features x BT tokens a CTA, K split over the CTAs of a cluster where there are few tiles. Each stage of 128 k:
-// the tokens come by TMA, the codes by bulk copies; eight warps turn the codes into bf16 weights and store
+// the tokens come by TMA, the codes by bulk copies; the other warps turn the codes into bf16 weights and store
 // them to tensor memory, from where the MMAs take them as their row side, with the tokens in shared memory as
 // columns. So weights never pass through shared memory as bf16, and a tile's features are the accumulator's lanes.
 template <int BT, int SPAN, bool ZEROS, bool HALF>
-__global__ void __launch_bounds__(MANY_THREADS, ManyCfg<BT>::CTAS)
+__global__ void __launch_bounds__((ManyCfg<BT, SPAN>::THREADS), (ManyCfg<BT, SPAN>::CTAS))
     int4_many_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ Int4Args p) {
-    using C = ManyCfg<BT>;
-    constexpr int STAGES = C::STAGES, BUFS = C::BUFS;
+    using C = ManyCfg<BT, SPAN>;
+    using S = Stage<SPAN, ZEROS, HALF>;
+    constexpr int CS = C::CS, BUFS = C::BUFS, WARPS = C::WARPS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 2 * BUFS + 2);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RINGS);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * CS + 3 * BUFS + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* never = reinterpret_cast<int*>(tmem_slot + 2);
     float* sums = reinterpret_cast<float*>(smem);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, made0 = empty0 + 8 * STAGES,
-                   used0 = made0 + 8 * BUFS, done_bar = used0 + 8 * BUFS, free_bar = done_bar + 8;
-    const uint32_t smem0 = smem_u32(smem);
+    const uint32_t xfull0 = smem_u32(bars), cfull0 = xfull0 + 8 * BUFS, cempty0 = cfull0 + 8 * CS, made0 = cempty0 + 8 * CS, used0 = made0 + 8 * BUFS,
+                   done_bar = used0 + 8 * BUFS, free_bar = done_bar + 8;
+    const uint32_t smem0 = smem_u32(smem), codes0 = smem0 + BUFS * C::X_BYTES;
     const uint64_t tmo = p.timeout_ns;
     const uint32_t splits = gridDim.x, rank = blockIdx.x;
     const int blocks = int4_blocks(p.K), n_tiles = (p.N + 127) / 128, tiles = n_tiles * ((p.M + BT - 1) / BT);
@@ -397,16 +453,17 @@ __global__ void __launch_bounds__(MANY_THREADS, ManyCfg<BT>::CTAS)
     const int tile0 = blockIdx.y, tile_step = gridDim.y;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full0 + 8 * s, 1);
-            mbar_init(empty0 + 8 * s, 1 + MANY_WARPS);  // the MMAs' commit, and each warp that has read its codes
+        for (int s = 0; s < CS; ++s) {
+            mbar_init(cfull0 + 8 * s, 1);
+            mbar_init(cempty0 + 8 * s, WARPS);
         }
         for (int b = 0; b < BUFS; ++b) {
-            mbar_init(made0 + 8 * b, MANY_WARPS);
+            mbar_init(xfull0 + 8 * b, 1);
+            mbar_init(made0 + 8 * b, WARPS);
             mbar_init(used0 + 8 * b, 1);
         }
         mbar_init(done_bar, 1);
-        mbar_init(free_bar, MANY_WARPS);
+        mbar_init(free_bar, WARPS);
         *abort_flag = 0;
         *never = 0;
         fence_mbar_init();
@@ -427,62 +484,73 @@ __global__ void __launch_bounds__(MANY_THREADS, ManyCfg<BT>::CTAS)
     bool complete = true;  // meaningful in the warps that store
     if (warp == 0) {
         const bool elected = elect_one();
-        int issued = 0;
+        int codes = 0, stages = 0;  // issued: codes, tokens
+        int ctile = tile0, ci = 0;  // whose codes are next
         bool ok = true;
+        auto load_codes = [&]() {
+            const int stage = codes % CS;
+            if (ctile >= tiles) return;
+            if (!soon_wait(cempty0 + 8 * stage, ((codes / CS) & 1) ^ 1, tmo, abort_flag)) {
+                give_up();
+                ok = false;
+                return;
+            }
+            if (elected)
+                S::copy(p, ctile % n_tiles, k0 + ci, blocks, codes0 + stage * C::CODE_BYTES, cfull0 + 8 * stage);
+            __syncwarp();
+            ++codes;
+            if (++ci == steps) ci = 0, ctile += tile_step;
+        };
+        for (int i = 0; i < C::AHEAD; ++i) load_codes();
         for (int tile = tile0; ok && tile < tiles; tile += tile_step) {
-            const int nt = tile % n_tiles, tt = tile / n_tiles;
-            for (int i = 0; i < steps; ++i, ++issued) {
-                const int stage = issued % STAGES;
-                if (!warp_wait(empty0 + 8 * stage, ((issued / STAGES) & 1) ^ 1, tmo, abort_flag)) {
+            for (int i = 0; ok && i < steps; ++i) {
+                load_codes();
+                const int buf = stages % BUFS;
+                if (!ok || !warp_wait(used0 + 8 * buf, ((stages / BUFS) & 1) ^ 1, tmo, abort_flag)) {
                     give_up();
                     ok = false;
                     break;
                 }
                 if (elected) {
-                    const uint32_t st = smem0 + stage * C::STAGE, full = full0 + 8 * stage;
-                    const int ks = k0 + i;
-                    mbar_arrive_expect_tx(full, C::STAGE);
-                    tma_load_2d(st, &tmX, full, 128 * ks, tt * BT);
-                    tma_load_2d(st + C::X_BYTES / 2, &tmX, full, 128 * ks + 64, tt * BT);
-                    const uint4* codes = p.codes + ((int64_t)nt * 8 * blocks + ks) * 64;
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        bulk_load(st + C::X_BYTES + 1024 * r, codes + (int64_t)r * blocks * 64, 1024, full);
+                    const uint32_t st = smem0 + buf * C::X_BYTES, full = xfull0 + 8 * buf;
+                    mbar_arrive_expect_tx(full, C::X_BYTES);
+                    tma_load_2d(st, &tmX, full, 128 * (k0 + i), tile / n_tiles * BT);
+                    tma_load_2d(st + C::X_BYTES / 2, &tmX, full, 128 * (k0 + i) + 64, tile / n_tiles * BT);
                 }
                 __syncwarp();
+                ++stages;
             }
         }
-        // every load issued lands before the CTA may exit or reuse the ring
-        for (int s = 0; s < STAGES && s < issued; ++s) {
-            const int last = s + (issued - 1 - s) / STAGES * STAGES;
-            mbar_wait(full0 + 8 * s, (last / STAGES) & 1, DRAIN_TIMEOUT_NS, never);
-        }
+        // every load issued lands before the CTA may exit or reuse the rings
+        for (int s = 0; s < BUFS && s < stages; ++s)
+            mbar_wait(xfull0 + 8 * s, ((stages - 1 - s) / BUFS) & 1, DRAIN_TIMEOUT_NS, never);
+        for (int s = 0; s < CS && s < codes; ++s)
+            mbar_wait(cfull0 + 8 * s, ((codes - 1 - s) / CS) & 1, DRAIN_TIMEOUT_NS, never);
         __syncwarp();
     } else if (warp == 1) {
         const bool elected = elect_one();
         int at = 0, round = 0;  // stages, tiles so far
         bool ok = true;
         for (int tile = tile0; ok && tile < tiles; tile += tile_step, ++round) {
-            if (round > 0 && !warp_wait(free_bar, (round - 1) & 1, tmo, abort_flag)) {  // the accumulators
+            if (round > 0 && !soon_wait(free_bar, (round - 1) & 1, tmo, abort_flag)) {  // the accumulators
                 give_up();
                 break;
             }
             for (int i = 0; i < steps; ++i, ++at) {
-                const int stage = at % STAGES, buf = at % BUFS;
-                if (!warp_wait(full0 + 8 * stage, (at / STAGES) & 1, tmo, abort_flag) ||
-                    !warp_wait(made0 + 8 * buf, (at / BUFS) & 1, tmo, abort_flag)) {
+                const int buf = at % BUFS;
+                if (!soon_wait(xfull0 + 8 * buf, (at / BUFS) & 1, tmo, abort_flag) ||
+                    !soon_wait(made0 + 8 * buf, (at / BUFS) & 1, tmo, abort_flag)) {
                     give_up();
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (elected) {
-                    const uint32_t x = (smem0 + stage * C::STAGE) / 16, w = weights0 + 64 * buf;
+                    const uint32_t x = (smem0 + buf * C::X_BYTES) / 16, w = weights0 + 64 * buf;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         mma_bf16_ta(tmem_base, w + 8 * j, row_desc(x + j / 4 * (C::X_BYTES / 32) + 2 * (j % 4)),
                                     idesc_bf16(BT), i > 0 || j > 0);
-                    tc_commit(empty0 + 8 * stage);
                     tc_commit(used0 + 8 * buf);
                 }
                 __syncwarp();
@@ -497,67 +565,29 @@ __global__ void __launch_bounds__(MANY_THREADS, ManyCfg<BT>::CTAS)
         // a quarter of the tensor memory's lanes, two tiles of 16 features, and one of the stage's units
         const int quarter = warp % 4, half = (warp - 2) / 4;
         const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16);
-        constexpr int OWN = SPAN == 4 ? 2 : 1;  // groups of a unit
-        uint32_t sc[2][OWN], zp[2][OWN];
-        auto fetch = [&](int tile, int i) {  // the scales of a tile's stage, or of the next tile's first one
-            if (i == steps) i = 0, tile += tile_step;
-            if (tile >= tiles) return;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int g = 0; g < OWN; ++g) {
-                    const int slot = SPAN * (k0 + i) + (SPAN == 1 ? 0 : OWN * half) + g;
-                    const int64_t from = ((int64_t)(tile % n_tiles * 8 + 2 * quarter + j) * p.slots + slot) * 8 + lane / 4;
-                    sc[j][g] = p.scales[from];
-                    if (ZEROS) zp[j][g] = p.zeros[from];
-                }
-        };
         int at = 0, round = 0;
-        fetch(tile0, 0);
         for (int tile = tile0; complete && tile < tiles; tile += tile_step, ++round) {
             for (int i = 0; i < steps; ++i, ++at) {
-                const int stage = at % STAGES, buf = at % BUFS;
-                uint32_t scale[2][OWN], zero[2][OWN];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int g = 0; g < OWN; ++g) scale[j][g] = sc[j][g], zero[j][g] = ZEROS ? zp[j][g] : 0;
-                fetch(tile, i + 1);
-                if (!warp_wait(full0 + 8 * stage, (at / STAGES) & 1, tmo, abort_flag)) {
+                const int stage = at % CS, buf = at % BUFS;
+                if (!soon_wait(cfull0 + 8 * stage, (at / CS) & 1, tmo, abort_flag)) {
                     complete = false;
                     break;
                 }
-                uint4 codes[2];
+                S own[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    codes[j] = *reinterpret_cast<const uint4*>(smem + stage * C::STAGE + C::X_BYTES +
-                                                               (2 * quarter + j) * 1024 + half * 512 + lane * 16);
+                    own[j].load(smem + BUFS * C::X_BYTES + stage * C::CODE_BYTES, 2 * quarter + j, half, lane);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(empty0 + 8 * stage);
-                if (!warp_wait(used0 + 8 * buf, ((at / BUFS) & 1) ^ 1, tmo, abort_flag)) {
+                if (lane == 0) mbar_arrive(cempty0 + 8 * stage);
+                if (!soon_wait(used0 + 8 * buf, ((at / BUFS) & 1) ^ 1, tmo, abort_flag)) {
                     complete = false;
                     break;
                 }
                 tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint32_t w[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
                     uint32_t r[16];
-#pragma unroll
-                    for (int g = 0; g < OWN; ++g) {
-                        uint32_t low = 0x43084308u, high = low;  // 136: the zero point is 8
-                        if (ZEROS) zero_points(zero[j][g], low, high);
-                        const Scaled<HALF> scaled(scale[j][g]);
-#pragma unroll
-                        for (int s = 4 / OWN * g; s < 4 / OWN * (g + 1); ++s) {
-                            uint32_t a[4];
-                            whole_numbers(p, w[s], low, high, a);
-                            r[4 * s] = scaled.times(a[0], 0);
-                            r[4 * s + 1] = scaled.times(a[2], 0);
-                            r[4 * s + 2] = scaled.times(a[1], 1);
-                            r[4 * s + 3] = scaled.times(a[3], 1);
-                        }
-                    }
+                    own[j].weights(p, r);
                     tmem_st_16x32(weights0 + 64 * buf + 32 * half + ((uint32_t)(32 * quarter + 16 * j) << 16), r);
                 }
                 tmem_st_wait();
@@ -565,7 +595,7 @@ __global__ void __launch_bounds__(MANY_THREADS, ManyCfg<BT>::CTAS)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(made0 + 8 * buf);
             }
-            if (complete) complete = warp_wait(done_bar, round & 1, tmo, abort_flag);
+            if (complete) complete = soon_wait(done_bar, round & 1, tmo, abort_flag);
             if (!complete) {
                 give_up();
                 break;
@@ -575,7 +605,7 @@ __global__ void __launch_bounds__(MANY_THREADS, ManyCfg<BT>::CTAS)
             const int n = tile % n_tiles * 128 + quarter * 32 + lane, t0 = tile / n_tiles * BT;
             const int tokens = min(BT, p.M - t0);
 #pragma unroll 1
-            for (int c0 = half * 32; c0 < tokens; c0 += 64) {
+            for (int c0 = (warp - 2) / 4 * 32; c0 < tokens; c0 += 8 * WARPS) {
                 float v[32];
                 tmem_ld32(tacc + c0, v);
                 tmem_ld_wait();
@@ -603,7 +633,7 @@ __global__ void __launch_bounds__(MANY_THREADS, ManyCfg<BT>::CTAS)
             const int quarter = warp % 4;
             const uint32_t mine = smem_u32(sums + (int)rank * per_rank * 128 + quarter * 32 + lane);
 #pragma unroll 1
-            for (int c0 = (warp - 2) / 4 * 32; c0 < tokens; c0 += 64) {
+            for (int c0 = (warp - 2) / 4 * 32; c0 < tokens; c0 += 8 * WARPS) {
                 float v[32];
                 tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + c0, v);
                 tmem_ld_wait();
@@ -625,7 +655,7 @@ __global__ void __launch_bounds__(MANY_THREADS, ManyCfg<BT>::CTAS)
         // this CTA's tokens: a warp takes a token, a lane 4 features, the ranks added in order
         if (warp >= 2 && complete) {
             const int first = (int)rank * per_rank, count = min(per_rank, tokens - first);
-            for (int i = warp - 2; i < count; i += MANY_WARPS) {
+            for (int i = warp - 2; i < count; i += WARPS) {
                 const float4* u = reinterpret_cast<const float4*>(sums + i * 128) + lane;
                 float4 y = u[0];
                 for (uint32_t r = 1; r < splits; ++r) {
@@ -650,6 +680,346 @@ __global__ void __launch_bounds__(MANY_THREADS, ManyCfg<BT>::CTAS)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, C::TMEM);
+    }
+}
+
+// ------------------------------------------------------------------ many tokens
+// Which tiles of 256 features x 256 tokens a CTA pair takes: every pairs-th one of the whole rounds, and of the tiles
+// left, too few for all pairs, a piece of 256 >> cut tokens.
+struct Pairs {
+    int pairs, whole, cut;
+};
+static Pairs pairs_of(int M, int N, int num_sms) {
+    const int64_t tiles = ceil_div(N, 256) * ceil_div(M, 256);
+    Pairs s{num_sms / 2, 0, 0};
+    const int left = (int)(tiles % s.pairs);
+    s.whole = (int)(tiles - left);
+    while (s.cut < 2 && left << (s.cut + 1) <= s.pairs) ++s.cut;
+    if (s.whole == 0) s.pairs = left << s.cut;
+    return s;
+}
+
+template <int SPAN>
+struct PairCfg {
+    static constexpr int X_BYTES = 128 * 256, CODE_BYTES = Stage<SPAN, true, true>::BYTES;  // half of a stage's tokens; codes
+    static constexpr int CS = 8, BUFS = 4;
+    static constexpr int AHEAD = CS - BUFS;
+    static constexpr int BAR_BYTES = 512;
+    static constexpr int WARPS = 16;
+    static constexpr int THREADS = 64 + 32 * WARPS;
+    static constexpr int RINGS = BUFS * X_BYTES + CS * CODE_BYTES;
+    static constexpr int SMEM = RINGS + BAR_BYTES + 1024;
+    static_assert(SMEM <= 232448 && (2 * CS + 3 * BUFS + 4) * 8 + 16 <= BAR_BYTES, "shared memory");
+    static_assert(AHEAD >= 0 && AHEAD < CS + BUFS, "no ring waits for itself");
+};
+__device__ __forceinline__ void mma2_bf16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Persistent CTA pairs: 256 features x 256 tokens, 128 features and half of the tokens' rows a CTA, so that a token
+// is read once for 256 features: with CTAs of their own, x came from L2 at 43 bytes a cycle and SM, and
+// that bounded the kernel (2048 x 8192 x 4096: 105 us, 91 with no x loaded).
+// The weights are made as above, by sixteen warps; those of a tile's first stages before the tile before is stored.
+template <int SPAN, bool ZEROS, bool HALF>
+__global__ void __launch_bounds__(PairCfg<SPAN>::THREADS, 1)
+    int4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmCut,
+                     const __grid_constant__ Int4Args p, const Pairs s) {
+    using C = PairCfg<SPAN>;
+    using S = Stage<SPAN, ZEROS, HALF>;
+    constexpr int CS = C::CS, BUFS = C::BUFS, WARPS = C::WARPS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RINGS);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * CS + 3 * BUFS + 4);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* never = reinterpret_cast<int*>(tmem_slot + 2);
+    volatile uint32_t* peer_issued = tmem_slot + 3;  // leader: stages of tokens that the follower's warp 0 asked for
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    // the leader's: xfull, made, free; each CTA's own: the others
+    const uint32_t xfull0 = smem_u32(bars), cfull0 = xfull0 + 8 * BUFS, cempty0 = cfull0 + 8 * CS, made0 = cempty0 + 8 * CS, used0 = made0 + 8 * BUFS,
+                   done_bar = used0 + 8 * BUFS, free_bar = done_bar + 8, drain_bar = done_bar + 16,
+                   teardown_bar = done_bar + 24;
+    const uint32_t smem0 = smem_u32(smem), codes0 = smem0 + BUFS * C::X_BYTES;
+    const uint64_t tmo = p.timeout_ns;
+    const int steps = int4_blocks(p.K), n_tiles = (p.N + 255) / 256, tiles = n_tiles * ((p.M + 255) / 256);
+    const int pair = blockIdx.x / 2, rounds = s.whole / s.pairs;
+
+    // item r of this pair; false after the last one
+    struct Item {
+        int nt, t0, tokens, cols, cut;  // tile of 256 features; tokens; the same in whole blocks of 32
+    };
+    auto item = [&](int r, Item& i) -> bool {
+        int tile = pair + r * s.pairs, sub = 0, width = 256;
+        if (r > rounds) return false;
+        if (r == rounds) {
+            tile = s.whole + (pair >> s.cut);
+            sub = pair & ((1 << s.cut) - 1);
+            width = 256 >> s.cut;
+            if (tile >= tiles) return false;
+        }
+        i.nt = tile % n_tiles;
+        i.t0 = tile / n_tiles * 256 + sub * width;
+        i.tokens = min(width, p.M - i.t0);
+        i.cols = (i.tokens + 31) / 32 * 32;
+        i.cut = r == rounds;
+        return i.tokens > 0;
+    };
+
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < CS; ++b) {
+            mbar_init(cfull0 + 8 * b, 1);
+            mbar_init(cempty0 + 8 * b, WARPS / 2);
+        }
+        for (int b = 0; b < BUFS; ++b) {
+            mbar_init(xfull0 + 8 * b, leader ? 2 : 1);  // both CTAs ask for their rows
+            mbar_init(made0 + 8 * b, WARPS);            // of either CTA half of the warps
+            mbar_init(used0 + 8 * b, 1);
+        }
+        mbar_init(done_bar, 1);
+        mbar_init(free_bar, 2 * WARPS);
+        mbar_init(drain_bar, 1);
+        mbar_init(teardown_bar, 1);
+        *abort_flag = 0;
+        *peer_issued = 0;
+        *never = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tmX);
+        prefetch_tmap(&tmCut);
+    }
+    if (warp == 1) {
+        tmem_alloc2(smem_u32(tmem_slot), 512);
+        tmem_relinquish2();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the peer's barriers exist before anyone arrives on them
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot, weights0 = tmem_base + 256;
+    auto give_up = [&]() { *abort_flag = 1; };
+    grid_dep_wait();
+    grid_dep_launch();
+
+    if (warp == 0) {
+        const bool elected = elect_one();
+        const int last_nt = (p.N + 127) / 128 - 1;
+        const uint32_t xfull_cl0 = mapa_shared(xfull0, 0);
+        int codes = 0;
+        uint32_t stages = 0;  // of tokens, asked for
+        int cr = 0, ci = 0;  // the item and stage whose codes are next
+        Item ctile, x;
+        bool more = item(0, ctile), ok = true;
+        auto load_codes = [&]() {
+            if (!more) return;
+            const int stage = codes % CS;
+            if (!warp_wait(cempty0 + 8 * stage, ((codes / CS) & 1) ^ 1, tmo, abort_flag)) {
+                give_up();
+                ok = false;
+                return;
+            }
+            // features past the last block of 128 are that one's again: they are not stored
+            if (elected)
+                S::copy(p, min(2 * ctile.nt + (int)rank, last_nt), ci, steps, codes0 + stage * C::CODE_BYTES, cfull0 + 8 * stage);
+            __syncwarp();
+            ++codes;
+            if (++ci == steps) {
+                ci = 0;
+                more = item(++cr, ctile);
+            }
+        };
+        for (int i = 0; ok && i < C::AHEAD; ++i) load_codes();
+        for (int r = 0; ok && item(r, x); ++r) {
+            const CUtensorMap* map = x.cut ? &tmCut : &tmX;
+            const uint32_t bytes = x.cut ? C::X_BYTES >> s.cut : C::X_BYTES;
+            for (int i = 0; ok && i < steps; ++i) {
+                load_codes();
+                const uint32_t buf = stages % BUFS;
+                if (!ok || !warp_wait(used0 + 8 * buf, ((stages / BUFS) & 1) ^ 1, tmo, abort_flag)) {
+                    give_up();
+                    ok = false;
+                    break;
+                }
+                if (elected) {
+                    const uint32_t st = smem0 + buf * C::X_BYTES, full = xfull_cl0 + 8 * buf;
+                    const int t = x.t0 + (int)rank * x.cols / 2;
+                    if (leader)
+                        mbar_arrive_expect_tx(xfull0 + 8 * buf, bytes);
+                    else
+                        mbar_arrive_expect_tx_cluster(full, bytes);
+                    tma_load_2d_cg2(st, map, full, 128 * i, t);
+                    tma_load_2d_cg2(st + C::X_BYTES / 2, map, full, 128 * i + 64, t);
+                }
+                __syncwarp();
+                ++stages;
+            }
+        }
+        // Every copy that either CTA asked for lands before the pair may exit. The follower reports its stages to the
+        // leader; for a stage that only one CTA asked for (one of them gave up), the leader supplies the missing
+        // arrival. Either is at most BUFS stages ahead of the other: a slot is used again only after both halves of
+        // its last stage were multiplied.
+        if (elected) {
+            if (!leader) {
+                st_cluster_u32(mapa_shared(smem_u32((const void*)peer_issued), 0), stages);
+                mbar_arrive_release_cluster(mapa_shared(teardown_bar, 0));
+            } else {
+                uint32_t other = stages;
+                if (mbar_wait_cl(teardown_bar, 0, DRAIN_TIMEOUT_NS, never)) other = *peer_issued;
+                const uint32_t lo = min(stages, other), hi = max(stages, other);
+                for (uint32_t n = lo; n < hi; ++n) mbar_arrive(xfull0 + 8 * (n % BUFS));
+                for (uint32_t b = 0; b < (uint32_t)BUFS && b < hi; ++b)
+                    mbar_wait(xfull0 + 8 * b, ((hi - 1 - b) / BUFS) & 1, DRAIN_TIMEOUT_NS, never);
+            }
+            for (int b = 0; b < CS && b < codes; ++b)
+                mbar_wait(cfull0 + 8 * b, ((codes - 1 - b) / CS) & 1, DRAIN_TIMEOUT_NS, never);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (leader) {
+            const bool elected = elect_one();
+            int at = 0;
+            bool ok = true;
+            Item x;
+            for (int r = 0; ok && item(r, x); ++r) {
+                if (r > 0 && !warp_wait(free_bar, (r - 1) & 1, tmo, abort_flag)) {  // the accumulators
+                    give_up();
+                    break;
+                }
+                const uint32_t idesc = idesc_m(idesc_bf16(x.cols), 2 * BM);
+                for (int i = 0; i < steps; ++i, ++at) {
+                    const int buf = at % BUFS;
+                    if (!soon_wait(xfull0 + 8 * buf, (at / BUFS) & 1, tmo, abort_flag) ||
+                        !soon_wait(made0 + 8 * buf, (at / BUFS) & 1, tmo, abort_flag)) {
+                        give_up();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (elected) {
+                        const uint32_t b = (smem0 + buf * C::X_BYTES) / 16, w = weights0 + 64 * buf;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            mma2_bf16_ta(tmem_base, w + 8 * j, row_desc(b + j / 4 * (C::X_BYTES / 32) + 2 * (j % 4)), idesc,
+                                         i > 0 || j > 0);
+                        tc_commit2_mc(used0 + 8 * buf, 0x3);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (elected) tc_commit2_mc(done_bar, 0x3);
+                __syncwarp();
+            }
+            // every MMA issued completes before either CTA frees its tensor memory
+            if (elected) tc_commit2_mc(drain_bar, 0x1);
+            __syncwarp();
+            mbar_wait(drain_bar, 0, DRAIN_TIMEOUT_NS, never);
+        }
+    } else {
+        // A quarter of the tensor memory's lanes, two tiles of 16 features, one of the stage's units, of every other
+        // stage (with all sixteen warps on each stage it took 1.2 times as long, most of it latency); 64 tokens.
+        const int quarter = warp % 4, half = (warp - 2) / 4 % 2, turn = (warp - 2) / 8, cg = (warp - 2) / 4;
+        const uint32_t mine = weights0 + 32 * half + ((uint32_t)(32 * quarter) << 16);
+        const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) + 64 * cg;
+        const uint32_t made_cl0 = mapa_shared(made0, 0), free_cl = mapa_shared(free_bar, 0);
+        auto tell = [&](uint32_t bar, uint32_t bar_cl) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader)
+                    mbar_arrive(bar);
+                else
+                    mbar_arrive_cluster(bar_cl);
+            }
+        };
+        auto store = [&](int r, const Item& x) -> bool {
+            if (!warp_wait(done_bar, r & 1, tmo, abort_flag)) return false;
+            tc_fence_after();
+            // into registers, then the accumulators are handed back, and only then stored
+            __nv_bfloat162 y[32];
+            const bool any = 64 * cg < x.tokens;
+            if (any) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v[32];
+                    tmem_ld32(tacc + 32 * c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) y[16 * c + j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                }
+            }
+            tell(free_bar, free_cl);
+            const int n = x.nt * 256 + (int)rank * 128 + quarter * 32 + lane, left = x.tokens - 64 * cg;
+            if (any && n < p.N) {
+                __nv_bfloat16* o = p.out + (int64_t)(x.t0 + 64 * cg) * p.ldo + n;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    if (2 * j < left) *o = y[j].x;
+                    o += p.ldo;
+                    if (2 * j + 1 < left) *o = y[j].y;
+                    o += p.ldo;
+                }
+            }
+            return true;
+        };
+        const int behind = min(steps, BUFS);  // the stages made before the tile before is stored
+        int at = 0;
+        bool ok = true;
+        Item now, before{};
+        bool more = item(0, now);
+        for (int r = 0; ok && (more || r > 0); ++r) {
+            for (int i = more ? 0 : behind; i <= steps; ++i) {
+                if (r > 0 && i == behind && !store(r - 1, before)) {
+                    ok = false;
+                    break;
+                }
+                if (!more || i == steps) break;
+                const int stage = at % CS, buf = at % BUFS, n = at++;
+                if (n % 2 != turn) continue;
+                if (!soon_wait(cfull0 + 8 * stage, (n / CS) & 1, tmo, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                S own[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    own[j].load(smem + BUFS * C::X_BYTES + stage * C::CODE_BYTES, 2 * quarter + j, half, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(cempty0 + 8 * stage);
+                if (!soon_wait(used0 + 8 * buf, ((n / BUFS) & 1) ^ 1, tmo, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t w[16];
+                    own[j].weights(p, w);
+                    tmem_st_16x32(mine + 64 * buf + ((uint32_t)(16 * j) << 16), w);
+                }
+                tmem_st_wait();
+                tell(made0 + 8 * buf, made_cl0 + 8 * buf);
+            }
+            if (!more) break;
+            before = now;
+            more = item(r + 1, now);
+        }
+        if (!ok) give_up();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {  // after every warp's last wait
+        if (blockIdx.x == 0) p.status[0] = (int)gridDim.x;
+        p.status[1 + blockIdx.x] = *abort_flag != 0 ? MOE_ERR_TIMEOUT : MOE_OK;
+    }
+    cluster_sync();  // both CTAs are done with each other's barriers and the MMAs have drained
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc2(tmem_base, 512);
     }
 }
 
@@ -692,7 +1062,7 @@ static cudaError_t few_g(const Int4Args& p, int num_sms, cudaStream_t st) {
     // K over the CTAs of a cluster, as long as all CTAs fit and a warp has two blocks or more
     const int64_t ctas = ceil_div(p.N, 16 * RT) * ceil_div(p.M, 8 * MT);
     int s = 1;
-    while (2 * s <= few_max_splits(RT, MT) && ctas * 2 * s <= CTAS * num_sms && int4_blocks(p.K) >= 4 * s * WARPS) s *= 2;
+    while (s < few_max_splits(RT, MT) && ctas * (s + 1) <= CTAS * num_sms && int4_blocks(p.K) >= 2 * (s + 1) * WARPS) ++s;
     return p.group == 32   ? few_s<RT, MT, WARPS, CTAS, 4>(p, s, st)
            : p.group == 64 ? few_s<RT, MT, WARPS, CTAS, 2>(p, s, st)
                            : few_s<RT, MT, WARPS, CTAS, 1>(p, s, st);
@@ -700,14 +1070,14 @@ static cudaError_t few_g(const Int4Args& p, int num_sms, cudaStream_t st) {
 
 template <int BT, int SPAN, bool ZEROS, bool HALF>
 static cudaError_t many_t(const CUtensorMap& x, const Int4Args& p, int splits, int num_sms, cudaStream_t st) {
-    using C = ManyCfg<BT>;
+    using C = ManyCfg<BT, SPAN>;
     const auto kernel = int4_many_kernel<BT, SPAN, ZEROS, HALF>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t tiles = ceil_div(p.N, 128) * ceil_div(p.M, BT), most = (int64_t)C::CTAS * num_sms;
     LaunchAttrs at(true, splits);
     cudaLaunchConfig_t cfg = at.config(dim3((unsigned)splits, (unsigned)(splits > 1 || tiles < most ? tiles : most)),
-                                       dim3(MANY_THREADS), C::SMEM, st);
+                                       dim3(C::THREADS), C::SMEM, st);
     return cudaLaunchKernelEx(&cfg, kernel, x, p);
 }
 template <int BT, int SPAN>
@@ -720,29 +1090,52 @@ static cudaError_t many_g(const CUtensorMap& x, const Int4Args& p, int num_sms, 
     // K over the CTAs of a cluster, as long as all CTAs fit and each has four stages or more
     const int64_t tiles = ceil_div(p.N, 128) * ceil_div(p.M, BT);
     int s = 1;
-    while (BT < 256 && 2 * s <= MANY_MAX_SPLITS && tiles * 2 * s <= ManyCfg<BT>::CTAS * num_sms && int4_blocks(p.K) >= 8 * s) s *= 2;
+    while (s < MANY_MAX_SPLITS && tiles * (s + 1) <= ManyCfg<BT, 1>::CTAS * num_sms && int4_blocks(p.K) >= 4 * (s + 1)) ++s;
     return p.group == 32   ? many_s<BT, 4>(x, p, s, num_sms, st)
            : p.group == 64 ? many_s<BT, 2>(x, p, s, num_sms, st)
                            : many_s<BT, 1>(x, p, s, num_sms, st);
 }
 
-static int many_tokens(int M) { return M <= 32 ? 32 : M <= 64 ? 64 : M <= 512 ? 128 : 256; }
-bool int4_few(int M) { return M <= 16; }
-int int4_box(int M) { return many_tokens(M); }
+template <int SPAN, bool ZEROS, bool HALF>
+static cudaError_t pair_t(const Int4Maps& m, const Int4Args& p, const Pairs& s, cudaStream_t st) {
+    using C = PairCfg<SPAN>;
+    const auto kernel = int4_pair_kernel<SPAN, ZEROS, HALF>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    LaunchAttrs at(true, 2);
+    cudaLaunchConfig_t cfg = at.config(dim3((unsigned)(2 * s.pairs)), dim3(C::THREADS), C::SMEM, st);
+    return cudaLaunchKernelEx(&cfg, kernel, m.x, m.cut, p, s);
+}
+template <int SPAN>
+static cudaError_t pair_s(const Int4Maps& m, const Int4Args& p, const Pairs& s, cudaStream_t st) {
+    if (p.zeros) return p.half ? pair_t<SPAN, true, true>(m, p, s, st) : pair_t<SPAN, true, false>(m, p, s, st);
+    return p.half ? pair_t<SPAN, false, true>(m, p, s, st) : pair_t<SPAN, false, false>(m, p, s, st);
+}
 
-cudaError_t launch_int4(const CUtensorMap& x, const Int4Args& args, int num_sms, cudaStream_t st) {
+static int many_tokens(int M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+static bool in_pairs(int M) { return M > 512; }
+Int4Boxes int4_boxes(int M, int N, int num_sms) {
+    if (M <= 16) return {0, 0};
+    if (!in_pairs(M)) return {many_tokens(M), 0};
+    return {128, 128 >> pairs_of(M, N, num_sms).cut};
+}
+
+cudaError_t launch_int4(const Int4Maps& m, const Int4Args& args, int num_sms, cudaStream_t st) {
     Int4Args p = args;
     p.slots = int4_slots(p.K, p.group);
     p.by4 = 1u << 28;
     p.by8 = 1u << 24;
     p.by12 = 1u << 20;
     if (p.M <= 8) return few_g<2, 1, 8, 2>(p, num_sms, st);
-    if (int4_few(p.M)) return few_g<2, 2, 4, 3>(p, num_sms, st);
+    if (p.M <= 16) return few_g<2, 2, 4, 3>(p, num_sms, st);
+    if (in_pairs(p.M)) {
+        const Pairs s = pairs_of(p.M, p.N, num_sms);
+        return p.group == 32 ? pair_s<4>(m, p, s, st) : p.group == 64 ? pair_s<2>(m, p, s, st) : pair_s<1>(m, p, s, st);
+    }
     switch (many_tokens(p.M)) {
-        case 32: return many_g<32>(x, p, num_sms, st);
-        case 64: return many_g<64>(x, p, num_sms, st);
-        case 128: return many_g<128>(x, p, num_sms, st);
-        default: return many_g<256>(x, p, num_sms, st);
+        case 32: return many_g<32>(m.x, p, num_sms, st);
+        case 64: return many_g<64>(m.x, p, num_sms, st);
+        default: return many_g<128>(m.x, p, num_sms, st);
     }
 }
 
