@@ -177,8 +177,8 @@ struct Int4Layout {
     const uint16_t* src_scales;  // [N][groups]
     const uint8_t* src_zeros;    // [N][groups] or null
     uint32_t* codes;             // [tiles / 8][blocks][8][2][32 lanes][4]
-    uint32_t* scales;            // [tiles / 8][slots][64]
-    uint8_t* zeros;              // [tiles / 8][slots][64] or null
+    uint32_t* scales;            // [tiles / 8][blocks][64][128 / group]
+    uint8_t* zeros;              // [tiles / 8][blocks][64][128 / group] or null
     int N, K, group;
 };
 struct Int4Args {

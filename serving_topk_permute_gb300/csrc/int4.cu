@@ -47,16 +47,18 @@ __global__ void __launch_bounds__(256) int4_codes_kernel(const uint8_t* src, uin
     }
     dst[at] = w;
 }
-// Scales: for each 128 features and group, 64 words, 8 of each 16 features: the scales of the features i and i + 8.
-// Zero points alike: bytes of the two nibbles. One thread for each word. Features past N have the scale 0.
+// Scales: for each block of 128 features x 128 k, 64 entries, 8 of each 16 features, of a word for each of the block's
+// groups: the scales of the features i and i + 8. Zero points alike: bytes of the two nibbles. One thread for each word.
+// Features past N have the scale 0.
 __global__ void __launch_bounds__(256)
     int4_scales_kernel(const uint16_t* scales, const uint8_t* zeros, uint32_t* dst, uint8_t* dst_zeros, int N, int groups,
-                       int slots, int64_t words) {
+                       int span, int slots, int64_t words) {
     const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
     grid_dep_wait();
     if (at >= words) return;
-    const int i = (int)(at % 8), g = (int)(at / 64 % slots);
-    const int64_t n = 128 * (at / 64 / slots) + 16 * (at / 8 % 8) + i;
+    const int64_t entry = at / span, block = entry / 64, blocks = slots / span;
+    const int g = (int)(block % blocks) * span + (int)(at % span);
+    const int64_t n = 128 * (block / blocks) + 16 * (entry / 8 % 8) + entry % 8;
     auto scale = [&](int64_t row) { return row < N && g < groups ? (uint32_t)scales[row * groups + g] : 0u; };
     dst[at] = scale(n) | scale(n + 8) << 16;
     if (zeros) {
@@ -102,6 +104,25 @@ __device__ __forceinline__ void whole_numbers(const Int4Args& p, uint32_t w, uin
 __device__ __forceinline__ void zero_points(uint32_t byte, uint32_t& low, uint32_t& high) {
     low = 0x43004300u | (byte & 15u) * 0x00010001u;
     high = 0x43004300u | (byte >> 4 & 15u) * 0x00010001u;
+}
+// an entry of words, and of bytes
+template <int SPAN>
+__device__ __forceinline__ void entry_words(const uint32_t* from, uint32_t (&w)[SPAN]) {
+    if constexpr (SPAN == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(from);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (SPAN == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(from);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = *from;
+    }
+}
+template <int SPAN>
+__device__ __forceinline__ uint32_t entry_bytes(const uint8_t* from) {
+    if constexpr (SPAN == 4) return *reinterpret_cast<const uint32_t*>(from);
+    if constexpr (SPAN == 2) return *reinterpret_cast<const uint16_t*>(from);
+    return *from;
 }
 // the scales of two features from their word
 template <bool HALF>
@@ -153,7 +174,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) int4_few_kernel(const __grid
     for (int r = 0; r < RT; ++r) {
         const int tile = min(tile0 + r, last_tile);
         codes[r] = p.codes + (((int64_t)(tile / 8) * blocks + first) * 8 + tile % 8) * 64 + lane;
-        const int64_t at = ((int64_t)(tile / 8) * p.slots + SPAN * first) * 64 + tile % 8 * 8 + lane / 4;
+        const int64_t at = (((int64_t)(tile / 8) * blocks + first) * 64 + tile % 8 * 8 + lane / 4) * SPAN;
         scales[r] = p.scales + at;
         zeros[r] = p.zeros + at;
     }
@@ -175,7 +196,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) int4_few_kernel(const __grid
     struct Block {
         uint4 codes[RT][2];
         uint2 x[MT][8];
-        uint32_t scale[RT][SPAN], zero[RT][SPAN];
+        uint32_t scale[RT][SPAN], zero[RT];  // zero: a byte for each group
     };
     auto fetch = [&](Block& a, int steps) {  // the block that the addresses stand at, which has so many steps of 16 k
 #pragma unroll
@@ -197,11 +218,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) int4_few_kernel(const __grid
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-#pragma unroll
-            for (int g = 0; g < SPAN; ++g) {
-                a.scale[r][g] = scales[r][64 * g];
-                if (ZEROS) a.zero[r][g] = zeros[r][64 * g];
-            }
+            entry_words<SPAN>(scales[r], a.scale[r]);
+            if (ZEROS) a.zero[r] = entry_bytes<SPAN>(zeros[r]);
             scales[r] += 64 * SPAN * WARPS;
             if (ZEROS) zeros[r] += 64 * SPAN * WARPS;
         }
@@ -214,7 +232,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) int4_few_kernel(const __grid
 #pragma unroll
             for (int g = 0; g < SPAN; ++g) {
                 uint32_t low = 0x43084308u, high = low;  // 136: the zero point is 8
-                if (ZEROS) zero_points(h.zero[r][g], low, high);
+                if (ZEROS) zero_points(h.zero[r] >> (8 * g), low, high);
                 float part[MT][4];
 #pragma unroll
                 for (int s = 0; s < 8 / SPAN; ++s) {
@@ -371,15 +389,12 @@ struct Stage {
     }
     // a lane's part of a unit (half) of tile t of 16 features
     uint4 codes;
-    uint32_t scale[OWN], zero[OWN];
+    uint32_t scale[OWN], zero;
     __device__ __forceinline__ void load(const uint8_t* from, int t, int half, int lane) {
         codes = *reinterpret_cast<const uint4*>(from + t * 1024 + half * 512 + lane * 16);
-#pragma unroll
-        for (int g = 0; g < OWN; ++g) {
-            const int at = (SPAN == 1 ? 0 : OWN * half + g) * 64 + t * 8 + lane / 4;
-            scale[g] = *reinterpret_cast<const uint32_t*>(from + SCALES + 4 * at);
-            zero[g] = ZEROS ? from[ZERO_POINTS + at] : 0;
-        }
+        const int at = (t * 8 + lane / 4) * SPAN + (SPAN == 1 ? 0 : OWN * half);
+        entry_words<OWN>(reinterpret_cast<const uint32_t*>(from + SCALES) + at, scale);
+        zero = ZEROS ? entry_bytes<OWN>(from + ZERO_POINTS + at) : 0;
     }
     // its weights, as 16 lanes x 32 columns of tensor memory hold them
     __device__ __forceinline__ void weights(const Int4Args& p, uint32_t (&r)[16]) const {
@@ -387,7 +402,7 @@ struct Stage {
 #pragma unroll
         for (int g = 0; g < OWN; ++g) {
             uint32_t low = 0x43084308u, high = low;  // 136: the zero point is 8
-            if (ZEROS) zero_points(zero[g], low, high);
+            if (ZEROS) zero_points(zero >> (8 * g), low, high);
             const Scaled<HALF> scaled(scale[g]);
 #pragma unroll
             for (int s = 4 / OWN * g; s < 4 / OWN * (g + 1); ++s) {
@@ -1035,7 +1050,7 @@ cudaError_t launch_int4_layout(const Int4Layout& a, cudaStream_t st) {
     LaunchAttrs at2(true);
     cfg = at2.config(dim3((unsigned)ceil_div(swords, 256)), dim3(256), 0, st);
     return cudaLaunchKernelEx(&cfg, int4_scales_kernel, a.src_scales, a.src_zeros, a.scales, a.zeros, a.N,
-                              (int)ceil_div(a.K, a.group), slots, swords);
+                              (int)ceil_div(a.K, a.group), 128 / a.group, slots, swords);
 }
 
 cudaError_t launch_int4_rows(const void* x, int64_t ldx, void* dst, int M, int K, cudaStream_t st) {
@@ -1057,12 +1072,16 @@ static cudaError_t few_s(const Int4Args& p, int splits, cudaStream_t st) {
     if (p.zeros) return p.half ? few_t<RT, MT, WARPS, CTAS, SPAN, true, true>(p, splits, st) : few_t<RT, MT, WARPS, CTAS, SPAN, true, false>(p, splits, st);
     return p.half ? few_t<RT, MT, WARPS, CTAS, SPAN, false, true>(p, splits, st) : few_t<RT, MT, WARPS, CTAS, SPAN, false, false>(p, splits, st);
 }
-template <int RT, int MT, int WARPS, int CTAS>
-static cudaError_t few_g(const Int4Args& p, int num_sms, cudaStream_t st) {
-    // K over the CTAs of a cluster, as long as all CTAs fit and a warp has two blocks or more
+// K over the CTAs of a cluster, as long as all CTAs fit and a warp has two blocks or more
+static int few_splits(const Int4Args& p, int RT, int MT, int WARPS, int CTAS, int num_sms) {
     const int64_t ctas = ceil_div(p.N, 16 * RT) * ceil_div(p.M, 8 * MT);
     int s = 1;
     while (s < few_max_splits(RT, MT) && ctas * (s + 1) <= CTAS * num_sms && int4_blocks(p.K) >= 2 * (s + 1) * WARPS) ++s;
+    return s;
+}
+template <int RT, int MT, int WARPS, int CTAS>
+static cudaError_t few_g(const Int4Args& p, int num_sms, cudaStream_t st) {
+    const int s = few_splits(p, RT, MT, WARPS, CTAS, num_sms);
     return p.group == 32   ? few_s<RT, MT, WARPS, CTAS, 4>(p, s, st)
            : p.group == 64 ? few_s<RT, MT, WARPS, CTAS, 2>(p, s, st)
                            : few_s<RT, MT, WARPS, CTAS, 1>(p, s, st);
@@ -1113,10 +1132,12 @@ static cudaError_t pair_s(const Int4Maps& m, const Int4Args& p, const Pairs& s, 
 }
 
 static int many_tokens(int M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
-static bool in_pairs(int M) { return M > 512; }
+static bool in_pairs(int M, int N, int num_sms) {
+    return M >= 512 && 5 * ceil_div(M, 256) * ceil_div(N, 256) >= num_sms;
+}
 Int4Boxes int4_boxes(int M, int N, int num_sms) {
     if (M <= 16) return {0, 0};
-    if (!in_pairs(M)) return {many_tokens(M), 0};
+    if (!in_pairs(M, N, num_sms)) return {many_tokens(M), 0};
     return {128, 128 >> pairs_of(M, N, num_sms).cut};
 }
 
@@ -1126,9 +1147,20 @@ cudaError_t launch_int4(const Int4Maps& m, const Int4Args& args, int num_sms, cu
     p.by4 = 1u << 28;
     p.by8 = 1u << 24;
     p.by12 = 1u << 20;
-    if (p.M <= 8) return few_g<2, 1, 8, 2>(p, num_sms, st);
-    if (p.M <= 16) return few_g<2, 2, 4, 3>(p, num_sms, st);
-    if (in_pairs(p.M)) {
+    // Two CTAs of eight warps on an SM; the two blocks that a warp holds with zero points want more registers
+    // (1 x 7168 x 4096 in groups of 32: 8.7 us, 7.6 with three CTAs of four; without zero points 7.3 and 7.6).
+    if (p.M <= 8) return p.zeros ? few_g<2, 1, 4, 3>(p, num_sms, st) : few_g<2, 1, 8, 2>(p, num_sms, st);
+    if (p.M <= 16) {
+        // Two CTAs of six warps on an SM, or three of four where those leave fewer of the SMs' places empty
+        // (16 x 7168 x 4096 9.2 us, with two of six 10.8; 16 x 8192 x 8192 24.7 and 17.6).
+        auto filled = [&](int warps, int ctas) {
+            const int64_t all = ceil_div(p.N, 32) * few_splits(p, 2, 2, warps, ctas, num_sms), places = ctas * num_sms;
+            return 100 * all / (ceil_div(all, places) * places);
+        };
+        if (ceil_div(p.N, 32) > num_sms && 5 * filled(4, 3) > 6 * filled(6, 2)) return few_g<2, 2, 4, 3>(p, num_sms, st);
+        return few_g<2, 2, 6, 2>(p, num_sms, st);
+    }
+    if (in_pairs(p.M, p.N, num_sms)) {
         const Pairs s = pairs_of(p.M, p.N, num_sms);
         return p.group == 32 ? pair_s<4>(m, p, s, st) : p.group == 64 ? pair_s<2>(m, p, s, st) : pair_s<1>(m, p, s, st);
     }
