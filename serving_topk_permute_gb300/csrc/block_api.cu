@@ -5,6 +5,7 @@
 
 #include <mutex>
 #include <new>
+#include <utility>
 
 #include "block.h"
 #include "common.cuh"
@@ -121,6 +122,11 @@ int check_linear(const moe_linear_config_t* c) {
     if (c->in_features < 32 || c->in_features % 32 || c->in_features > MAX_ROW) return MOE_ERR_INVALID_ARG;
     if (c->max_tokens < 1 || c->max_tokens > (1 << 28)) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
+}
+
+// the same address at another row stride
+bool shifted(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows) {
+    return a && a == b && rows > 1 && lda != ldb;
 }
 
 int check_sandwich(const moe_sandwich_t* p, int rows, int hidden) {
@@ -368,6 +374,10 @@ int moe_sandwich_norm(int32_t rows, int32_t hidden, const moe_sandwich_t* p, con
         !aligned_to(stats, 4))
         return MOE_ERR_INVALID_ARG;
     if (sum_out && sum_out == out) return MOE_ERR_INVALID_ARG;
+    // rows written over rows that are read: row by row the same ones
+    if (shifted(sum_out, sum_stride, f, f_stride, rows) || shifted(sum_out, sum_stride, residual, residual_stride, rows) ||
+        shifted(out, out_stride, f, f_stride, rows) || shifted(out, out_stride, residual, residual_stride, rows))
+        return MOE_ERR_INVALID_ARG;
     SandwichArgs a{};
     NormArgs& n = a.n;
     n.x = (const __nv_bfloat16*)f;
@@ -430,6 +440,9 @@ int moe_sandwich_norm_backward(int32_t rows, int32_t hidden, const moe_sandwich_
         (d_sum && !rows_ok(d_sum, d_sum_stride, rows, hidden)) || (d_out && !rows_ok(d_out, d_out_stride, rows, hidden)) ||
         !rows_ok(d_f, d_f_stride, rows, hidden) || !rows_ok(d_residual, d_residual_stride, rows, hidden))
         return MOE_ERR_INVALID_ARG;
+    for (const auto& g : {std::pair<const void*, int64_t>{d_f, d_f_stride}, {d_residual, d_residual_stride}})
+        if (shifted(g.first, g.second, d_sum, d_sum_stride, rows) || shifted(g.first, g.second, d_out, d_out_stride, rows))
+            return MOE_ERR_INVALID_ARG;
     if (d_gamma_post || d_gamma_pre || (d_gate && p->gate_kind == MOE_GATE_CHANNEL)) {
         size_t need = 0;
         moe_sandwich_norm_workspace_size(rows, hidden, &need);

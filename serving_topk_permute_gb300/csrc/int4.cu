@@ -2,19 +2,31 @@
 // point, for each group of K (moe_int4_forward):
 //   out[t, n] = bf16(sum_k x[t, k] (q[n, k] - z[n, k / g]) s[n, k / g]),  z = 8 without zero points
 //
-// Weights are laid out once in blocks of 16 features x 128 k, two units of 64 k and 512 bytes each: lane i of a
-// warp owns 16 bytes of a unit, in 4 words its 16 k steps; word s holds, for the features i / 4 and i / 4 + 8, the
-// four k from 16 s + 4 (i % 4) on.
-// That is what lane i feeds to the tensor cores for its rows, from registers (mma.sync) as well as through
-// tensor memory (16 lanes x 256 bits), so one layout serves every batch size. Inside a word the nibbles lie so
-// that (w >> 4 i) & 0x000F000F is a pair of neighbouring k.
+// Weights are laid out once in blocks of 128 features x 128 k, eight times 16 features x two units of 64 k and 512
+// bytes: lane i of a warp owns 16 bytes of a unit, in 4 words its 16 k steps; word s holds, for the features i / 4
+// and i / 4 + 8, the four k from 16 s + 4 (i % 4) on. That is what lane i feeds to the tensor cores for its rows, from
+// registers (mma.sync) as well as through tensor memory (16 lanes x 256 bits), so one layout serves every batch size, and
+// a block is one copy. Inside a word the nibbles lie so that (w >> 4 i) & 0x000F000F is a pair of neighbouring k.
 //
 // A code becomes a bf16 without a conversion: 0x4300 | q is 128 + q, and 128 + q - (128 + z) is exact.
 //
-// int4_few_kernel: up to 16 tokens a tile. The codes go from global memory straight into the registers of the
-// warps that multiply them; a CTA's warps share out K, and the CTAs of a cluster where there are few features.
-// Products of whole numbers times activations are summed for each group in fp32 and scaled there: the only
-// roundings are fp32's.
+// int4_few_kernel, up to 16 tokens: the codes go from global memory straight into the registers of the warps that
+// multiply them; a CTA's warps share out K, and the CTAs of a cluster where there are few features. Products of whole
+// numbers times activations are summed for each group in fp32 and scaled there: the only roundings are fp32's.
+// 1 x 4096 x 7168 in groups of 128: 7.2 us, 2.1 TB/s; 8 x 4096 x 7168 7.7; 16 x 7168 x 4096 9.2, in groups of 32 with zero
+// points 10.6. What bounds it is latency: a warp has two blocks in flight, and more would not fit its registers (codes
+// through a ring in shared memory: 10.9 us for the first one).
+//
+// int4_many_kernel, more tokens: tcgen05, the weights made bf16 in tensor memory, K split over clusters. 77 x 2999 x 2080
+// 8.5 us, 128 x 4096 x 7168 17.2 (4 of them the sums of a split tile through distributed shared memory).
+//
+// int4_pair_kernel, 512 tokens or more and tiles of 256 x 256 for a fifth of the SMs: CTA pairs. 2048 x 8192 x 4096
+// 82 us, 1.68 PFLOP/s, 88% of the measured bf16 rate; 4096 x 8192 x 4096 149. At 512 x 8192 x 8192 43 us against 62 of
+// int4_many_kernel, at 1024 x 2048 x 2048 13.7 and 15.5; below the rule's sizes it is the slower one: 700 x 2048 x 4096
+// 21.7 against 20.3, 256 x 8192 x 8192 40 against 38. What made it fast: scales that come with the codes, a ring or more
+// ahead (loaded by the warps that use them, one stage ahead, a stage took a trip to memory); one wait and one commit a
+// stage for the tokens and the weights (each wait of the issuing warp costs it 200 to 300 cycles; two pieces of 64 k and
+// barriers of their own: 100 us); and sixteen warps that take turns, so that half of them wait while the others compute.
 #include <cuda_fp16.h>
 
 #include "block.h"
@@ -310,6 +322,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) int4_few_kernel(const __grid
 }
 
 // ------------------------------------------------------------------ more tokens
+// The weights are rounded to bf16: the tensor cores take 16-bit operands, and sums of a group's own, scaled in fp32 as
+// above, would take the accumulators out of tensor memory once a group.
 // bf16 pairs q s of whole numbers: the nearest ones. An fp16 scale is two bf16, the second the exact rest of the
 // first, its product with q exact: one FMA rounds their sum.
 template <bool HALF>
@@ -737,8 +751,7 @@ __device__ __forceinline__ void mma2_bf16_ta(uint32_t d, uint32_t a, uint64_t b,
 }
 
 // Persistent CTA pairs: 256 features x 256 tokens, 128 features and half of the tokens' rows a CTA, so that a token
-// is read once for 256 features: with CTAs of their own, x came from L2 at 43 bytes a cycle and SM, and
-// that bounded the kernel (2048 x 8192 x 4096: 105 us, 91 with no x loaded).
+// is read once for 256 features: with CTAs of their own, x came from L2 at 43 bytes a cycle and SM.
 // The weights are made as above, by sixteen warps; those of a tile's first stages before the tile before is stored.
 template <int SPAN, bool ZEROS, bool HALF>
 __global__ void __launch_bounds__(PairCfg<SPAN>::THREADS, 1)
@@ -764,7 +777,7 @@ __global__ void __launch_bounds__(PairCfg<SPAN>::THREADS, 1)
                    teardown_bar = done_bar + 24;
     const uint32_t smem0 = smem_u32(smem), codes0 = smem0 + BUFS * C::X_BYTES;
     const uint64_t tmo = p.timeout_ns;
-    const int steps = int4_blocks(p.K), n_tiles = (p.N + 255) / 256, tiles = n_tiles * ((p.M + 255) / 256);
+    const int steps = int4_blocks(p.K), n_tiles = (p.N + 255) / 256, tiles = n_tiles * ((p.M - 1) / 256 + 1);
     const int pair = blockIdx.x / 2, rounds = s.whole / s.pairs;
 
     // item r of this pair; false after the last one
