@@ -190,7 +190,6 @@ struct Int4Args {
     int half;                    // scales are fp16 (else bf16)
     int group, M, N, K;
     int slots;                   // set by launch_int4
-    uint32_t by4, by8, by12;     // 2^(32 - 4) and so on, set by launch_int4
     __nv_bfloat16* out;
     int64_t ldo;
     int* status;                 // number of CTAs that report, then a word of each

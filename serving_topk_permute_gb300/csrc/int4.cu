@@ -13,15 +13,15 @@
 // int4_few_kernel, up to 16 tokens: the codes go from global memory straight into the registers of the warps that
 // multiply them; a CTA's warps share out K, and the CTAs of a cluster where there are few features. Products of whole
 // numbers times activations are summed for each group in fp32 and scaled there: the only roundings are fp32's.
-// 1 x 4096 x 7168 in groups of 128: 7.2 us, 2.1 TB/s; 8 x 4096 x 7168 7.7; 16 x 7168 x 4096 9.2, in groups of 32 with zero
-// points 10.6. What bounds it is latency: a warp has two blocks in flight, and more would not fit its registers (codes
+// 1 x 4096 x 7168 in groups of 128: 6.7 us, 2.3 TB/s; 8 x 4096 x 7168 7.6; 16 x 7168 x 4096 8.4, in groups of 32 with zero
+// points 9.8. What bounds it is latency: a warp has two blocks in flight, and more would not fit its registers (codes
 // through a ring in shared memory: 10.9 us for the first one).
 //
 // int4_many_kernel, more tokens: tcgen05, the weights made bf16 in tensor memory, K split over clusters. 77 x 2999 x 2080
-// 8.5 us, 128 x 4096 x 7168 17.2 (4 of them the sums of a split tile through distributed shared memory).
+// 8.3 us, 128 x 4096 x 7168 17.1 (4 of them the sums of a split tile through distributed shared memory).
 //
 // int4_pair_kernel, 512 tokens or more and tiles of 256 x 256 for a fifth of the SMs: CTA pairs. 2048 x 8192 x 4096
-// 82 us, 1.68 PFLOP/s, 88% of the measured bf16 rate; 4096 x 8192 x 4096 149. At 512 x 8192 x 8192 43 us against 62 of
+// 80 us, 1.71 PFLOP/s, 90% of the measured bf16 rate; 4096 x 8192 x 4096 146. At 512 x 8192 x 8192 43 us against 62 of
 // int4_many_kernel, at 1024 x 2048 x 2048 13.7 and 15.5; below the rule's sizes it is the slower one: 700 x 2048 x 4096
 // 21.7 against 20.3, 256 x 8192 x 8192 40 against 38. What made it fast: scales that come with the codes, a ring or more
 // ahead (loaded by the warps that use them, one stage ahead, a stage took a trip to memory); one wait and one commit a
@@ -98,17 +98,12 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
     const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
+// Plain shifts: as upper halves of products, which spares the pipe of half the rate that shifts share with masks, they
+// took longer (1 x 4096 x 7168 7.1 us against 6.7, 2048 x 8192 x 4096 in groups of 32 97 against 87).
 // A word's fragment: (k, k + 1) of the features i and i + 8, then (k + 2, k + 3), as whole numbers q - z.
-// low, high: 128 + z of the two features, twice each. The shifts are the upper halves of products with 2^28 and so
-// on, which p brings along so that they stay products: shifts and masks share a pipe of half the rate, which
-// would bound the kernel.
-__device__ __forceinline__ uint32_t upper(uint32_t w, uint32_t by) {
-    unsigned long long r;
-    asm("mul.wide.u32 %0, %1, %2;" : "=l"(r) : "r"(w), "r"(by));
-    return (uint32_t)(r >> 32);
-}
-__device__ __forceinline__ void whole_numbers(const Int4Args& p, uint32_t w, uint32_t low, uint32_t high, uint32_t (&a)[4]) {
-    const uint32_t v[4] = {w, upper(w, p.by4), upper(w, p.by8), upper(w, p.by12)};
+// low, high: 128 + z of the two features, twice each.
+__device__ __forceinline__ void whole_numbers(uint32_t w, uint32_t low, uint32_t high, uint32_t (&a)[4]) {
+    const uint32_t v[4] = {w, w >> 4, w >> 8, w >> 12};
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = sub_bf16x2((v[i] & 0x000F000Fu) | 0x43004300u, i & 1 ? high : low);
 }
@@ -249,7 +244,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) int4_few_kernel(const __grid
 #pragma unroll
                 for (int s = 0; s < 8 / SPAN; ++s) {
                     uint32_t a[4];
-                    whole_numbers(p, w[8 / SPAN * g + s], low, high, a);
+                    whole_numbers(w[8 / SPAN * g + s], low, high, a);
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
                         if (s == 0)
@@ -411,7 +406,7 @@ struct Stage {
         zero = ZEROS ? entry_bytes<OWN>(from + ZERO_POINTS + at) : 0;
     }
     // its weights, as 16 lanes x 32 columns of tensor memory hold them
-    __device__ __forceinline__ void weights(const Int4Args& p, uint32_t (&r)[16]) const {
+    __device__ __forceinline__ void weights(uint32_t (&r)[16]) const {
         const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
         for (int g = 0; g < OWN; ++g) {
@@ -421,7 +416,7 @@ struct Stage {
 #pragma unroll
             for (int s = 4 / OWN * g; s < 4 / OWN * (g + 1); ++s) {
                 uint32_t a[4];
-                whole_numbers(p, w[s], low, high, a);
+                whole_numbers(w[s], low, high, a);
                 r[4 * s] = scaled.times(a[0], 0);
                 r[4 * s + 1] = scaled.times(a[2], 0);
                 r[4 * s + 2] = scaled.times(a[1], 1);
@@ -616,7 +611,7 @@ __global__ void __launch_bounds__((ManyCfg<BT, SPAN>::THREADS), (ManyCfg<BT, SPA
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     uint32_t r[16];
-                    own[j].weights(p, r);
+                    own[j].weights(r);
                     tmem_st_16x32(weights0 + 64 * buf + 32 * half + ((uint32_t)(32 * quarter + 16 * j) << 16), r);
                 }
                 tmem_st_wait();
@@ -1027,7 +1022,7 @@ __global__ void __launch_bounds__(PairCfg<SPAN>::THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     uint32_t w[16];
-                    own[j].weights(p, w);
+                    own[j].weights(w);
                     tmem_st_16x32(mine + 64 * buf + ((uint32_t)(16 * j) << 16), w);
                 }
                 tmem_st_wait();
@@ -1157,15 +1152,12 @@ Int4Boxes int4_boxes(int M, int N, int num_sms) {
 cudaError_t launch_int4(const Int4Maps& m, const Int4Args& args, int num_sms, cudaStream_t st) {
     Int4Args p = args;
     p.slots = int4_slots(p.K, p.group);
-    p.by4 = 1u << 28;
-    p.by8 = 1u << 24;
-    p.by12 = 1u << 20;
     // Two CTAs of eight warps on an SM; the two blocks that a warp holds with zero points want more registers
-    // (1 x 7168 x 4096 in groups of 32: 8.7 us, 7.6 with three CTAs of four; without zero points 7.3 and 7.6).
+    // (1 x 7168 x 4096 in groups of 32: 8.3 us, 7.6 with three CTAs of four; without zero points 7.3 and 7.6).
     if (p.M <= 8) return p.zeros ? few_g<2, 1, 4, 3>(p, num_sms, st) : few_g<2, 1, 8, 2>(p, num_sms, st);
     if (p.M <= 16) {
         // Two CTAs of six warps on an SM, or three of four where those leave fewer of the SMs' places empty
-        // (16 x 7168 x 4096 9.2 us, with two of six 10.8; 16 x 8192 x 8192 24.7 and 17.6).
+        // (16 x 14336 x 4096 14.3 us, with two of six 17.3; 16 x 8192 x 8192 24.7 and 15.6).
         auto filled = [&](int warps, int ctas) {
             const int64_t all = ceil_div(p.N, 32) * few_splits(p, 2, 2, warps, ctas, num_sms), places = ctas * num_sms;
             return 100 * all / (ceil_div(all, places) * places);
